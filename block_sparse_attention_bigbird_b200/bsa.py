@@ -27,6 +27,21 @@ BSA_ERR_STATIC_WORKSPACE = -8
 STATIC_WORKSPACE_BYTES = 32 * 1024 * 1024  # BSA_STATIC_WORKSPACE_BYTES in include/bsa.h
 SPLIT_THRESHOLD = 48  # BSA_SPLIT_THRESHOLD in include/bsa.h: longer tile unions are split
 
+# bsa_type in include/bsa.h
+BF16, FP16, FP32, E4M3, E5M2, INT32, INT64 = range(7)
+NORMS = {None: 0, "rms": 1, "layer": 2}  # BSA_NORM_*
+NORM_COLUMNS_MOST = 8192
+
+
+class BlockNormArgs(ctypes.Structure):
+    """bsa_block_norm_args in include/bsa.h."""
+    _fields_ = [("B", ctypes.c_int), ("rows_per_batch", ctypes.c_int), ("C", ctypes.c_int), ("type", ctypes.c_int),
+                ("param_type", ctypes.c_int), ("post", ctypes.c_int), ("pre", ctypes.c_int),
+                ("post_weight", ctypes.c_void_p), ("post_bias", ctypes.c_void_p), ("gate", ctypes.c_void_p),
+                ("pre_weight", ctypes.c_void_p), ("pre_bias", ctypes.c_void_p), ("gate_rows", ctypes.c_int),
+                ("branch_scale", ctypes.c_float), ("stream_scale", ctypes.c_float), ("eps", ctypes.c_float)]
+
+
 # name -> (restype, argtypes); mirrors include/bsa.h
 _SIGNATURES = {
     "bsa_layout_build": (ctypes.c_int, [ctypes.c_int, ctypes.c_int, ctypes.c_int, ctypes.c_int,
@@ -79,6 +94,35 @@ _SIGNATURES = {
     "bsa_out_projection": (ctypes.c_int, [ctypes.c_void_p, ctypes.c_void_p, ctypes.c_void_p, ctypes.c_int,
                                           ctypes.c_int, ctypes.c_int, ctypes.c_int, ctypes.c_void_p,
                                           ctypes.c_void_p]),
+    "bsa_rope_build": (ctypes.c_int, [ctypes.POINTER(ctypes.c_int32), ctypes.c_int, ctypes.c_double, ctypes.c_int,
+                                      ctypes.c_int, ctypes.c_int, ctypes.POINTER(ctypes.c_void_p)]),
+    "bsa_rope_from_table": (ctypes.c_int, [ctypes.POINTER(ctypes.c_int32), ctypes.POINTER(ctypes.c_double),
+                                           ctypes.c_int, ctypes.c_int, ctypes.POINTER(ctypes.c_void_p)]),
+    "bsa_rope_table": (ctypes.c_int, [ctypes.c_void_p, ctypes.POINTER(ctypes.c_void_p),
+                                      ctypes.POINTER(ctypes.c_void_p), ctypes.POINTER(ctypes.c_int),
+                                      ctypes.POINTER(ctypes.c_int), ctypes.POINTER(ctypes.c_int)]),
+    "bsa_rope_free": (None, [ctypes.c_void_p]),
+    "bsa_rope_apply": (ctypes.c_int, [ctypes.c_void_p, ctypes.c_void_p, ctypes.c_int, ctypes.c_void_p,
+                                      ctypes.c_void_p, ctypes.c_int, ctypes.c_int, ctypes.c_int, ctypes.c_int,
+                                      ctypes.c_int, ctypes.POINTER(ctypes.c_int64), ctypes.c_void_p, ctypes.c_int,
+                                      ctypes.POINTER(ctypes.c_int64), ctypes.c_void_p, ctypes.c_int,
+                                      ctypes.c_void_p]),
+    "bsa_block_norm": (ctypes.c_int, [ctypes.POINTER(BlockNormArgs), ctypes.c_void_p, ctypes.c_void_p,
+                                      ctypes.c_void_p, ctypes.c_void_p, ctypes.c_void_p, ctypes.c_void_p]),
+    "bsa_block_norm_backward_workspace_bytes": (ctypes.c_int, [ctypes.POINTER(BlockNormArgs),
+                                                               ctypes.POINTER(ctypes.c_size_t)]),
+    "bsa_block_norm_backward": (ctypes.c_int, [ctypes.POINTER(BlockNormArgs)] + [ctypes.c_void_p] * 13 +
+                                [ctypes.c_size_t, ctypes.c_void_p]),
+    "bsa_fp8_quantize": (ctypes.c_int, [ctypes.c_void_p, ctypes.c_int, ctypes.c_int, ctypes.c_int, ctypes.c_int,
+                                        ctypes.c_int, ctypes.c_void_p, ctypes.c_int64, ctypes.c_void_p,
+                                        ctypes.c_void_p, ctypes.c_int64, ctypes.c_void_p, ctypes.c_void_p]),
+    "bsa_fp8_matmul_workspace_bytes": (ctypes.c_int, [ctypes.c_int, ctypes.c_int, ctypes.c_int,
+                                                      ctypes.POINTER(ctypes.c_size_t)]),
+    "bsa_fp8_matmul": (ctypes.c_int, [ctypes.c_void_p, ctypes.c_int, ctypes.c_int64, ctypes.c_void_p, ctypes.c_int,
+                                      ctypes.c_void_p, ctypes.c_int, ctypes.c_int64, ctypes.c_void_p, ctypes.c_int,
+                                      ctypes.c_void_p, ctypes.c_int, ctypes.c_int, ctypes.c_int, ctypes.c_int,
+                                      ctypes.c_void_p, ctypes.c_int, ctypes.c_void_p, ctypes.c_size_t,
+                                      ctypes.c_void_p]),
     "bsa_sync_status": (ctypes.c_int, [ctypes.c_void_p]),
     "bsa_strerror": (ctypes.c_char_p, [ctypes.c_int]),
     "bsa_debug_wait_timeout": (ctypes.c_int, [ctypes.c_uint64, ctypes.c_void_p]),
@@ -439,6 +483,372 @@ def bsa_out_projection(o, weight, bias=None, y=None, stream=None):
                                   B, H, L, N, y.data_ptr(), ctypes.c_void_p(_stream_ptr(stream)))
     _check(code, "bsa_out_projection")
     return y
+
+
+_type_codes = {}
+
+
+def _type_of(dtype) -> Optional[int]:
+    """bsa_type of a torch dtype, None for one the library has no name for."""
+    if not _type_codes:
+        import torch
+        _type_codes.update({torch.bfloat16: BF16, torch.float16: FP16, torch.float32: FP32,
+                            torch.float8_e4m3fn: E4M3, torch.float8_e5m2: E5M2, torch.int32: INT32,
+                            torch.int64: INT64})
+    return _type_codes.get(dtype)
+
+
+def _on(device, stream, call):
+    """call(stream pointer) with the tensors' device current, and ``stream``, where one is
+    given, the stream that call's allocations belong to."""
+    import torch
+    if stream is None and device.index == torch.cuda.current_device():
+        return call(torch.cuda.current_stream().cuda_stream)
+    with torch.cuda.device(device):
+        if stream is None:
+            return call(torch.cuda.current_stream().cuda_stream)
+        if isinstance(stream, int):
+            stream = torch.cuda.ExternalStream(stream, device=device)
+        with torch.cuda.stream(stream):
+            return call(stream.cuda_stream)
+
+
+def _check_same(device, **tensors):
+    for name, t in tensors.items():
+        if t is not None and t.device != device:
+            raise ValueError(f"{name} is on {t.device}, not on {device}")
+
+
+def _ptr(t):
+    return None if t is None else t.data_ptr()
+
+
+# ---------------------------------------------------------------- rotary positions
+class Rope:
+    """Owner of a bsa_rope*; freed with the object."""
+
+    def __init__(self, handle: int):
+        self._h = ctypes.c_void_p(handle)
+        n, a, adj = ctypes.c_int(), ctypes.c_int(), ctypes.c_int()
+        lib.bsa_rope_table(self._h, None, None, ctypes.byref(n), ctypes.byref(a), ctypes.byref(adj))
+        self.n_pairs, self.n_axes, self.adjacent = n.value, a.value, bool(adj.value)
+
+    @property
+    def handle(self) -> ctypes.c_void_p:
+        return self._h
+
+    def __del__(self):
+        h = getattr(self, "_h", None)
+        if h is not None and h.value and lib is not None:   # lib is None at interpreter exit
+            lib.bsa_rope_free(h)
+            self._h = ctypes.c_void_p(0)
+
+
+def bsa_rope_build(sections, base: float = 10000.0, per_axis: bool = False, interleave: bool = False,
+                   adjacent: bool = False) -> Rope:
+    """A rotary code whose axis a (time, height, ..) turns sections[a] pairs of a head.
+
+    Frequencies are base^(-j / n) over all n pairs, or with ``per_axis``
+    base^(-i / sections[a]) for the i-th pair of each axis; ``interleave`` deals the
+    pairs to the axes in turn; pair j holds columns j and n + j, or 2 j and 2 j + 1 with
+    ``adjacent``.
+    """
+    s = np.ascontiguousarray(np.asarray(sections, dtype=np.int32).reshape(-1))
+    out = ctypes.c_void_p()
+    _check(lib.bsa_rope_build(s.ctypes.data_as(ctypes.POINTER(ctypes.c_int32)), s.size, base, int(per_axis),
+                              int(interleave), int(adjacent), ctypes.byref(out)), "bsa_rope_build")
+    return Rope(out.value)
+
+
+def bsa_rope_from_table(axis, freq, adjacent: bool = False) -> Rope:
+    """A rotary code from the axis and the frequency (radians per position) of each pair."""
+    a = np.ascontiguousarray(np.asarray(axis, dtype=np.int32).reshape(-1))
+    f = np.ascontiguousarray(np.asarray(freq, dtype=np.float64).reshape(-1))
+    if a.size != f.size:
+        raise BsaError(BSA_ERR_INVALID_ARG, "bsa_rope_from_table: axis and freq differ in length")
+    out = ctypes.c_void_p()
+    _check(lib.bsa_rope_from_table(a.ctypes.data_as(ctypes.POINTER(ctypes.c_int32)),
+                                   f.ctypes.data_as(ctypes.POINTER(ctypes.c_double)), a.size, int(adjacent),
+                                   ctypes.byref(out)), "bsa_rope_from_table")
+    return Rope(out.value)
+
+
+def bsa_rope_table(rope: Rope):
+    """(axis int32 [n_pairs], freq float64 [n_pairs]) as numpy copies."""
+    a, f = ctypes.c_void_p(), ctypes.c_void_p()
+    _check(lib.bsa_rope_table(rope.handle, ctypes.byref(a), ctypes.byref(f), None, None, None), "bsa_rope_table")
+    n = (rope.n_pairs,)
+    return (np.ctypeslib.as_array(ctypes.cast(a, ctypes.POINTER(ctypes.c_int32)), n).copy(),
+            np.ctypeslib.as_array(ctypes.cast(f, ctypes.POINTER(ctypes.c_double)), n).copy())
+
+
+_Strides3 = ctypes.c_int64 * 3
+_Strides12 = ctypes.c_int64 * 12
+
+
+def bsa_rope_apply(q, k, positions, rope: Rope, inverse: bool = False, q_out=None, k_out=None, stream=None):
+    """q [B, H, L, d] and k [B, Hk, L, d] (or None) with their pairs turned by their positions.
+
+    bf16, fp16 or fp32 CUDA tensors of any strides with contiguous columns (views of a packed
+    projection too).  positions: int32, int64 or fp32 [axes, L], shared by the batch, or
+    [axes, B, L].  ``inverse`` turns back (the gradient).  Results are new contiguous tensors,
+    or q_out and k_out, which may be q and k themselves; other overlaps are not allowed.
+    """
+    import torch
+    B, H, L, d = q.shape if q.dim() == 4 else (0, 0, 0, 0)
+    ty, pt = _type_of(q.dtype), _type_of(positions.dtype)
+    if q.dim() != 4 or ty not in (BF16, FP16, FP32) or not q.is_cuda or (d > 1 and q.stride(3) != 1):
+        raise ValueError("q must be a bf16, fp16 or fp32 CUDA tensor [B, H, L, d] with contiguous columns")
+    if k is not None and (k.dim() != 4 or k.dtype != q.dtype or k.shape[0] != B or k.shape[2] != L or
+                          k.shape[3] != d or (d > 1 and k.stride(3) != 1)):
+        raise ValueError("k must be like q, [B, Hk, L, d]")
+    if pt not in (INT32, INT64, FP32) or positions.dim() not in (2, 3) or positions.shape[0] < rope.n_axes or \
+            positions.shape[-1] != L or (positions.dim() == 3 and positions.shape[1] != B):
+        raise ValueError(f"positions must be int32, int64 or fp32 [axes, L] or [axes, B, L] with at least "
+                         f"{rope.n_axes} axes")
+    _check_same(q.device, k=k, positions=positions, q_out=q_out, k_out=k_out)
+    for name, t, src in (("q_out", q_out, q), ("k_out", k_out, k)):
+        if t is not None and (src is None or t.dtype != q.dtype or t.shape != src.shape or
+                              (d > 1 and t.stride(3) != 1) or
+                              any(n > 1 and s == 0 for n, s in zip(t.shape, t.stride()))):
+            raise ValueError(f"{name} must have its input's type and shape, contiguous columns and no shared rows")
+
+    def call(ptr):
+        qo = torch.empty((B, H, L, d), dtype=q.dtype, device=q.device) if q_out is None else q_out
+        ko = k_out
+        if k is not None and k_out is None:
+            ko = torch.empty(k.shape, dtype=k.dtype, device=k.device)
+        ks = (0,) * 6 if k is None else (*k.stride()[:3], *ko.stride()[:3])
+        ps = positions.stride()
+        _check(lib.bsa_rope_apply(q.data_ptr(), qo.data_ptr(), H, _ptr(k), _ptr(ko), 0 if k is None else k.shape[1],
+                                  B, L, d, ty, _Strides12(*q.stride()[:3], *qo.stride()[:3], *ks),
+                                  positions.data_ptr(), pt,
+                                  _Strides3(ps[0], ps[1] if len(ps) == 3 else 0, ps[-1]), rope.handle, int(inverse),
+                                  ptr), "bsa_rope_apply")
+        return qo, ko
+    return _on(q.device, stream, call)
+
+
+# ---------------------------------------------------------------- norms and residual of a block
+def _norm_args(x, y, post, post_weight, post_bias, gate, branch_scale, stream_scale, pre, pre_weight, pre_bias, eps):
+    ty = _type_of(x.dtype)
+    if ty not in (BF16, FP16, FP32) or not x.is_cuda or not x.is_contiguous() or x.dim() < 1 or x.shape[-1] < 1:
+        raise ValueError("x must be a contiguous bf16, fp16 or fp32 CUDA tensor [.., C]")
+    C = x.shape[-1]
+    B = x.shape[0] if x.dim() > 1 else 1
+    if post not in NORMS or pre not in NORMS:
+        raise ValueError('post and pre must be "rms", "layer" or None')
+    if y is not None and (y.shape != x.shape or y.dtype != x.dtype or not y.is_contiguous()):
+        raise ValueError("y must be like x")
+    if y is None and (post is not None or gate is not None or pre is None or branch_scale != 1.0 or
+                      stream_scale != 1.0):
+        raise ValueError("without y there is the pre norm alone")
+    params = {"post_weight": post_weight, "post_bias": post_bias, "gate": gate, "pre_weight": pre_weight,
+              "pre_bias": pre_bias}
+    pt, gate_rows = None, 1
+    for name, t in params.items():
+        if t is None:
+            continue
+        if pt is None:
+            pt = _type_of(t.dtype)
+        if _type_of(t.dtype) != pt or pt not in (ty, FP32) or not t.is_contiguous():
+            raise ValueError("parameters and gate must be contiguous and all of x's type or all fp32")
+        if name == "gate" and t.dim() == 2 and t.shape[1] == C and t.shape[0] in (1, B):
+            gate_rows = t.shape[0]
+        elif tuple(t.shape) != (C,):
+            raise ValueError(f"{name} must be [C]" + (" or [B, C]" if name == "gate" else ""))
+    if (post is None and (post_weight is not None or post_bias is not None)) or \
+            (pre is None and (pre_weight is not None or pre_bias is not None)):
+        raise ValueError("a weight or bias needs its norm")
+    _check_same(x.device, y=y, **params)
+    rows = x.numel() // C
+    a = BlockNormArgs(B, rows // B if B else 0, C, ty, ty if pt is None else pt, NORMS[post], NORMS[pre],
+                      _ptr(post_weight), _ptr(post_bias), _ptr(gate), _ptr(pre_weight), _ptr(pre_bias), gate_rows,
+                      branch_scale, stream_scale, eps)
+    return a, rows
+
+
+def bsa_block_norm(x, y=None, post: Optional[str] = None, post_weight=None, post_bias=None, gate=None,
+                   branch_scale: float = 1.0, stream_scale: float = 1.0, pre: Optional[str] = "rms",
+                   pre_weight=None, pre_bias=None, eps: float = 1e-6, save_stats: bool = False, out=None,
+                   normed=None, stream=None):
+    """(stream, normed, stats) of the residual after a block and the norm before the next.
+
+        stream = stream_scale x + branch_scale gate (N_post(y) post_weight + post_bias)
+        normed = N_pre(stream) pre_weight + pre_bias
+
+    x, y: contiguous bf16, fp16 or fp32 CUDA tensors [.., C], C <= 8192.  post, pre: "rms",
+    "layer" or None for no norm (then normed is None).  gate: [C], or [B, C] with one row for
+    each index of x's first axis.  Parameters and gate are all of x's type or all fp32; None
+    stands for 1 (weights, gate) and 0 (biases).  Without y the stream is x itself and only
+    the pre norm is taken.  stats (with ``save_stats``): fp32 [rows, 4], for the backward.
+    out and normed may be given; they may be x or y.
+    """
+    import torch
+    a, rows = _norm_args(x, y, post, post_weight, post_bias, gate, branch_scale, stream_scale, pre, pre_weight,
+                         pre_bias, eps)
+    for name, t in (("out", out), ("normed", normed)):
+        if t is not None and (t.shape != x.shape or t.dtype != x.dtype or not t.is_contiguous() or
+                              t.device != x.device):
+            raise ValueError(f"{name} must be like x")
+    if (out is not None and y is None) or (normed is not None and pre is None):
+        raise ValueError("an output was given that the call does not have")
+
+    def call(ptr):
+        o = torch.empty_like(x) if y is not None and out is None else out
+        n = torch.empty_like(x) if pre is not None and normed is None else normed
+        st = torch.empty((rows, 4), dtype=torch.float32, device=x.device) if save_stats else None
+        _check(lib.bsa_block_norm(ctypes.byref(a), x.data_ptr(), _ptr(y), _ptr(o), _ptr(n), _ptr(st), ptr),
+               "bsa_block_norm")
+        return (x if y is None else o), n, st
+    return _on(x.device, stream, call)
+
+
+def bsa_block_norm_backward(dstream, dnormed, x, y, stats, post: Optional[str] = None, post_weight=None,
+                            post_bias=None, gate=None, branch_scale: float = 1.0, stream_scale: float = 1.0,
+                            pre: Optional[str] = "rms", pre_weight=None, pre_bias=None, params: bool = True,
+                            stream=None):
+    """Gradients of bsa_block_norm, as a dict with the keys x, y, post_weight, post_bias, gate,
+    pre_weight and pre_bias (None for what the call does not have).
+
+    dstream, dnormed: the loss's gradients by both results (None for zero).  x: the forward's
+    stream, its first result.  y, stats and the other arguments: the forward's.  ``params``
+    False leaves the parameters' and the gate's gradients out.
+    """
+    import torch
+    a, rows = _norm_args(x, y, post, post_weight, post_bias, gate, branch_scale, stream_scale, pre, pre_weight,
+                         pre_bias, 0.0)
+    for name, t in (("dstream", dstream), ("dnormed", dnormed)):
+        if t is not None and (t.shape != x.shape or t.dtype != x.dtype or not t.is_contiguous() or
+                              t.device != x.device):
+            raise ValueError(f"{name} must be like x")
+    if dnormed is not None and pre is None:
+        raise ValueError("dnormed without a pre norm")
+    if stats.dtype != torch.float32 or tuple(stats.shape) != (rows, 4) or not stats.is_contiguous() or \
+            stats.device != x.device:
+        raise ValueError("stats must be the forward's fp32 [rows, 4]")
+
+    def call(ptr):
+        g = {"x": torch.empty_like(x), "y": None if y is None else torch.empty_like(y)}
+        for name, t in (("post_weight", post_weight), ("post_bias", post_bias), ("gate", gate),
+                        ("pre_weight", pre_weight), ("pre_bias", pre_bias)):
+            g[name] = torch.empty_like(t) if params and t is not None else None
+        ws = None
+        if params:
+            n = ctypes.c_size_t()
+            _check(lib.bsa_block_norm_backward_workspace_bytes(ctypes.byref(a), ctypes.byref(n)),
+                   "bsa_block_norm_backward_workspace_bytes")
+            ws = torch.empty(max(n.value, 1), dtype=torch.uint8, device=x.device)
+        _check(lib.bsa_block_norm_backward(ctypes.byref(a), _ptr(dstream), _ptr(dnormed), x.data_ptr(), _ptr(y),
+                                           stats.data_ptr(), g["x"].data_ptr(), _ptr(g["y"]), _ptr(g["post_weight"]),
+                                           _ptr(g["post_bias"]), _ptr(g["gate"]), _ptr(g["pre_weight"]),
+                                           _ptr(g["pre_bias"]), _ptr(ws), 0 if ws is None else ws.numel(), ptr),
+               "bsa_block_norm_backward")
+        return g
+    return _on(x.device, stream, call)
+
+
+# ---------------------------------------------------------------- 8-bit floating point
+def bsa_fp8_quantize(x, square: bool = False, rows: bool = True, cols: bool = False, dtype=None, stream=None):
+    """8-bit codes of x [.., C] (R rows of C) with an fp32 scale for each block of 128.
+
+    Returns (codes [R, C], scale [R, C/128]) with ``rows``: a block is 128 columns of one row;
+    then (codes_t [C, R], scale_t [C, R/128]) with ``cols``: the same of x transposed.  With
+    ``square`` blocks are 128 x 128 and the scales [R/128, C/128] and its transpose (sizes
+    over 128 round up).  x: contiguous bf16, fp16 or fp32.  dtype: torch.float8_e4m3fn (the
+    default) or torch.float8_e5m2.  Rows of codes start at multiples of 16 bytes.
+    """
+    import torch
+    dtype = torch.float8_e4m3fn if dtype is None else dtype
+    ty, ct = _type_of(x.dtype), _type_of(dtype)
+    if ty not in (BF16, FP16, FP32) or not x.is_cuda or not x.is_contiguous() or x.dim() < 1 or x.shape[-1] < 1:
+        raise ValueError("x must be a contiguous bf16, fp16 or fp32 CUDA tensor [.., C]")
+    if ct not in (E4M3, E5M2):
+        raise ValueError("dtype must be torch.float8_e4m3fn or torch.float8_e5m2")
+    if not rows and not cols:
+        raise ValueError("ask for rows, cols or both")
+    C = x.shape[-1]
+    R = x.numel() // C
+
+    def form(n, m):  # codes [n, m] in padded rows, and their scales
+        ld = (m + 15) // 16 * 16
+        codes = torch.empty((n, ld), dtype=dtype, device=x.device)
+        scale = torch.empty(((n + 127) // 128 if square else n, (m + 127) // 128), dtype=torch.float32,
+                            device=x.device)
+        return (codes if ld == m else codes[:, :m]), scale
+
+    def call(ptr):
+        got = (form(R, C) if rows else (None, None)) + (form(C, R) if cols else (None, None))
+        ld = (0 if got[0] is None else (C + 15) // 16 * 16, 0 if got[2] is None else (R + 15) // 16 * 16)
+        _check(lib.bsa_fp8_quantize(x.data_ptr(), ty, R, C, int(square), ct, _ptr(got[0]), ld[0], _ptr(got[1]),
+                                    _ptr(got[2]), ld[1], _ptr(got[3]), ptr), "bsa_fp8_quantize")
+        return tuple(t for t in got if t is not None)
+    return _on(x.device, stream, call)
+
+
+def _scale_rows(name, scale, rows, kb):
+    """How many rows share a scale: 1 or 128."""
+    import torch
+    if scale.dtype != torch.float32 or scale.dim() != 2 or not scale.is_contiguous() or scale.shape[1] != kb:
+        raise ValueError(f"{name} must be contiguous fp32 with one column for each 128 of K")
+    if scale.shape[0] == rows:
+        return 1
+    if scale.shape[0] == (rows + 127) // 128:
+        return 128
+    raise ValueError(f"{name} must have a row for each row, or for each 128 rows, of its matrix")
+
+
+def bsa_fp8_matmul_workspace_bytes(M: int, N: int, K: int) -> int:
+    n = ctypes.c_size_t()
+    _check(lib.bsa_fp8_matmul_workspace_bytes(M, N, K, ctypes.byref(n)), "bsa_fp8_matmul_workspace_bytes")
+    return n.value
+
+
+def bsa_fp8_matmul(a, a_scale, b, b_scale, bias=None, out_dtype=None, out=None, workspace=None, stream=None):
+    """a b^T [M, N] of 8-bit a [M, K] and b [N, K] with their scales, plus bias [N].
+
+    a, b: torch.float8_e4m3fn or float8_e5m2, rows starting at multiples of 16 bytes (as
+    bsa_fp8_quantize lays them out).  Scales: fp32 [rows, K/128] or [rows/128, K/128] (sizes
+    over 128 round up).  bias: bf16 or fp32.  Result: bf16, or ``out_dtype`` fp32, or ``out``.
+    workspace: uint8, at least bsa_fp8_matmul_workspace_bytes(M, N, K) bytes; allocated when
+    omitted.
+    """
+    import torch
+    at, bt = _type_of(a.dtype), _type_of(b.dtype)
+    for name, t, ty in (("a", a, at), ("b", b, bt)):
+        if ty not in (E4M3, E5M2) or not t.is_cuda or t.dim() != 2 or t.shape[1] < 1 or \
+                (t.shape[1] > 1 and t.stride(1) != 1) or t.stride(0) % 16 or t.stride(0) < t.shape[1] or \
+                t.data_ptr() % 16:
+            raise ValueError(f"{name} must be an 8-bit CUDA matrix whose rows start at multiples of 16 bytes")
+    (M, K), N = a.shape, b.shape[0]
+    if b.shape[1] != K:
+        raise ValueError("a and b must have the same number of columns")
+    kb = (K + 127) // 128
+    ar, br = _scale_rows("a_scale", a_scale, M, kb), _scale_rows("b_scale", b_scale, N, kb)
+    if bias is not None and (_type_of(bias.dtype) not in (BF16, FP32) or tuple(bias.shape) != (N,) or
+                             not bias.is_contiguous()):
+        raise ValueError("bias must be a contiguous bf16 or fp32 vector [N]")
+    if out is not None:
+        if out_dtype not in (None, out.dtype) or tuple(out.shape) != (M, N) or not out.is_contiguous():
+            raise ValueError("out must be a contiguous tensor [M, N] of the result's type")
+        out_dtype = out.dtype
+    out_dtype = torch.bfloat16 if out_dtype is None else out_dtype
+    if _type_of(out_dtype) not in (BF16, FP32):
+        raise ValueError("the result is bf16 or fp32")
+    _check_same(a.device, b=b, a_scale=a_scale, b_scale=b_scale, bias=bias, out=out, workspace=workspace)
+
+    def call(ptr):
+        o = torch.empty((M, N), dtype=out_dtype, device=a.device) if out is None else out
+        ws = workspace
+        if ws is None and M > 32:
+            n = bsa_fp8_matmul_workspace_bytes(M, N, K)
+            ws = torch.empty(n, dtype=torch.uint8, device=a.device) if n else None
+        _check(lib.bsa_fp8_matmul(a.data_ptr(), at, a.stride(0), a_scale.data_ptr(), ar, b.data_ptr(), bt, b.stride(0),
+                                  b_scale.data_ptr(), br, _ptr(bias), BF16 if bias is None else _type_of(bias.dtype),
+                                  M, N, K, o.data_ptr(), _type_of(out_dtype), _ptr(ws),
+                                  0 if ws is None else ws.numel() * ws.element_size(), ptr), "bsa_fp8_matmul")
+        return o
+    return _on(a.device, stream, call)
 
 
 def bsa_sync_status(stream=None) -> int:

@@ -53,7 +53,7 @@ def build(force: bool = False, verbose: bool = False) -> str:
         return LIB_PATH
     tmp = LIB_PATH + ".tmp"
     cmd = [_nvcc(), *ARCH_FLAGS, "-O3", "-lineinfo", "-std=c++17", "-shared",
-           "-Xcompiler", "-fPIC,-O3", "-I", INCLUDE, "-o", tmp, *sources(), "-lcudart_static"]
+           "--threads", "0", "-Xcompiler", "-fPIC,-O3", "-I", INCLUDE, "-o", tmp, *sources(), "-lcudart_static"]
     if verbose:
         cmd.insert(1, "-Xptxas=-v")
     res = subprocess.run(cmd, capture_output=True, text=True)

@@ -1,0 +1,81 @@
+// Element access shared by the kernels around the attention (rotary positions, block
+// norms, the 8-bit quantiser): eight neighbouring elements by 16-byte accesses, or one.
+// Arithmetic is in fp32; storing rounds once, to nearest even.
+#pragma once
+
+#include <cuda_bf16.h>
+#include <cuda_fp16.h>
+
+#include <cstdint>
+
+#include "../../include/bsa.h"
+
+namespace bsa {
+
+__device__ __forceinline__ float to_f32(float v) { return v; }
+__device__ __forceinline__ float to_f32(__nv_bfloat16 v) { return __bfloat162float(v); }
+__device__ __forceinline__ float to_f32(__half v) { return __half2float(v); }
+template <typename T>
+__device__ __forceinline__ T from_f32(float v);
+template <>
+__device__ __forceinline__ float from_f32<float>(float v) { return v; }
+template <>
+__device__ __forceinline__ __nv_bfloat16 from_f32<__nv_bfloat16>(float v) { return __float2bfloat16_rn(v); }
+template <>
+__device__ __forceinline__ __half from_f32<__half>(float v) { return __float2half_rn(v); }
+
+__device__ __forceinline__ void unpack(uint32_t w, __nv_bfloat16, float& lo, float& hi) {
+  lo = __uint_as_float(w << 16);
+  hi = __uint_as_float(w & 0xffff0000u);
+}
+__device__ __forceinline__ void unpack(uint32_t w, __half, float& lo, float& hi) {
+  const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&w));
+  lo = f.x;
+  hi = f.y;
+}
+__device__ __forceinline__ uint32_t pack(float lo, float hi, __nv_bfloat16) {
+  const __nv_bfloat162 v = __floats2bfloat162_rn(lo, hi);
+  return *reinterpret_cast<const uint32_t*>(&v);
+}
+__device__ __forceinline__ uint32_t pack(float lo, float hi, __half) {
+  const __half2 v = __floats2half2_rn(lo, hi);
+  return *reinterpret_cast<const uint32_t*>(&v);
+}
+
+// kVec consecutive elements; kVec = 8 needs a 16-byte aligned address.
+template <int kVec, typename T>
+struct Elems {
+  static __device__ __forceinline__ void load(const T* p, float (&v)[kVec]) {
+    if constexpr (kVec == 1) {
+      v[0] = to_f32(*p);
+    } else if constexpr (sizeof(T) == 4) {
+      static_assert(kVec == 8, "one or eight elements");
+      const float4 a = reinterpret_cast<const float4*>(p)[0], b = reinterpret_cast<const float4*>(p)[1];
+      v[0] = a.x, v[1] = a.y, v[2] = a.z, v[3] = a.w, v[4] = b.x, v[5] = b.y, v[6] = b.z, v[7] = b.w;
+    } else {
+      static_assert(kVec == 8, "one or eight elements");
+      const uint4 a = *reinterpret_cast<const uint4*>(p);
+      unpack(a.x, T(), v[0], v[1]);
+      unpack(a.y, T(), v[2], v[3]);
+      unpack(a.z, T(), v[4], v[5]);
+      unpack(a.w, T(), v[6], v[7]);
+    }
+  }
+  static __device__ __forceinline__ void store(T* p, const float (&v)[kVec]) {
+    if constexpr (kVec == 1) {
+      *p = from_f32<T>(v[0]);
+    } else if constexpr (sizeof(T) == 4) {
+      reinterpret_cast<float4*>(p)[0] = make_float4(v[0], v[1], v[2], v[3]);
+      reinterpret_cast<float4*>(p)[1] = make_float4(v[4], v[5], v[6], v[7]);
+    } else {
+      *reinterpret_cast<uint4*>(p) = make_uint4(pack(v[0], v[1], T()), pack(v[2], v[3], T()),
+                                                pack(v[4], v[5], T()), pack(v[6], v[7], T()));
+    }
+  }
+};
+
+inline bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
+inline size_t type_bytes(int type) { return type == BSA_FP32 ? 4 : 2; }  // of bf16, fp16, fp32
+inline bool is_float_type(int type) { return type == BSA_BF16 || type == BSA_FP16 || type == BSA_FP32; }
+
+}  // namespace bsa

@@ -1,0 +1,735 @@
+// Product of 8-bit matrices with a scale for each block of 128, for B200 (sm_100a):
+//
+//     out[m, n] = sum_kb sa[m, kb] sb[n, kb] ( sum_{k in block kb} a[m, k] b[n, k] ) + bias[n].
+//
+// The scale of a block multiplies a finished partial sum, so the sum over 128 products stays
+// in the tensor cores and the sum over blocks is done in fp32 by threads, each block's
+// partial read from TMEM and added with its scale by one fma an element.
+//
+// bsa_fp8_mma_kernel, for more than 32 rows.  Persistent, one CTA per SM, 384 threads.  A
+// unit of work is a tile of 128 rows by kBN columns, over all of K or one of `splits` ranges
+// of blocks.
+//   warp 0     TMA producer: per block of K (128 bytes: one 128-byte swizzle atom) the A box
+//              (128 rows) and the B box (kBN rows) into a ring of shared-memory stages.
+//   warp 1     owns TMEM; lane 0 issues four tcgen05.mma (kind::f8f6f4, M = 128, N = kBN,
+//              K = 32) a block into one of 512 / kBN accumulators, each block starting from 0.
+//   warps 2-3  with a scale for each row of b: bring a block's kBN scales into shared memory.
+//   warps 4-11 two warpgroups; each takes half of the tile's columns and keeps their sums in
+//              registers (kBN / 2 a thread, a thread owning one row), reading an accumulator
+//              with tcgen05.ld as its MMAs complete and handing it back before the fmas.
+//              At a tile's end they add the bias and write rows through shared memory.
+// While they add one block the MMAs of the next run: at kBN = 256 the MMAs of a block take
+// 512 cycles of the tensor pipe and the fmas 256 of the fp32 pipes (512 with a scale for
+// each row of b, which costs a multiplication more).
+//
+// bsa_fp8_rows_kernel, for up to 32 rows (tokens).  There the time is that of reading b
+// once.  A block of threads takes 16 rows of b, its warps an equal share of K's blocks each;
+// the codes go straight from global memory to registers (16 bytes a thread and row), are
+// widened to fp16, which holds every e4m3 and e5m2 value, and multiplied by
+// mma.sync m16n8k16 with b as the 16-row side and the tokens as the 8 columns.  The products
+// of a block of 128 are summed in fp32 before their scale; the warps' sums meet in shared
+// memory in a fixed order.
+//
+// Every wait is bounded; on expiry the CTA records BSA_ERR_DEVICE_TIMEOUT, drains its copies
+// and MMAs, frees TMEM and returns.
+#include <cuda.h>
+#include <cuda_bf16.h>
+#include <cuda_fp16.h>
+#include <cuda_runtime.h>
+#include <cudaTypedefs.h>
+
+#include <algorithm>
+#include <mutex>
+
+#include "sm100_ptx.cuh"
+#include "bsa_wait.cuh"
+#include "bsa_elem.cuh"
+#include "bsa_host_cuda.h"
+
+namespace bsa {
+namespace {
+
+constexpr int kMThreads = 384;
+constexpr int kMB = 128;   // tile rows (TMEM lanes)
+constexpr int kKB = 128;   // block of K: bytes, products and scales
+constexpr int kPromoteWarp0 = 4, kPromoteWarps = 8;
+constexpr uint32_t kStgBytes = 2048;  // one warp's 32 rows of 64 bytes
+constexpr uint32_t kTmem = 512;
+
+template <int kBN>
+struct MmaCfg {
+  static constexpr int kStages = kBN == 256 ? 4 : 6;
+  static constexpr int kAcc = static_cast<int>(kTmem) / kBN;  // accumulators
+  static constexpr uint32_t kABytes = kMB * kKB, kBBytes = kBN * kKB, kStageBytes = kABytes + kBBytes;
+  static constexpr uint32_t kStg = kStages * kStageBytes;
+  static constexpr uint32_t kScale = kStg + kPromoteWarps * kStgBytes;  // [kAcc][kBN] fp32
+  static constexpr uint32_t kBar = kScale + kAcc * kBN * 4;
+  // barriers: stage full, stage empty, accumulator full, accumulator empty, scales full, scales empty, final
+  static constexpr int kFull = 0, kEmpty = kStages, kAccFull = 2 * kStages, kAccEmpty = kAccFull + kAcc,
+                       kScFull = kAccEmpty + kAcc, kScEmpty = kScFull + kAcc, kFinal = kScEmpty + kAcc,
+                       kBars = kFinal + 1;
+  static constexpr uint32_t kMisc = kBar + 8 * kBars;
+  static constexpr uint32_t kAlloc = kMisc + 16 + 1024;  // + slack for 1024-byte alignment
+  static_assert(kAlloc <= 227 * 1024, "shared memory budget");
+  static_assert(kStageBytes % 1024 == 0, "swizzle atoms must stay 1024-byte aligned");
+};
+
+struct MmaParams {
+  CUtensorMap tm_a, tm_b;
+  const float *sa, *sb;
+  const void* bias;
+  void* out;
+  int M, N, kb;         // kb: blocks of K
+  int a_shift, b_rows;  // row of sa = m >> a_shift; b_rows: a scale for each row of b
+  int bias_f32, out_f32;
+  int idesc_formats;    // A and B format bits of the instruction descriptor
+  int m_tiles, n_tiles, splits, kb_split, units;
+  int64_t split_stride;  // elements of one split's partial result (splits > 1: out is fp32 partials)
+  uint64_t timeout_ns;
+};
+
+__device__ __forceinline__ uint32_t bar_at(uint32_t bars, int i) { return bars + 8u * static_cast<uint32_t>(i); }
+
+// D[tmem] (+)= A[smem desc] * B[smem desc]^T, 8-bit floating point in, fp32 accumulate.
+__device__ __forceinline__ void mma_f8(uint32_t d_tmem, uint64_t a_desc, uint64_t b_desc, uint32_t idesc,
+                                       uint32_t accumulate) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "setp.ne.b32 p, %4, 0;\n\t"
+      "tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], %1, %2, %3, p;\n\t}" ::"r"(d_tmem),
+      "l"(a_desc), "l"(b_desc), "r"(idesc), "r"(accumulate)
+      : "memory");
+}
+
+// A unit of work: tile (m0, n0) over the blocks [k0, k1) of K.  Column tiles go fastest, so
+// that the CTAs of one moment share a few row tiles of A and all of B stays in L2.
+struct Unit {
+  int m0, n0, k0, k1, split;
+};
+template <int kBN>
+__device__ __forceinline__ Unit unit_of(const MmaParams& p, int u) {
+  const int tile = u / p.splits, split = u % p.splits;
+  Unit t;
+  t.m0 = (tile / p.n_tiles) * kMB;
+  t.n0 = (tile % p.n_tiles) * kBN;
+  t.k0 = split * p.kb_split;
+  t.k1 = min(t.k0 + p.kb_split, p.kb);
+  t.split = split;
+  return t;
+}
+
+template <int kBN>
+__device__ void mma_producer(const MmaParams& p, uint32_t smem, uint32_t bars, volatile int* abort_flag) {
+  using C = MmaCfg<kBN>;
+  const uint64_t pol_a = ptx::policy_evict_first(), pol_b = ptx::policy_evict_last();
+  uint32_t it = 0;
+  bool alive = true;
+  for (int u = blockIdx.x; alive && u < p.units; u += gridDim.x) {
+    const Unit t = unit_of<kBN>(p, u);
+    for (int kb = t.k0; kb < t.k1; ++kb, ++it) {
+      const uint32_t s = it % C::kStages;
+      if (it >= C::kStages &&
+          !wait_one(bar_at(bars, C::kEmpty + s), ((it / C::kStages) - 1u) & 1u, abort_flag, p.timeout_ns)) {
+        alive = false;
+        break;
+      }
+      const uint32_t full = bar_at(bars, C::kFull + s), dst = smem + s * C::kStageBytes;
+      ptx::mbar_arrive_expect_tx(full, C::kStageBytes);
+      ptx::tma_load_2d(dst, &p.tm_a, full, kb * kKB, t.m0, pol_a);
+      ptx::tma_load_2d(dst + C::kABytes, &p.tm_b, full, kb * kKB, t.n0, pol_b);
+    }
+  }
+  // the last load of each stage has landed before the CTA may exit
+  for (uint32_t j = it > C::kStages ? it - C::kStages : 0u; j < it; ++j)
+    wait_force(bar_at(bars, C::kFull + static_cast<int>(j % C::kStages)), (j / C::kStages) & 1u, abort_flag,
+               p.timeout_ns);
+}
+
+template <int kBN>
+__device__ void mma_issuer(const MmaParams& p, uint32_t smem, uint32_t bars, uint32_t tmem, volatile int* abort_flag) {
+  using C = MmaCfg<kBN>;
+  // bits 4-5 D format (1 = fp32), 7-9 and 10-12 A and B formats, 17-22 N >> 3, 24-28 M >> 4
+  const uint32_t idesc = (1u << 4) | static_cast<uint32_t>(p.idesc_formats) | (static_cast<uint32_t>(kBN >> 3) << 17) |
+                         (static_cast<uint32_t>(kMB >> 4) << 24);
+  uint32_t it = 0;
+  bool alive = true;
+  for (int u = blockIdx.x; alive && u < p.units; u += gridDim.x) {
+    const Unit t = unit_of<kBN>(p, u);
+    for (int kb = t.k0; kb < t.k1; ++kb, ++it) {
+      const uint32_t s = it % C::kStages, as = it % C::kAcc;
+      if ((it >= C::kAcc &&
+           !wait_one(bar_at(bars, C::kAccEmpty + as), ((it / C::kAcc) - 1u) & 1u, abort_flag, p.timeout_ns)) ||
+          !wait_one(bar_at(bars, C::kFull + s), (it / C::kStages) & 1u, abort_flag, p.timeout_ns)) {
+        alive = false;
+        break;
+      }
+      ptx::tc_fence_after();
+      const uint32_t sa = smem + s * C::kStageBytes;
+      const uint64_t da = ptx::smem_desc_sw128(sa, 16), db = ptx::smem_desc_sw128(sa + C::kABytes, 16);
+#pragma unroll
+      for (int j = 0; j < kKB / 32; ++j) mma_f8(tmem + as * kBN, da + 2u * j, db + 2u * j, idesc, j > 0 ? 1u : 0u);
+      ptx::mma_commit(bar_at(bars, C::kEmpty + s));
+      ptx::mma_commit(bar_at(bars, C::kAccFull + as));
+    }
+  }
+  ptx::mma_commit(bar_at(bars, C::kFinal));
+  wait_force(bar_at(bars, C::kFinal), 0u, abort_flag, p.timeout_ns);
+}
+
+// Two warps bring each block's kBN scales of b's rows into the buffer of its accumulator.
+template <int kBN>
+__device__ void scale_loader(const MmaParams& p, uint8_t* smem_gen, uint32_t bars, int t64, volatile int* abort_flag) {
+  using C = MmaCfg<kBN>;
+  uint32_t it = 0;
+  for (int u = blockIdx.x; u < p.units; u += gridDim.x) {
+    const Unit t = unit_of<kBN>(p, u);
+    for (int kb = t.k0; kb < t.k1; ++kb, ++it) {
+      const uint32_t as = it % C::kAcc;
+      float v[kBN / 64];
+#pragma unroll
+      for (int i = 0; i < kBN / 64; ++i) {
+        const int n = t.n0 + i * 64 + t64;
+        v[i] = n < p.N ? __ldg(p.sb + static_cast<int64_t>(n) * p.kb + kb) : 0.f;
+      }
+      if (it >= C::kAcc &&
+          !wait_warp(bar_at(bars, C::kScEmpty + as), ((it / C::kAcc) - 1u) & 1u, abort_flag, p.timeout_ns))
+        return;
+      float* dst = reinterpret_cast<float*>(smem_gen + C::kScale) + as * kBN;
+#pragma unroll
+      for (int i = 0; i < kBN / 64; ++i) dst[i * 64 + t64] = v[i];
+      __syncwarp();
+      if ((t64 & 31) == 0) ptx::mbar_arrive(bar_at(bars, C::kScFull + as));
+    }
+  }
+}
+
+// Adds the blocks of this thread's row and half of the columns, and writes them.
+template <int kBN, bool kBRows>
+__device__ void promoter(const MmaParams& p, uint8_t* smem_gen, uint32_t bars, uint32_t tmem, int warp, int lane,
+                         volatile int* abort_flag) {
+  using C = MmaCfg<kBN>;
+  constexpr int kCols = kBN / 2;
+  const int half = (warp - kPromoteWarp0) >> 2, quad = warp & 3;
+  const uint32_t taddr = tmem + (static_cast<uint32_t>(quad * 32) << 16) + half * kCols;
+  uint8_t* stg = smem_gen + C::kStg + (warp - kPromoteWarp0) * kStgBytes;
+  uint32_t it = 0;
+  for (int u = blockIdx.x; u < p.units; u += gridDim.x) {
+    const Unit t = unit_of<kBN>(p, u);
+    const int row = t.m0 + quad * 32 + lane, col0 = t.n0 + half * kCols;
+    const float* sa = p.sa + static_cast<int64_t>(min(row, p.M - 1) >> p.a_shift) * p.kb;
+    const float* sb = p.sb + static_cast<int64_t>(min(col0, p.N - 1) >> 7) * p.kb;  // kBRows: unused
+    uint64_t acc[kCols / 2];
+#pragma unroll
+    for (int i = 0; i < kCols / 2; ++i) acc[i] = 0ull;
+    float next_a = __ldg(sa + t.k0), next_b = kBRows ? 1.f : __ldg(sb + t.k0);
+    for (int kb = t.k0; kb < t.k1; ++kb, ++it) {
+      const uint32_t as = it % C::kAcc, parity = (it / C::kAcc) & 1u;
+      const float s = kBRows ? next_a : next_a * next_b;
+      if (kb + 1 < t.k1) {
+        next_a = __ldg(sa + kb + 1);
+        if (!kBRows) next_b = __ldg(sb + kb + 1);
+      }
+      if (kBRows && !wait_warp<1>(bar_at(bars, C::kScFull + as), parity, abort_flag, p.timeout_ns)) return;
+      if (!wait_warp<1>(bar_at(bars, C::kAccFull + as), parity, abort_flag, p.timeout_ns)) return;
+      ptx::tc_fence_after();
+      const uint64_t s2 = ptx::pack2(s, s);
+      const float4* sc = reinterpret_cast<const float4*>(smem_gen + C::kScale) + as * (kBN / 4) + half * (kCols / 4);
+#pragma unroll
+      for (int g = 0; g < kCols / 32; ++g) {
+        uint32_t r[32];
+        ptx::tmem_ld32(taddr + as * kBN + 32u * g, r);
+        ptx::tmem_wait_ld();
+        ptx::reg_fence(r);
+        if (g == kCols / 32 - 1) {
+          ptx::tc_fence_before();
+          __syncwarp();
+          if (lane == 0) ptx::mbar_arrive(bar_at(bars, C::kAccEmpty + as));
+        }
+#pragma unroll
+        for (int j = 0; j < 32; j += 4) {
+          uint64_t lo = ptx::pack2(__uint_as_float(r[j]), __uint_as_float(r[j + 1]));
+          uint64_t hi = ptx::pack2(__uint_as_float(r[j + 2]), __uint_as_float(r[j + 3]));
+          if constexpr (kBRows) {
+            const float4 b = sc[g * 8 + j / 4];
+            lo = ptx::fmul2(lo, ptx::pack2(b.x, b.y));
+            hi = ptx::fmul2(hi, ptx::pack2(b.z, b.w));
+          }
+          uint64_t& a0 = acc[(g * 32 + j) / 2];
+          uint64_t& a1 = acc[(g * 32 + j) / 2 + 1];
+          a0 = ptx::ffma2(lo, s2, a0);
+          a1 = ptx::ffma2(hi, s2, a1);
+        }
+      }
+      if constexpr (kBRows) {
+        __syncwarp();
+        if (lane == 0) ptx::mbar_arrive(bar_at(bars, C::kScEmpty + as));
+      }
+    }
+    // ---- write: 64 bytes of each of the warp's 32 rows at a time, through shared memory
+    // (16-byte chunk j of row r at chunk j ^ (r / 2 % 4), so that neither side conflicts)
+    const int esize = p.out_f32 ? 4 : 2;
+    uint8_t* out = static_cast<uint8_t*>(p.out) + t.split * p.split_stride * esize;
+    const bool whole = (static_cast<int64_t>(p.N) * esize) % 16 == 0 && (reinterpret_cast<uintptr_t>(p.out) & 15u) == 0;
+    auto put = [&](int c, int cols) {  // columns c .. c + cols of the tile's half are staged
+      __syncwarp();
+      const int n0 = col0 + c;
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const int r = i * 8 + (lane >> 2), j = lane & 3, m = t.m0 + quad * 32 + r;
+        const int per = cols / 4;  // elements of a 16-byte chunk
+        const uint4 w = *reinterpret_cast<const uint4*>(stg + r * 64 + ((j ^ ((r >> 1) & 3)) << 4));
+        const int n = n0 + j * per;
+        if (m >= p.M || n >= p.N) continue;
+        uint8_t* dst = out + (static_cast<int64_t>(m) * p.N + n) * esize;
+        if (whole) {
+          *reinterpret_cast<uint4*>(dst) = w;
+        } else if (p.out_f32) {
+          const uint32_t x[4] = {w.x, w.y, w.z, w.w};
+#pragma unroll
+          for (int e = 0; e < 4; ++e)
+            if (n + e < p.N) reinterpret_cast<uint32_t*>(dst)[e] = x[e];
+        } else {
+          const uint32_t x[4] = {w.x, w.y, w.z, w.w};
+#pragma unroll
+          for (int e = 0; e < 8; ++e)
+            if (n + e < p.N) reinterpret_cast<uint16_t*>(dst)[e] = static_cast<uint16_t>(x[e >> 1] >> ((e & 1) * 16));
+        }
+      }
+      __syncwarp();
+    };
+#pragma unroll
+    for (int g = 0; g < kCols / 32; ++g) {
+      if (col0 + 32 * g >= p.N) break;
+      float v[32];
+#pragma unroll
+      for (int j = 0; j < 16; ++j) ptx::unpack2(acc[g * 16 + j], v[2 * j], v[2 * j + 1]);
+      if (p.bias != nullptr) {
+#pragma unroll
+        for (int j = 0; j < 32; ++j) {
+          const int n = col0 + 32 * g + j;
+          if (n < p.N)
+            v[j] += p.bias_f32 ? __ldg(static_cast<const float*>(p.bias) + n)
+                               : __bfloat162float(static_cast<const __nv_bfloat16*>(p.bias)[n]);
+        }
+      }
+      uint8_t* mine = stg + lane * 64;
+      const int x = (lane >> 1) & 3;
+      if (p.out_f32) {
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+#pragma unroll
+          for (int j = 0; j < 4; ++j)
+            *reinterpret_cast<float4*>(mine + ((j ^ x) << 4)) =
+                make_float4(v[h * 16 + 4 * j], v[h * 16 + 4 * j + 1], v[h * 16 + 4 * j + 2], v[h * 16 + 4 * j + 3]);
+          put(32 * g + 16 * h, 16);
+        }
+      } else {
+#pragma unroll
+        for (int j = 0; j < 4; ++j)
+          *reinterpret_cast<uint4*>(mine + ((j ^ x) << 4)) =
+              make_uint4(pack_bf16x2(v[8 * j], v[8 * j + 1]), pack_bf16x2(v[8 * j + 2], v[8 * j + 3]),
+                         pack_bf16x2(v[8 * j + 4], v[8 * j + 5]), pack_bf16x2(v[8 * j + 6], v[8 * j + 7]));
+        put(32 * g, 32);
+      }
+    }
+  }
+}
+
+template <int kBN, bool kBRows>
+__global__ void __launch_bounds__(kMThreads, 1) bsa_fp8_mma_kernel(const __grid_constant__ MmaParams p) {
+  using C = MmaCfg<kBN>;
+  extern __shared__ uint8_t smem_raw[];
+  const uint32_t raw = ptx::smem_addr(smem_raw);
+  const uint32_t base = (raw + 1023u) & ~1023u;
+  uint8_t* smem = smem_raw + (base - raw);
+  volatile uint32_t* misc = reinterpret_cast<volatile uint32_t*>(smem + C::kMisc);
+  volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + C::kMisc + 4);
+  const uint32_t bars = base + C::kBar;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  if (threadIdx.x == 0) {
+    for (int i = 0; i < C::kBars; ++i) {
+      const bool acc_empty = i >= C::kAccEmpty && i < C::kAccEmpty + C::kAcc;
+      const bool sc_empty = i >= C::kScEmpty && i < C::kScEmpty + C::kAcc;
+      const bool sc_full = i >= C::kScFull && i < C::kScFull + C::kAcc;
+      ptx::mbar_init(bar_at(bars, i), acc_empty || sc_empty ? kPromoteWarps : sc_full ? 2u : 1u);
+    }
+    *abort_flag = 0;
+    ptx::fence_barrier_init();
+    ptx::prefetch_tensormap(&p.tm_a);
+    ptx::prefetch_tensormap(&p.tm_b);
+  }
+  if (warp == 1) {
+    ptx::tmem_alloc(ptx::smem_addr(const_cast<uint32_t*>(&misc[0])), kTmem);
+    ptx::tmem_relinquish();
+  }
+  ptx::tc_fence_before();
+  __syncthreads();
+  ptx::tc_fence_after();
+  const uint32_t tmem = misc[0];
+  // the launch's 168 registers a thread, split: 128 * 56 + 256 * 216 <= 384 * 168
+  if (warp < kPromoteWarp0) {
+    ptx::setmaxnreg_dec<56>();
+    if (warp == 0) {
+      if (lane == 0) mma_producer<kBN>(p, base, bars, abort_flag);
+    } else if (warp == 1) {
+      if (lane == 0) mma_issuer<kBN>(p, base, bars, tmem, abort_flag);
+    } else if (kBRows) {
+      scale_loader<kBN>(p, smem, bars, static_cast<int>(threadIdx.x) - 64, abort_flag);
+    }
+    __syncwarp();
+  } else {
+    ptx::setmaxnreg_inc<216>();
+    promoter<kBN, kBRows>(p, smem, bars, tmem, warp, lane, abort_flag);
+  }
+  ptx::tc_fence_before();
+  __syncthreads();
+  ptx::tc_fence_after();
+  if (warp == 1) ptx::tmem_dealloc(tmem, kTmem);
+}
+
+// Sums the splits' partial results in order, adds the bias and rounds once.
+__global__ void __launch_bounds__(256) bsa_fp8_sum_kernel(const float* part, int splits, int64_t stride, int64_t n,
+                                                          int N, const void* bias, int bias_f32, void* out,
+                                                          int out_f32) {
+  const int64_t i = static_cast<int64_t>(blockIdx.x) * 256 + threadIdx.x;
+  if (i >= n) return;
+  float v = 0.f;
+#pragma unroll 8
+  for (int s = 0; s < splits; ++s) v += part[s * stride + i];
+  if (bias != nullptr) {
+    const int c = static_cast<int>(i % N);
+    v += bias_f32 ? static_cast<const float*>(bias)[c] : __bfloat162float(static_cast<const __nv_bfloat16*>(bias)[c]);
+  }
+  if (out_f32) static_cast<float*>(out)[i] = v;
+  else static_cast<__nv_bfloat16*>(out)[i] = __float2bfloat16_rn(v);
+}
+
+// ------------------------------------------------------------ a few rows
+struct RowsParams {
+  const uint8_t *a, *b;
+  int64_t lda, ldb;
+  const float *sa, *sb;
+  const void* bias;
+  void* out;
+  int M, N, K, kb;
+  int a_shift, b_shift;
+  int bias_f32, out_f32;
+};
+
+constexpr int kRowsMost = 32;      // rows of a that the kernel takes
+constexpr int kRowsWarpsMost = 8;  // warps of a block at most
+
+template <bool kE5>
+__device__ __forceinline__ uint32_t widen(uint32_t two) {  // two codes in the low 16 bits -> two fp16
+  uint32_t r;
+  const uint16_t h = static_cast<uint16_t>(two);
+  if constexpr (kE5) asm("cvt.rn.f16x2.e5m2x2 %0, %1;" : "=r"(r) : "h"(h));
+  else asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(r) : "h"(h));
+  return r;
+}
+
+__device__ __forceinline__ void mma_f16(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
+                                        uint32_t b1) {
+  asm volatile("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+               : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+               : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
+
+// 16 codes of a row at column k (a multiple of 16); zeros past the row's end, which is not
+// read past.
+__device__ __forceinline__ uint4 codes16(const uint8_t* row, int k, int K) {
+  if (k + 16 <= K) return __ldg(reinterpret_cast<const uint4*>(row + k));
+  uint32_t x[4] = {};
+#pragma unroll
+  for (int i = 0; i < 15; ++i)
+    if (k + i < K) x[i >> 2] |= static_cast<uint32_t>(row[k + i]) << (8 * (i & 3));
+  return make_uint4(x[0], x[1], x[2], x[3]);
+}
+
+// kG groups of eight tokens.  Thread (g, t) of a warp (lane / 4, lane % 4) holds, of each 64
+// codes of K, the 16 at 16 t of b's rows g and g + 8 and of tokens g, g + 8, ..: any order of
+// K's products gives the same sum, so four codes of these serve as the thread's k-slots of one
+// m16n8k16 product.
+template <int kG, bool kAE5, bool kBE5>
+__global__ void __launch_bounds__(kRowsWarpsMost * 32) bsa_fp8_rows_kernel(const __grid_constant__ RowsParams p) {
+  __shared__ float part[kRowsWarpsMost][kG][32][4];
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
+  const int warps = blockDim.x >> 5;
+  const int n0 = blockIdx.x * 16 + g, n1 = n0 + 8;
+  const uint8_t* b0 = p.b + static_cast<int64_t>(min(n0, p.N - 1)) * p.ldb;
+  const uint8_t* b1 = p.b + static_cast<int64_t>(min(n1, p.N - 1)) * p.ldb;
+  const float* sb0 = p.sb + static_cast<int64_t>(min(n0, p.N - 1) >> p.b_shift) * p.kb;
+  const float* sb1 = p.sb + static_cast<int64_t>(min(n1, p.N - 1) >> p.b_shift) * p.kb;
+  const int per = (p.kb + warps - 1) / warps;
+  const int k0 = warp * per, k1 = min(k0 + per, p.kb);
+  float acc[kG][4] = {};
+  for (int kb = k0; kb < k1; ++kb) {
+    uint4 w0[2], w1[2];
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+      w0[h] = codes16(b0, kb * kKB + h * 64 + t * 16, p.K);
+      w1[h] = codes16(b1, kb * kKB + h * 64 + t * 16, p.K);
+    }
+    const float s0 = __ldg(sb0 + kb), s1 = __ldg(sb1 + kb);
+    float d[kG][4] = {};
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+      uint4 x[kG];
+#pragma unroll
+      for (int q = 0; q < kG; ++q) {
+        const int m = q * 8 + g;
+        x[q] = m < p.M ? codes16(p.a + static_cast<int64_t>(m) * p.lda, kb * kKB + h * 64 + t * 16, p.K)
+                       : make_uint4(0, 0, 0, 0);
+      }
+      const uint32_t r0[4] = {w0[h].x, w0[h].y, w0[h].z, w0[h].w}, r1[4] = {w1[h].x, w1[h].y, w1[h].z, w1[h].w};
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const uint32_t a0 = widen<kBE5>(r0[i]), a2 = widen<kBE5>(r0[i] >> 16);
+        const uint32_t a1 = widen<kBE5>(r1[i]), a3 = widen<kBE5>(r1[i] >> 16);
+#pragma unroll
+        for (int q = 0; q < kG; ++q) {
+          const uint32_t xi = i == 0 ? x[q].x : i == 1 ? x[q].y : i == 2 ? x[q].z : x[q].w;
+          mma_f16(d[q], a0, a1, a2, a3, widen<kAE5>(xi), widen<kAE5>(xi >> 16));
+        }
+      }
+    }
+#pragma unroll
+    for (int q = 0; q < kG; ++q) {
+      const int m = q * 8 + 2 * t;
+      const float m0 = __ldg(p.sa + static_cast<int64_t>(min(m, p.M - 1) >> p.a_shift) * p.kb + kb);
+      const float m1 = __ldg(p.sa + static_cast<int64_t>(min(m + 1, p.M - 1) >> p.a_shift) * p.kb + kb);
+      acc[q][0] = fmaf(d[q][0], s0 * m0, acc[q][0]);
+      acc[q][1] = fmaf(d[q][1], s0 * m1, acc[q][1]);
+      acc[q][2] = fmaf(d[q][2], s1 * m0, acc[q][2]);
+      acc[q][3] = fmaf(d[q][3], s1 * m1, acc[q][3]);
+    }
+  }
+#pragma unroll
+  for (int q = 0; q < kG; ++q)
+#pragma unroll
+    for (int i = 0; i < 4; ++i) part[warp][q][lane][i] = acc[q][i];
+  __syncthreads();
+  // output (m, n): 16 neighbouring threads write 16 neighbouring columns of one token
+  for (int o = threadIdx.x; o < kG * 8 * 16; o += blockDim.x) {
+    const int c = o & 15, m = o >> 4, n = blockIdx.x * 16 + c;
+    if (m >= p.M || n >= p.N) continue;
+    const int q = m >> 3, ln = (c & 7) * 4 + ((m & 7) >> 1), i = (c >> 3) * 2 + (m & 1);
+    float v = 0.f;
+    for (int w = 0; w < warps; ++w) v += part[w][q][ln][i];
+    if (p.bias != nullptr)
+      v += p.bias_f32 ? static_cast<const float*>(p.bias)[n]
+                      : __bfloat162float(static_cast<const __nv_bfloat16*>(p.bias)[n]);
+    const int64_t at = static_cast<int64_t>(m) * p.N + n;
+    if (p.out_f32) static_cast<float*>(p.out)[at] = v;
+    else static_cast<__nv_bfloat16*>(p.out)[at] = __float2bfloat16_rn(v);
+  }
+}
+
+template <int kG>
+void launch_rows(const RowsParams& p, bool ae5, bool be5, int grid, int threads, cudaStream_t s) {
+  if (ae5) be5 ? bsa_fp8_rows_kernel<kG, true, true><<<grid, threads, 0, s>>>(p)
+               : bsa_fp8_rows_kernel<kG, true, false><<<grid, threads, 0, s>>>(p);
+  else be5 ? bsa_fp8_rows_kernel<kG, false, true><<<grid, threads, 0, s>>>(p)
+           : bsa_fp8_rows_kernel<kG, false, false><<<grid, threads, 0, s>>>(p);
+}
+
+// ------------------------------------------------------------ host
+PFN_cuTensorMapEncodeTiled_v12000 encode_fn() {
+  static PFN_cuTensorMapEncodeTiled_v12000 fn = nullptr;
+  static std::once_flag once;
+  std::call_once(once, [] {
+    void* ptr = nullptr;
+    cudaDriverEntryPointQueryResult q{};
+    if (cudaGetDriverEntryPoint("cuTensorMapEncodeTiled", &ptr, cudaEnableDefault, &q) == cudaSuccess &&
+        q == cudaDriverEntryPointSuccess)
+      fn = reinterpret_cast<PFN_cuTensorMapEncodeTiled_v12000>(ptr);
+  });
+  return fn;
+}
+
+// 8-bit [rows, cols] of the given pitch, boxes of 128 columns x box_rows, 128-byte swizzle;
+// what lies past the matrix reads as zeros.
+bool map_codes(CUtensorMap* m, const void* ptr, uint64_t rows, uint64_t cols, uint64_t pitch, uint32_t box_rows) {
+  auto fn = encode_fn();
+  if (fn == nullptr) return false;
+  const cuuint64_t dims[2] = {cols, rows}, strides[1] = {pitch};
+  const cuuint32_t box[2] = {kKB, box_rows}, estr[2] = {1, 1};
+  return fn(m, CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, const_cast<void*>(ptr), dims, strides, box, estr,
+            CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+            CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+// Per device, once: whether it is an sm_100 part, its SM count, and the kernels' shared-
+// memory attributes set.  A failed setup is not cached.
+constexpr int kMaxFp8Devices = 64;
+int g_fp8_sms[kMaxFp8Devices] = {};
+std::mutex g_fp8_mu;
+
+template <int kBN, bool kBRows>
+bool allow_smem() {
+  return cudaFuncSetAttribute(bsa_fp8_mma_kernel<kBN, kBRows>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                              static_cast<int>(MmaCfg<kBN>::kAlloc)) == cudaSuccess;
+}
+
+int fp8_device_sms() {
+  int dev = -1;
+  if (cudaGetDevice(&dev) != cudaSuccess) return BSA_ERR_CUDA;
+  if (dev < 0 || dev >= kMaxFp8Devices) return BSA_ERR_UNSUPPORTED;
+  std::lock_guard<std::mutex> lk(g_fp8_mu);
+  if (g_fp8_sms[dev] != 0) return g_fp8_sms[dev];
+  int major = 0, minor = 0, sms = 0;
+  if (cudaDeviceGetAttribute(&major, cudaDevAttrComputeCapabilityMajor, dev) != cudaSuccess ||
+      cudaDeviceGetAttribute(&minor, cudaDevAttrComputeCapabilityMinor, dev) != cudaSuccess ||
+      cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess)
+    return BSA_ERR_CUDA;
+  if (major != 10 || minor != 0) {
+    g_fp8_sms[dev] = BSA_ERR_UNSUPPORTED;
+    return BSA_ERR_UNSUPPORTED;
+  }
+  if (!allow_smem<256, false>() || !allow_smem<256, true>() || !allow_smem<128, false>() || !allow_smem<128, true>())
+    return BSA_ERR_CUDA;
+  g_fp8_sms[dev] = sms;
+  return sms;
+}
+
+// Tile width and split of K for a product on `sms` SMs: the pair with the least estimate of
+//     waves of units x (blocks of K a unit x block time + a unit's start and end) + bytes of
+// the splits' partial results, in cycles.
+struct MmaPlan {
+  int bn, splits, kb_split;
+  size_t bytes;
+};
+MmaPlan mma_plan(int64_t M, int64_t N, int64_t kb, int sms) {
+  MmaPlan best{256, 1, static_cast<int>(kb), 0};
+  double least = 1e30;
+  for (const int bn : {256, 128}) {
+    const int64_t tiles = ((M + kMB - 1) / kMB) * ((N + bn - 1) / bn);
+    for (int64_t want = 1; want <= 32 && want <= kb; ++want) {
+      const int64_t per = (kb + want - 1) / want, splits = (kb + per - 1) / per;
+      if (splits != want) continue;
+      const int64_t waves = (tiles * splits + sms - 1) / sms;
+      double cost = static_cast<double>(waves) * (static_cast<double>(per) * (bn == 256 ? 560 : 330) + 2500.0);
+      // partials: written and read once, about 3000 bytes a cycle, and a second launch
+      if (splits > 1) cost += 4000.0 + static_cast<double>(splits) * M * N * 8.0 / 3000.0;
+      if (cost < least) {
+        least = cost;
+        best = MmaPlan{bn, static_cast<int>(splits), static_cast<int>(per),
+                       splits > 1 ? static_cast<size_t>(splits) * M * N * sizeof(float) : 0};
+      }
+    }
+  }
+  return best;
+}
+
+int format_bits(int type) { return type == BSA_E5M2 ? 1 : 0; }
+
+template <int kBN>
+void launch_mma(const MmaParams& p, int grid, cudaStream_t s) {
+  if (p.b_rows) bsa_fp8_mma_kernel<kBN, true><<<grid, kMThreads, MmaCfg<kBN>::kAlloc, s>>>(p);
+  else bsa_fp8_mma_kernel<kBN, false><<<grid, kMThreads, MmaCfg<kBN>::kAlloc, s>>>(p);
+}
+
+}  // namespace
+
+int fp8_take_status() {
+  int st = 0;
+  if (cudaMemcpyFromSymbol(&st, g_bsa_status, sizeof(int)) != cudaSuccess) return BSA_ERR_CUDA;
+  if (st != 0) {
+    const int zero = 0;
+    if (cudaMemcpyToSymbol(g_bsa_status, &zero, sizeof(int)) != cudaSuccess) return BSA_ERR_CUDA;
+  }
+  return st;
+}
+
+}  // namespace bsa
+
+using namespace bsa;
+
+namespace {
+bool sizes_ok(int M, int N, int K) {
+  return M >= 0 && N >= 0 && K >= 1 && M <= (1 << 30) && N <= (1 << 30) && K <= (1 << 30);
+}
+}  // namespace
+
+extern "C" {
+
+int bsa_fp8_matmul_workspace_bytes(int M, int N, int K, size_t* bytes) {
+  if (bytes == nullptr || !sizes_ok(M, N, K)) return BSA_ERR_INVALID_ARG;
+  *bytes = 0;
+  if (M <= kRowsMost || N == 0) return BSA_OK;
+  const int sms = fp8_device_sms();
+  if (sms < 0) return sms;
+  *bytes = (mma_plan(M, N, (static_cast<int64_t>(K) + kKB - 1) / kKB, sms).bytes + 255) / 256 * 256;
+  return BSA_OK;
+}
+
+int bsa_fp8_matmul(const void* a, int a_type, int64_t lda, const float* a_scale, int a_rows, const void* b,
+                   int b_type, int64_t ldb, const float* b_scale, int b_rows, const void* bias, int bias_type,
+                   int M, int N, int K, void* out, int out_type, void* workspace, size_t workspace_bytes,
+                   void* stream) {
+  if (!sizes_ok(M, N, K)) return BSA_ERR_INVALID_ARG;
+  if ((a_type != BSA_E4M3 && a_type != BSA_E5M2) || (b_type != BSA_E4M3 && b_type != BSA_E5M2) ||
+      (out_type != BSA_BF16 && out_type != BSA_FP32) || (a_rows != 1 && a_rows != 128) ||
+      (b_rows != 1 && b_rows != 128) || (bias != nullptr && bias_type != BSA_BF16 && bias_type != BSA_FP32))
+    return BSA_ERR_UNSUPPORTED;
+  if (M == 0 || N == 0) return BSA_OK;
+  if (a == nullptr || b == nullptr || a_scale == nullptr || b_scale == nullptr || out == nullptr)
+    return BSA_ERR_INVALID_ARG;
+  if (!aligned16(a) || !aligned16(b) || lda % 16 != 0 || ldb % 16 != 0 || lda < K || ldb < K)
+    return BSA_ERR_INVALID_ARG;
+  if ((reinterpret_cast<uintptr_t>(a_scale) | reinterpret_cast<uintptr_t>(b_scale)) % 4 != 0 ||
+      reinterpret_cast<uintptr_t>(out) % type_bytes(out_type) != 0 ||
+      (bias != nullptr && reinterpret_cast<uintptr_t>(bias) % type_bytes(bias_type) != 0))
+    return BSA_ERR_INVALID_ARG;
+  const int sms = fp8_device_sms();
+  if (sms < 0) return sms;
+  cudaStream_t s = static_cast<cudaStream_t>(stream);
+  const int kb = static_cast<int>((static_cast<int64_t>(K) + kKB - 1) / kKB);
+  const int bias_f32 = bias_type == BSA_FP32, out_f32 = out_type == BSA_FP32;
+  if (M <= kRowsMost) {
+    RowsParams p{};
+    p.a = static_cast<const uint8_t*>(a), p.b = static_cast<const uint8_t*>(b);
+    p.lda = lda, p.ldb = ldb, p.sa = a_scale, p.sb = b_scale, p.bias = bias, p.out = out;
+    p.M = M, p.N = N, p.K = K, p.kb = kb;
+    p.a_shift = a_rows == 128 ? 7 : 0, p.b_shift = b_rows == 128 ? 7 : 0;
+    p.bias_f32 = bias_f32, p.out_f32 = out_f32;
+    const int grid = (N + 15) / 16, threads = 32 * std::min(kb, kRowsWarpsMost);
+    const bool ae5 = a_type == BSA_E5M2, be5 = b_type == BSA_E5M2;
+    if (M <= 8) launch_rows<1>(p, ae5, be5, grid, threads, s);
+    else if (M <= 16) launch_rows<2>(p, ae5, be5, grid, threads, s);
+    else launch_rows<4>(p, ae5, be5, grid, threads, s);
+    return cudaGetLastError() == cudaSuccess ? BSA_OK : BSA_ERR_CUDA;
+  }
+  const MmaPlan plan = mma_plan(M, N, kb, sms);
+  if (plan.bytes > 0 && (workspace == nullptr || reinterpret_cast<uintptr_t>(workspace) % 256 != 0 ||
+                         workspace_bytes < plan.bytes))
+    return BSA_ERR_WORKSPACE;
+  MmaParams p{};
+  if (!map_codes(&p.tm_a, a, M, K, lda, kMB) || !map_codes(&p.tm_b, b, N, K, ldb, plan.bn)) return BSA_ERR_CUDA;
+  p.sa = a_scale, p.sb = b_scale;
+  p.M = M, p.N = N, p.kb = kb;
+  p.a_shift = a_rows == 128 ? 7 : 0, p.b_rows = b_rows == 1;
+  p.idesc_formats = (format_bits(a_type) << 7) | (format_bits(b_type) << 10);
+  p.m_tiles = (M + kMB - 1) / kMB, p.n_tiles = (N + plan.bn - 1) / plan.bn;
+  p.splits = plan.splits, p.kb_split = plan.kb_split;
+  const int64_t units = static_cast<int64_t>(p.m_tiles) * p.n_tiles * p.splits;
+  if (units > (1 << 30)) return BSA_ERR_INVALID_ARG;
+  p.units = static_cast<int>(units);
+  p.timeout_ns = kDefaultTimeoutNs;
+  const bool split = plan.splits > 1;
+  const int64_t n = static_cast<int64_t>(M) * N;
+  p.split_stride = split ? n : 0;
+  p.out = split ? workspace : out;
+  p.out_f32 = split || out_f32;
+  p.bias = split ? nullptr : bias;
+  p.bias_f32 = bias_f32;
+  const int grid = static_cast<int>(std::min<int64_t>(units, sms));
+  if (plan.bn == 256) launch_mma<256>(p, grid, s);
+  else launch_mma<128>(p, grid, s);
+  if (split)
+    bsa_fp8_sum_kernel<<<static_cast<unsigned>((n + 255) / 256), 256, 0, s>>>(
+        static_cast<const float*>(workspace), plan.splits, n, n, N, bias, bias_f32, out, out_f32);
+  return cudaGetLastError() == cudaSuccess ? BSA_OK : BSA_ERR_CUDA;
+}
+
+}  // extern "C"

@@ -382,7 +382,8 @@ int proj_take_status() {
     const int zero = 0;
     if (cudaMemcpyToSymbol(g_bsa_status, &zero, sizeof(int)) != cudaSuccess) return BSA_ERR_CUDA;
   }
-  return st;
+  const int st_fp8 = fp8_take_status();  // the 8-bit product's status word
+  return st != 0 ? st : st_fp8;
 }
 
 }  // namespace bsa

@@ -388,6 +388,174 @@ int bsa_qkv_projection(const void* x, const void* w, const void* bias, int B, in
 int bsa_out_projection(const void* o, const void* w, const void* bias, int B, int H, int L, int N, void* y,
                        void* stream);
 
+/* ------------------------------------------------------------------------
+ * Around the attention: rotary positions, the norms and the residual of a block,
+ * and projections in 8-bit floating point.  Element types of these entry points:
+ */
+typedef enum {
+  BSA_BF16 = 0,
+  BSA_FP16 = 1,
+  BSA_FP32 = 2,
+  BSA_E4M3 = 3, /* 8-bit floating point: 4 exponent bits, 3 mantissa bits, largest value 448 */
+  BSA_E5M2 = 4, /* 5 exponent bits, 2 mantissa bits, largest finite value 57344 */
+  BSA_INT32 = 5,
+  BSA_INT64 = 6
+} bsa_type;
+
+/* Frequencies and axes of a rotary position code.  Owned by the library; release with
+ * bsa_rope_free.  Host memory only, immutable, usable by concurrent calls on any device. */
+typedef struct bsa_rope bsa_rope;
+
+/*
+ * bsa_rope_build -- host only.  A rotary code over n_axes position axes (1 to 8; time,
+ * height and width for images and video).  sections[a] >= 0 is the number of pairs axis a
+ * turns, n = their sum, 1 <= n <= 128.  Pair j belongs to the axes in order (the first
+ * sections[0] pairs to axis 0, and so on), or with `interleave` to the axes in turn, an
+ * axis dropping out once its section is used up.  Its frequency is
+ *     base^(-j / n), or with `per_axis` base^(-i / sections[a]) for the i-th pair of axis a.
+ * adjacent = 0: pair j holds the columns j and n + j of a head; 1: 2 j and 2 j + 1.
+ * base > 0 and finite (else BSA_ERR_INVALID_ARG).
+ */
+int bsa_rope_build(const int32_t* sections, int n_axes, double base, int per_axis, int interleave, int adjacent,
+                   bsa_rope** out);
+
+/* bsa_rope_from_table -- host only.  The same from a caller's tables: axis[j] in [0, 8) and
+ * the finite frequency freq[j] (radians per position) of each of n_pairs pairs. */
+int bsa_rope_from_table(const int32_t* axis, const double* freq, int n_pairs, int adjacent, bsa_rope** out);
+
+/* bsa_rope_table -- host views of the axis and frequency of each pair, their number, the
+ * number of axes (one more than the largest axis used) and the pair order.  Any output may
+ * be NULL; the views stay valid until bsa_rope_free. */
+int bsa_rope_table(const bsa_rope* rope, const int32_t** axis, const double** freq, int* n_pairs, int* n_axes,
+                   int* adjacent);
+
+void bsa_rope_free(bsa_rope* rope);
+
+/*
+ * bsa_rope_apply -- turns the pairs (u, v) of every head of q and k by the angle of their
+ * token, and copies the columns past 2 n:
+ *     (u, v) -> (u cos t - v sin t, u sin t + v cos t),  t = p[axis_j, b, l] freq_j,
+ * or by -t with `inverse` (the gradient of the forward).
+ *   q, k      device, `type` (BSA_BF16, BSA_FP16 or BSA_FP32): [B, H, L, d] and
+ *             [B, Hk, L, d] with the element strides below; columns contiguous.  k may be
+ *             NULL (Hk ignored).
+ *   q_out, k_out  device, the same shapes; may be q and k themselves with the same strides
+ *             (any other overlap gives undefined results).
+ *   strides   host, 12 int64: (b, h, l) of q, of q_out, of k, of k_out.
+ *   positions device, BSA_INT32, BSA_INT64 or BSA_FP32: element
+ *             a p_strides[0] + b p_strides[1] + l p_strides[2] is p[a, b, l]
+ *             (p_strides host, 3 int64; 0 shares positions between batch elements).
+ *   d         2 n <= d <= 256.
+ * The angle is formed in 64 bits, so that far positions keep their phase.  B, H or L of 0
+ * is an empty call.  Enqueues one kernel on `stream`.
+ */
+int bsa_rope_apply(const void* q, void* q_out, int H, const void* k, void* k_out, int Hk, int B, int L, int d,
+                   int type, const int64_t* strides, const void* positions, int position_type,
+                   const int64_t* p_strides, const bsa_rope* rope, int inverse, void* stream);
+
+/* Norms of bsa_block_norm. */
+#define BSA_NORM_NONE 0
+#define BSA_NORM_RMS 1   /* x / sqrt(mean(x^2) + eps) */
+#define BSA_NORM_LAYER 2 /* (x - mean x) / sqrt(var x + eps), the biased variance */
+
+/*
+ * What bsa_block_norm and its backward share.  For each row (token) of C columns:
+ *     z       = N_post(y) post_weight + post_bias     (y itself with BSA_NORM_NONE)
+ *     stream  = stream_scale x + branch_scale gate z
+ *     normed  = N_pre(stream) pre_weight + pre_bias
+ * the residual after a block with the norm after it and its gate, and the norm before the
+ * next block.  Without y the stream is x itself and only the second norm is taken.
+ *   rows = B * rows_per_batch rows; gate is [C] (gate_rows = 1) or [B, C] (gate_rows = B),
+ *   row i taking row i / rows_per_batch of it.  1 <= C <= 8192.
+ *   Parameters and gate are device arrays of `param_type` (`type` or BSA_FP32); weights and
+ *   biases may be NULL (1 and 0), the gate too (1).  Biases need a norm.
+ */
+typedef struct {
+  int B, rows_per_batch, C;
+  int type, param_type;
+  int post, pre; /* BSA_NORM_* */
+  const void *post_weight, *post_bias, *gate, *pre_weight, *pre_bias;
+  int gate_rows;
+  float branch_scale, stream_scale, eps;
+} bsa_block_norm_args;
+
+/*
+ * bsa_block_norm -- the forward.  x, y: device, `type`, [rows, C] contiguous; y NULL for the
+ * norm alone (then post = BSA_NORM_NONE, no gate).  stream_out (NULL without y) and normed
+ * (NULL with pre = BSA_NORM_NONE): written, `type`; they may be x or y themselves.
+ * stats: device fp32 [rows, 4] or NULL: mean and 1/sqrt(..) of the post norm, then of the
+ * pre norm (0 where there is none), for the backward.  The second norm is taken of the
+ * stream before its rounding to `type`.  Enqueues one kernel.
+ */
+int bsa_block_norm(const bsa_block_norm_args* args, const void* x, const void* y, void* stream_out, void* normed,
+                   float* stats, void* stream);
+
+/* bsa_block_norm_backward_workspace_bytes -- scratch of the backward (partial sums over rows). */
+int bsa_block_norm_backward_workspace_bytes(const bsa_block_norm_args* args, size_t* bytes);
+
+/*
+ * bsa_block_norm_backward -- gradients of a loss from dstream and dnormed, its gradients by
+ * the two outputs (either may be NULL for zero; dnormed is NULL without a pre norm):
+ *     D   = dstream + (gradient of dnormed through N_pre at the stream)
+ *     dx  = stream_scale D,  dy = (gradient of branch_scale gate D through N_post at y)
+ *     dgate = sum branch_scale D z over the rows that share a gate row, and the sums over
+ *     rows that make the gradients of weights and biases.
+ * x: the forward's stream (its x without y); y, stats: the forward's.  dx, and dy with y,
+ * are written, `type`, and may be dstream or dnormed themselves.  dpost_weight, dpost_bias,
+ * dgate, dpre_weight, dpre_bias: `param_type`, each NULL or written in full (only of a
+ * parameter that args has).  All sums are in fp32 in a fixed order.  workspace: 256-byte aligned, any contents.  Enqueues two
+ * kernels.
+ */
+int bsa_block_norm_backward(const bsa_block_norm_args* args, const void* dstream, const void* dnormed,
+                            const void* x, const void* y, const float* stats, void* dx, void* dy,
+                            void* dpost_weight, void* dpost_bias, void* dgate, void* dpre_weight,
+                            void* dpre_bias, void* workspace, size_t workspace_bytes, void* stream);
+
+/*
+ * bsa_fp8_quantize -- 8-bit codes of x with one scale for each block of 128, for
+ * bsa_fp8_matmul.  x: device, BSA_BF16, BSA_FP16 or BSA_FP32, [R, C] contiguous.
+ * code_type T: BSA_E4M3 or BSA_E5M2 with largest value top.  A block with largest
+ * magnitude m (taken as at least 2^-100) has
+ *     scale = m / top,   code = T(x (top / m)), rounded to nearest even,
+ * so x ~ code scale.  A block that holds a NaN or an infinity has a scale or codes that
+ * are not finite either.
+ *   rows form: codes [R, C] with row pitch ld (bytes, a multiple of 16, >= C), scale fp32
+ *     [R, ceil(C/128)]: a block is 128 consecutive columns of one row;
+ *   columns form: codes_t [C, R], pitch ld_t >= R, scale_t fp32 [C, ceil(R/128)]: the same of
+ *     x transposed, so a block is 128 rows of one column;
+ *   square != 0: blocks are 128 x 128: scale [ceil(R/128), ceil(C/128)], scale_t its
+ *     transpose, and codes_t the transpose of codes.
+ * A form whose codes are NULL is left out (not both).  A row's bytes from its end to the next
+ * multiple of 16 are written too (bsa_fp8_matmul does not read them).  One pass over x, one kernel.
+ */
+int bsa_fp8_quantize(const void* x, int type, int R, int C, int square, int code_type, void* codes, int64_t ld,
+                     float* scale, void* codes_t, int64_t ld_t, float* scale_t, void* stream);
+
+/* bsa_fp8_matmul_workspace_bytes -- scratch of bsa_fp8_matmul for these sizes on the current
+ * device (0 for most; partial sums where the depth K is split over SMs). */
+int bsa_fp8_matmul_workspace_bytes(int M, int N, int K, size_t* bytes);
+
+/*
+ * bsa_fp8_matmul -- product of two 8-bit matrices with a scale for each block of 128:
+ *     out[m, n] = sum_k a[m, k] sa[m, k/128] b[n, k] sb[n, k/128] + bias[n].
+ *   a, b      device, BSA_E4M3 or BSA_E5M2 each: [M, K] and [N, K], row pitches lda and ldb
+ *             (bytes, multiples of 16), 16-byte aligned.
+ *   a_scale   device fp32 [ceil(M / a_rows), ceil(K / 128)]: one scale for a_rows rows (1 or
+ *             128) by 128 columns; b_scale and b_rows the same for b.
+ *   bias      device, bias_type (BSA_BF16 or BSA_FP32), [N], or NULL.
+ *   out       device, out_type (BSA_BF16 or BSA_FP32), [M, N] contiguous.
+ * With y = x W^T this is a linear layer (a: x in rows form, b: W in square form), its
+ * input's gradient (a: dy in rows form, b: W's columns form) and its weight's (a: dy, b: x,
+ * both in columns form).  Each block's products are summed by the tensor cores, the blocks
+ * in fp32 with their scales, in a fixed order.  M or N of 0 is an empty call; K >= 1.
+ * workspace: as sized above, 256-byte aligned, any contents (NULL when 0).  Enqueues one
+ * kernel, two where K is split.  A device-side timeout is reported by bsa_sync_status.
+ */
+int bsa_fp8_matmul(const void* a, int a_type, int64_t lda, const float* a_scale, int a_rows, const void* b,
+                   int b_type, int64_t ldb, const float* b_scale, int b_rows, const void* bias, int bias_type,
+                   int M, int N, int K, void* out, int out_type, void* workspace, size_t workspace_bytes,
+                   void* stream);
+
 /*
  * bsa_sync_status -- synchronises `stream`, then returns and clears the
  * device-side status word of the current device: BSA_OK, or
