@@ -101,6 +101,22 @@ __device__ __forceinline__ void mma_f8(uint32_t d_tmem, uint64_t a_desc, uint64_
       : "memory");
 }
 
+// Waits that poll the barrier a while (a poll lets the thread sleep in hardware for a short
+// time) before they take the timed path, whose clock read and call cost more than a block's
+// MMAs.
+constexpr int kPolls = 64;
+template <int kRegion>
+__device__ __forceinline__ bool ready_warp(uint32_t bar, uint32_t parity, volatile int* abort_flag, uint64_t timeout_ns) {
+  for (int i = 0; i < kPolls; ++i)
+    if (__all_sync(0xffffffffu, ptx::mbar_try_wait(bar, parity))) return true;
+  return wait_warp<kRegion>(bar, parity, abort_flag, timeout_ns);
+}
+__device__ __forceinline__ bool ready_one(uint32_t bar, uint32_t parity, volatile int* abort_flag, uint64_t timeout_ns) {
+  for (int i = 0; i < kPolls; ++i)
+    if (ptx::mbar_try_wait(bar, parity)) return true;
+  return wait_one(bar, parity, abort_flag, timeout_ns);
+}
+
 // A unit of work: tile (m0, n0) over the blocks [k0, k1) of K.  Column tiles go fastest, so
 // that the CTAs of one moment share a few row tiles of A and all of B stays in L2.
 struct Unit {
@@ -129,7 +145,7 @@ __device__ void mma_producer(const MmaParams& p, uint32_t smem, uint32_t bars, v
     for (int kb = t.k0; kb < t.k1; ++kb, ++it) {
       const uint32_t s = it % C::kStages;
       if (it >= C::kStages &&
-          !wait_one(bar_at(bars, C::kEmpty + s), ((it / C::kStages) - 1u) & 1u, abort_flag, p.timeout_ns)) {
+          !ready_one(bar_at(bars, C::kEmpty + s), ((it / C::kStages) - 1u) & 1u, abort_flag, p.timeout_ns)) {
         alive = false;
         break;
       }
@@ -158,8 +174,8 @@ __device__ void mma_issuer(const MmaParams& p, uint32_t smem, uint32_t bars, uin
     for (int kb = t.k0; kb < t.k1; ++kb, ++it) {
       const uint32_t s = it % C::kStages, as = it % C::kAcc;
       if ((it >= C::kAcc &&
-           !wait_one(bar_at(bars, C::kAccEmpty + as), ((it / C::kAcc) - 1u) & 1u, abort_flag, p.timeout_ns)) ||
-          !wait_one(bar_at(bars, C::kFull + s), (it / C::kStages) & 1u, abort_flag, p.timeout_ns)) {
+           !ready_one(bar_at(bars, C::kAccEmpty + as), ((it / C::kAcc) - 1u) & 1u, abort_flag, p.timeout_ns)) ||
+          !ready_one(bar_at(bars, C::kFull + s), (it / C::kStages) & 1u, abort_flag, p.timeout_ns)) {
         alive = false;
         break;
       }
@@ -192,7 +208,7 @@ __device__ void scale_loader(const MmaParams& p, uint8_t* smem_gen, uint32_t bar
         v[i] = n < p.N ? __ldg(p.sb + static_cast<int64_t>(n) * p.kb + kb) : 0.f;
       }
       if (it >= C::kAcc &&
-          !wait_warp(bar_at(bars, C::kScEmpty + as), ((it / C::kAcc) - 1u) & 1u, abort_flag, p.timeout_ns))
+          !ready_warp<0>(bar_at(bars, C::kScEmpty + as), ((it / C::kAcc) - 1u) & 1u, abort_flag, p.timeout_ns))
         return;
       float* dst = reinterpret_cast<float*>(smem_gen + C::kScale) + as * kBN;
 #pragma unroll
@@ -221,34 +237,47 @@ __device__ void promoter(const MmaParams& p, uint8_t* smem_gen, uint32_t bars, u
     uint64_t acc[kCols / 2];
 #pragma unroll
     for (int i = 0; i < kCols / 2; ++i) acc[i] = 0ull;
+    // An accumulator is read in groups of 32 columns, the next group (of the next block after
+    // the last) on its way while one is added.
+    constexpr int kGroups = kCols / 32;
+    static_assert(kGroups % 2 == 0, "a block starts in the first buffer");
+    uint32_t r[2][32];
+    auto open = [&](uint32_t i) {  // waits for block i and starts reading its first group
+      const uint32_t as = i % C::kAcc, parity = (i / C::kAcc) & 1u;
+      if (kBRows && !ready_warp<1>(bar_at(bars, C::kScFull + as), parity, abort_flag, p.timeout_ns)) return false;
+      if (!ready_warp<1>(bar_at(bars, C::kAccFull + as), parity, abort_flag, p.timeout_ns)) return false;
+      ptx::tc_fence_after();
+      ptx::tmem_ld32(taddr + as * kBN, r[0]);
+      return true;
+    };
+    if (!open(it)) return;
     float next_a = __ldg(sa + t.k0), next_b = kBRows ? 1.f : __ldg(sb + t.k0);
     for (int kb = t.k0; kb < t.k1; ++kb, ++it) {
-      const uint32_t as = it % C::kAcc, parity = (it / C::kAcc) & 1u;
+      const uint32_t as = it % C::kAcc;
       const float s = kBRows ? next_a : next_a * next_b;
       if (kb + 1 < t.k1) {
         next_a = __ldg(sa + kb + 1);
         if (!kBRows) next_b = __ldg(sb + kb + 1);
       }
-      if (kBRows && !wait_warp<1>(bar_at(bars, C::kScFull + as), parity, abort_flag, p.timeout_ns)) return;
-      if (!wait_warp<1>(bar_at(bars, C::kAccFull + as), parity, abort_flag, p.timeout_ns)) return;
-      ptx::tc_fence_after();
       const uint64_t s2 = ptx::pack2(s, s);
       const float4* sc = reinterpret_cast<const float4*>(smem_gen + C::kScale) + as * (kBN / 4) + half * (kCols / 4);
 #pragma unroll
-      for (int g = 0; g < kCols / 32; ++g) {
-        uint32_t r[32];
-        ptx::tmem_ld32(taddr + as * kBN + 32u * g, r);
+      for (int g = 0; g < kGroups; ++g) {
         ptx::tmem_wait_ld();
-        ptx::reg_fence(r);
-        if (g == kCols / 32 - 1) {
+        ptx::reg_fence(r[g & 1]);
+        if (g + 1 < kGroups) {
+          ptx::tmem_ld32(taddr + as * kBN + 32u * (g + 1), r[(g + 1) & 1]);
+        } else {
           ptx::tc_fence_before();
           __syncwarp();
           if (lane == 0) ptx::mbar_arrive(bar_at(bars, C::kAccEmpty + as));
+          if (kb + 1 < t.k1 && !open(it + 1)) return;
         }
 #pragma unroll
         for (int j = 0; j < 32; j += 4) {
-          uint64_t lo = ptx::pack2(__uint_as_float(r[j]), __uint_as_float(r[j + 1]));
-          uint64_t hi = ptx::pack2(__uint_as_float(r[j + 2]), __uint_as_float(r[j + 3]));
+          const uint32_t(&x)[32] = r[g & 1];
+          uint64_t lo = ptx::pack2(__uint_as_float(x[j]), __uint_as_float(x[j + 1]));
+          uint64_t hi = ptx::pack2(__uint_as_float(x[j + 2]), __uint_as_float(x[j + 3]));
           if constexpr (kBRows) {
             const float4 b = sc[g * 8 + j / 4];
             lo = ptx::fmul2(lo, ptx::pack2(b.x, b.y));
