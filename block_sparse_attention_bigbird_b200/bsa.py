@@ -498,15 +498,22 @@ def _type_of(dtype) -> Optional[int]:
     return _type_codes.get(dtype)
 
 
+def _raw_stream(index: int) -> int:
+    """The current stream's pointer (without building a stream object, where torch allows)."""
+    import torch
+    raw = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+    return raw(index) if raw is not None else torch.cuda.current_stream(index).cuda_stream
+
+
 def _on(device, stream, call):
     """call(stream pointer) with the tensors' device current, and ``stream``, where one is
     given, the stream that call's allocations belong to."""
     import torch
     if stream is None and device.index == torch.cuda.current_device():
-        return call(torch.cuda.current_stream().cuda_stream)
+        return call(_raw_stream(device.index))
     with torch.cuda.device(device):
         if stream is None:
-            return call(torch.cuda.current_stream().cuda_stream)
+            return call(_raw_stream(device.index))
         if isinstance(stream, int):
             stream = torch.cuda.ExternalStream(stream, device=device)
         with torch.cuda.stream(stream):
@@ -606,18 +613,20 @@ def bsa_rope_apply(q, k, positions, rope: Rope, inverse: bool = False, q_out=Non
             positions.shape[-1] != L or (positions.dim() == 3 and positions.shape[1] != B):
         raise ValueError(f"positions must be int32, int64 or fp32 [axes, L] or [axes, B, L] with at least "
                          f"{rope.n_axes} axes")
-    _check_same(q.device, k=k, positions=positions, q_out=q_out, k_out=k_out)
+    device = q.device
+    if positions.device != device or (k is not None and k.device != device):
+        raise ValueError("q, k and positions must be on one device")
     for name, t, src in (("q_out", q_out, q), ("k_out", k_out, k)):
-        if t is not None and (src is None or t.dtype != q.dtype or t.shape != src.shape or
+        if t is not None and (src is None or t.dtype != q.dtype or t.shape != src.shape or t.device != device or
                               (d > 1 and t.stride(3) != 1) or
                               any(n > 1 and s == 0 for n, s in zip(t.shape, t.stride()))):
             raise ValueError(f"{name} must have its input's type and shape, contiguous columns and no shared rows")
 
     def call(ptr):
-        qo = torch.empty((B, H, L, d), dtype=q.dtype, device=q.device) if q_out is None else q_out
+        qo = q.new_empty((B, H, L, d)) if q_out is None else q_out
         ko = k_out
         if k is not None and k_out is None:
-            ko = torch.empty(k.shape, dtype=k.dtype, device=k.device)
+            ko = k.new_empty(k.shape)
         ks = (0,) * 6 if k is None else (*k.stride()[:3], *ko.stride()[:3])
         ps = positions.stride()
         _check(lib.bsa_rope_apply(q.data_ptr(), qo.data_ptr(), H, _ptr(k), _ptr(ko), 0 if k is None else k.shape[1],
@@ -643,26 +652,31 @@ def _norm_args(x, y, post, post_weight, post_bias, gate, branch_scale, stream_sc
     if y is None and (post is not None or gate is not None or pre is None or branch_scale != 1.0 or
                       stream_scale != 1.0):
         raise ValueError("without y there is the pre norm alone")
-    params = {"post_weight": post_weight, "post_bias": post_bias, "gate": gate, "pre_weight": pre_weight,
-              "pre_bias": pre_bias}
-    pt, gate_rows = None, 1
-    for name, t in params.items():
+    device, pt, gate_rows = x.device, None, 1
+    if y is not None and y.device != device:
+        raise ValueError("y is on another device than x")
+    for name, t in (("post_weight", post_weight), ("post_bias", post_bias), ("gate", gate),
+                    ("pre_weight", pre_weight), ("pre_bias", pre_bias)):
         if t is None:
             continue
         if pt is None:
-            pt = _type_of(t.dtype)
-        if _type_of(t.dtype) != pt or pt not in (ty, FP32) or not t.is_contiguous():
-            raise ValueError("parameters and gate must be contiguous and all of x's type or all fp32")
-        if name == "gate" and t.dim() == 2 and t.shape[1] == C and t.shape[0] in (1, B):
+            pt = t.dtype
+        if t.dtype is not pt or not t.is_contiguous() or t.device != device:
+            raise ValueError("parameters and gate must be contiguous, on x's device and of one type")
+        if t.dim() != 1 and name == "gate" and t.dim() == 2 and t.shape[0] in (1, B):
             gate_rows = t.shape[0]
-        elif tuple(t.shape) != (C,):
+        elif t.dim() != 1:
             raise ValueError(f"{name} must be [C]" + (" or [B, C]" if name == "gate" else ""))
+        if t.shape[-1] != C:
+            raise ValueError(f"{name} must have C columns")
+    pt = ty if pt is None else _type_of(pt)
+    if pt != ty and pt != FP32:
+        raise ValueError("parameters and gate must be all of x's type or all fp32")
     if (post is None and (post_weight is not None or post_bias is not None)) or \
             (pre is None and (pre_weight is not None or pre_bias is not None)):
         raise ValueError("a weight or bias needs its norm")
-    _check_same(x.device, y=y, **params)
     rows = x.numel() // C
-    a = BlockNormArgs(B, rows // B if B else 0, C, ty, ty if pt is None else pt, NORMS[post], NORMS[pre],
+    a = BlockNormArgs(B, rows // B if B else 0, C, ty, pt, NORMS[post], NORMS[pre],
                       _ptr(post_weight), _ptr(post_bias), _ptr(gate), _ptr(pre_weight), _ptr(pre_bias), gate_rows,
                       branch_scale, stream_scale, eps)
     return a, rows

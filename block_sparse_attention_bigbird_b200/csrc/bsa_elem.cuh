@@ -5,6 +5,9 @@
 
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
+#include <cuda_runtime.h>
+
+#include <atomic>
 
 #include <cstdint>
 
@@ -42,18 +45,23 @@ __device__ __forceinline__ uint32_t pack(float lo, float hi, __half) {
   return *reinterpret_cast<const uint32_t*>(&v);
 }
 
-// kVec consecutive elements; kVec = 8 needs a 16-byte aligned address.
+// kVec consecutive elements; kVec = 8 needs a 16-byte aligned address, 2 one of two elements.
 template <int kVec, typename T>
 struct Elems {
   static __device__ __forceinline__ void load(const T* p, float (&v)[kVec]) {
     if constexpr (kVec == 1) {
       v[0] = to_f32(*p);
+    } else if constexpr (kVec == 2 && sizeof(T) == 4) {
+      const float2 a = *reinterpret_cast<const float2*>(p);
+      v[0] = a.x, v[1] = a.y;
+    } else if constexpr (kVec == 2) {
+      unpack(*reinterpret_cast<const uint32_t*>(p), T(), v[0], v[1]);
     } else if constexpr (sizeof(T) == 4) {
-      static_assert(kVec == 8, "one or eight elements");
+      static_assert(kVec == 8, "one, two or eight elements");
       const float4 a = reinterpret_cast<const float4*>(p)[0], b = reinterpret_cast<const float4*>(p)[1];
       v[0] = a.x, v[1] = a.y, v[2] = a.z, v[3] = a.w, v[4] = b.x, v[5] = b.y, v[6] = b.z, v[7] = b.w;
     } else {
-      static_assert(kVec == 8, "one or eight elements");
+      static_assert(kVec == 8, "one, two or eight elements");
       const uint4 a = *reinterpret_cast<const uint4*>(p);
       unpack(a.x, T(), v[0], v[1]);
       unpack(a.y, T(), v[2], v[3]);
@@ -64,6 +72,10 @@ struct Elems {
   static __device__ __forceinline__ void store(T* p, const float (&v)[kVec]) {
     if constexpr (kVec == 1) {
       *p = from_f32<T>(v[0]);
+    } else if constexpr (kVec == 2 && sizeof(T) == 4) {
+      *reinterpret_cast<float2*>(p) = make_float2(v[0], v[1]);
+    } else if constexpr (kVec == 2) {
+      *reinterpret_cast<uint32_t*>(p) = pack(v[0], v[1], T());
     } else if constexpr (sizeof(T) == 4) {
       reinterpret_cast<float4*>(p)[0] = make_float4(v[0], v[1], v[2], v[3]);
       reinterpret_cast<float4*>(p)[1] = make_float4(v[4], v[5], v[6], v[7]);
@@ -77,5 +89,25 @@ struct Elems {
 inline bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
 inline size_t type_bytes(int type) { return type == BSA_FP32 ? 4 : 2; }  // of bf16, fp16, fp32
 inline bool is_float_type(int type) { return type == BSA_BF16 || type == BSA_FP16 || type == BSA_FP32; }
+
+// SMs of the current device, or a negative bsa_status where it is no sm_100 part.  Asked
+// once per device; a failed query is not kept.
+inline int sm_count() {
+  constexpr int kMost = 64;
+  static std::atomic<int> known[kMost];
+  int dev = -1;
+  if (cudaGetDevice(&dev) != cudaSuccess) return BSA_ERR_CUDA;
+  if (dev < 0 || dev >= kMost) return BSA_ERR_UNSUPPORTED;
+  const int k = known[dev].load(std::memory_order_relaxed);
+  if (k != 0) return k;
+  int major = 0, minor = 0, sms = 0;
+  if (cudaDeviceGetAttribute(&major, cudaDevAttrComputeCapabilityMajor, dev) != cudaSuccess ||
+      cudaDeviceGetAttribute(&minor, cudaDevAttrComputeCapabilityMinor, dev) != cudaSuccess ||
+      cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess)
+    return BSA_ERR_CUDA;
+  const int got = major == 10 && minor == 0 ? sms : static_cast<int>(BSA_ERR_UNSUPPORTED);
+  known[dev].store(got, std::memory_order_relaxed);
+  return got;
+}
 
 }  // namespace bsa

@@ -5,9 +5,12 @@
 //
 // and the gradients of both outputs.  N is rms or layer normalisation over a row's C columns.
 //
-// Forward.  A row is held in the registers of one team of threads (a warp up to 1024
-// columns, else the block), so that x and y are read once and both outputs written once;
-// means, variances (of the centred values) and the residual are fp32 in registers.
+// A row belongs to one team of threads (a warp while a lane's share of it is small, else the
+// block), every thread owning fixed columns, so that each array is read and written once and
+// means, variances (of the centred values), sums and the residual are fp32 in registers.
+// Blocks are persistent.  A thread brings its own pieces of the rows to come into shared
+// memory with cp.async, up to three rows ahead, and reads back only what it brought, so that
+// no barrier is needed and the loads in flight do not depend on the warps that fit.
 //
 // Backward, with D the gradient of the stream by both its uses:
 //     a  = dnormed w_pre,  D = dstream + r (a - mean(a) - xh mean(a xh)),   dx = beta D,
@@ -50,6 +53,7 @@ struct NormParams {
   int params_f32;    // parameters are fp32 (else the activations' type)
   float alpha, beta, eps, inv_c;
   int64_t rows_per_block;
+  int depth;  // slots of the ring, 1 to 3
 };
 
 template <typename T, int kVec>
@@ -120,99 +124,169 @@ __device__ __forceinline__ float2 normalise(float (&v)[kE], int kind, int valid,
   return make_float2(mean, r);
 }
 
+// Rows on their way to this thread: kNA arrays, kNV pieces of kVec elements of each, `depth`
+// slots.  Pieces of two bytes (an odd row of 16-bit elements) are copied at once instead.
+template <typename T, int kVec, int kNV, int kNA>
+struct Ring {
+  static constexpr int kBytes = kVec * static_cast<int>(sizeof(T));
+  static constexpr int kPiece = kBytes > 16 ? 16 : kBytes;
+  uint8_t* mine;  // this thread's first piece; pieces of a thread are kPiece * blockDim.x apart
+  const T* src[kNA];
+  int C, team_threads, t, depth;
+  __device__ __forceinline__ uint8_t* at(int slot, int a, int i, int h) const {
+    return mine + ((((slot * kNA + a) * kNV + i) * (kBytes / kPiece) + h) * blockDim.x) * kPiece;
+  }
+  // starts bringing row `row` (nothing past the last) into `slot`, as one group
+  __device__ __forceinline__ void fetch(int slot, int64_t row, int64_t rows) {
+    if (row < rows) {
+#pragma unroll
+      for (int a = 0; a < kNA; ++a) {
+        if (src[a] == nullptr) continue;
+#pragma unroll
+        for (int i = 0; i < kNV; ++i) {
+          const int c = (i * team_threads + t) * kVec;
+          if (c >= C) continue;
+          const T* p = src[a] + row * C + c;
+          if constexpr (kBytes < 4) {
+            *reinterpret_cast<T*>(at(slot, a, i, 0)) = *p;
+          } else {
+#pragma unroll
+            for (int h = 0; h < kBytes / kPiece; ++h) {
+              const uint32_t dst = static_cast<uint32_t>(__cvta_generic_to_shared(at(slot, a, i, h)));
+              const uint8_t* from = reinterpret_cast<const uint8_t*>(p) + h * kPiece;
+              if constexpr (kPiece == 16)
+                asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(from) : "memory");
+              else
+                asm volatile("cp.async.ca.shared.global [%0], [%1], %2;" ::"r"(dst), "l"(from), "n"(kPiece) : "memory");
+            }
+          }
+        }
+      }
+    }
+    asm volatile("cp.async.commit_group;" ::: "memory");
+  }
+  // all but the newest depth - 1 groups have landed
+  __device__ __forceinline__ void wait() const {
+    if (depth == 3) asm volatile("cp.async.wait_group 2;" ::: "memory");
+    else if (depth == 2) asm volatile("cp.async.wait_group 1;" ::: "memory");
+    else asm volatile("cp.async.wait_group 0;" ::: "memory");
+  }
+  // this thread's elements of array a; 0 past the row's end and of an array that is not there
+  __device__ __forceinline__ void read(int slot, int a, float (&v)[kVec * kNV]) const {
+#pragma unroll
+    for (int i = 0; i < kNV; ++i) {
+      float e[kVec] = {};
+      if (src[a] != nullptr && (i * team_threads + t) * kVec < C) {
+        if constexpr (kBytes <= 16) {
+          Elems<kVec, T>::load(reinterpret_cast<const T*>(at(slot, a, i, 0)), e);
+        } else {
+          const float4 lo = *reinterpret_cast<const float4*>(at(slot, a, i, 0));
+          const float4 hi = *reinterpret_cast<const float4*>(at(slot, a, i, 1));
+          e[0] = lo.x, e[1] = lo.y, e[2] = lo.z, e[3] = lo.w, e[4] = hi.x, e[5] = hi.y, e[6] = hi.z, e[7] = hi.w;
+        }
+      }
+#pragma unroll
+      for (int j = 0; j < kVec; ++j) v[i * kVec + j] = e[j];
+    }
+  }
+};
+
 // Thread t of a team owns the columns (i * team + t) * kVec .. + kVec of its row, i < kNV.
 template <typename T, int kVec, int kNV, bool kWarpTeam>
-__global__ void __launch_bounds__(kWarpTeam ? 128 : 512) bsa_block_norm_kernel(const __grid_constant__ NormParams p) {
+__global__ void __launch_bounds__(kWarpTeam ? 128 : 512) bsa_block_norm_kernel(const __grid_constant__ NormParams p,
+                                                                               int team_threads) {
   constexpr int kE = kVec * kNV;
-  __shared__ float red[2 * 32];
-  const int team_threads = kWarpTeam ? 32 : blockDim.x;
-  const int t = threadIdx.x % team_threads;
-  TeamSum<1, kWarpTeam> sum{red, team_threads, 1};
-  const int64_t row = kWarpTeam ? static_cast<int64_t>(blockIdx.x) * (blockDim.x >> 5) + (threadIdx.x >> 5)
-                                : static_cast<int64_t>(blockIdx.x);
-  if (row >= p.rows) return;  // whole teams
-  const int64_t at = row * p.C;
+  extern __shared__ __align__(16) uint8_t smem[];  // the reduction areas, then the ring
+  const int teams = blockDim.x / team_threads, team = threadIdx.x / team_threads, t = threadIdx.x % team_threads;
+  TeamSum<1, kWarpTeam> sum{reinterpret_cast<float*>(smem) + team * 64, team_threads, 1 + team};
+  Ring<T, kVec, kNV, 2> ring;
+  ring.mine = smem + teams * 256 + threadIdx.x * ring.kPiece;
+  ring.src[0] = static_cast<const T*>(p.x), ring.src[1] = static_cast<const T*>(p.y);
+  ring.C = p.C, ring.team_threads = team_threads, ring.t = t, ring.depth = p.depth;
+  const int64_t step = static_cast<int64_t>(gridDim.x) * teams;
+  int64_t row = static_cast<int64_t>(blockIdx.x) * teams + team;
+  int slot = 0, next = p.depth - 1;
+  for (int d = 0; d + 1 < p.depth; ++d) ring.fetch(d, row + d * step, p.rows);
   int valid = 0;  // elements of this thread inside the row
 #pragma unroll
   for (int i = 0; i < kNV; ++i)
     if ((i * team_threads + t) * kVec < p.C) valid = (i + 1) * kVec;
-  float st[kE];
+  const bool f32 = p.params_f32 != 0;
+  for (; row < p.rows; row += step) {
+    ring.fetch(next, row + (p.depth - 1) * step, p.rows);
+    ring.wait();
+    const int64_t at = row * p.C;
+    float st[kE];
+    ring.read(slot, 0, st);
+    float2 post = make_float2(0.f, 0.f), pre = make_float2(0.f, 0.f);
+    if (p.y != nullptr) {
+      float y[kE];
+      ring.read(slot, 1, y);
+      if (p.post != BSA_NORM_NONE) post = normalise<kE, kWarpTeam>(y, p.post, valid, p, sum);
+      const int64_t g0 = row / p.per_gate * p.C;
+      const void* gate = p.gate == nullptr ? nullptr
+                         : f32             ? static_cast<const void*>(static_cast<const float*>(p.gate) + g0)
+                                           : static_cast<const void*>(static_cast<const T*>(p.gate) + g0);
 #pragma unroll
-  for (int i = 0; i < kNV; ++i) {
-    const int c = (i * team_threads + t) * kVec;
-    float v[kVec] = {};
-    if (c < p.C) Elems<kVec, T>::load(static_cast<const T*>(p.x) + at + c, v);
+      for (int i = 0; i < kNV; ++i) {
+        const int c = (i * team_threads + t) * kVec;
+        if (c >= p.C) continue;
+        float w[kVec], b[kVec], g[kVec], o[kVec];
+        load_param<T, kVec>(p.post_w, c, f32, 1.f, w);
+        load_param<T, kVec>(p.post_b, c, f32, 0.f, b);
+        load_param<T, kVec>(gate, c, f32, 1.f, g);
 #pragma unroll
-    for (int j = 0; j < kVec; ++j) st[i * kVec + j] = v[j];
-  }
-  float2 post = make_float2(0.f, 0.f), pre = make_float2(0.f, 0.f);
-  if (p.y != nullptr) {
-    float y[kE];
-#pragma unroll
-    for (int i = 0; i < kNV; ++i) {
-      const int c = (i * team_threads + t) * kVec;
-      float v[kVec] = {};
-      if (c < p.C) Elems<kVec, T>::load(static_cast<const T*>(p.y) + at + c, v);
-#pragma unroll
-      for (int j = 0; j < kVec; ++j) y[i * kVec + j] = v[j];
-    }
-    if (p.post != BSA_NORM_NONE) post = normalise<kE, kWarpTeam>(y, p.post, valid, p, sum);
-    const int64_t g0 = row / p.per_gate * p.C;
-    const bool f32 = p.params_f32 != 0;
-    const void* gate = p.gate == nullptr ? nullptr
-                       : f32             ? static_cast<const void*>(static_cast<const float*>(p.gate) + g0)
-                                         : static_cast<const void*>(static_cast<const T*>(p.gate) + g0);
-#pragma unroll
-    for (int i = 0; i < kNV; ++i) {
-      const int c = (i * team_threads + t) * kVec;
-      if (c >= p.C) continue;
-      float w[kVec], b[kVec], g[kVec], o[kVec];
-      load_param<T, kVec>(p.post_w, c, f32, 1.f, w);
-      load_param<T, kVec>(p.post_b, c, f32, 0.f, b);
-      load_param<T, kVec>(gate, c, f32, 1.f, g);
-#pragma unroll
-      for (int j = 0; j < kVec; ++j) {
-        const float z = fmaf(y[i * kVec + j], w[j], b[j]);
-        o[j] = st[i * kVec + j] = fmaf(p.alpha * g[j], z, p.beta * st[i * kVec + j]);
+        for (int j = 0; j < kVec; ++j) {
+          const float z = fmaf(y[i * kVec + j], w[j], b[j]);
+          o[j] = st[i * kVec + j] = fmaf(p.alpha * g[j], z, p.beta * st[i * kVec + j]);
+        }
+        Elems<kVec, T>::store(static_cast<T*>(p.out) + at + c, o);
       }
-      Elems<kVec, T>::store(static_cast<T*>(p.out) + at + c, o);
     }
-  }
-  if (p.pre != BSA_NORM_NONE) {
-    pre = normalise<kE, kWarpTeam>(st, p.pre, valid, p, sum);
-    const bool f32 = p.params_f32 != 0;
+    if (p.pre != BSA_NORM_NONE) {
+      pre = normalise<kE, kWarpTeam>(st, p.pre, valid, p, sum);
 #pragma unroll
-    for (int i = 0; i < kNV; ++i) {
-      const int c = (i * team_threads + t) * kVec;
-      if (c >= p.C) continue;
-      float w[kVec], b[kVec], o[kVec];
-      load_param<T, kVec>(p.pre_w, c, f32, 1.f, w);
-      load_param<T, kVec>(p.pre_b, c, f32, 0.f, b);
+      for (int i = 0; i < kNV; ++i) {
+        const int c = (i * team_threads + t) * kVec;
+        if (c >= p.C) continue;
+        float w[kVec], b[kVec], o[kVec];
+        load_param<T, kVec>(p.pre_w, c, f32, 1.f, w);
+        load_param<T, kVec>(p.pre_b, c, f32, 0.f, b);
 #pragma unroll
-      for (int j = 0; j < kVec; ++j) o[j] = fmaf(st[i * kVec + j], w[j], b[j]);
-      Elems<kVec, T>::store(static_cast<T*>(p.normed) + at + c, o);
+        for (int j = 0; j < kVec; ++j) o[j] = fmaf(st[i * kVec + j], w[j], b[j]);
+        Elems<kVec, T>::store(static_cast<T*>(p.normed) + at + c, o);
+      }
     }
+    if (p.stats != nullptr && t == 0)
+      reinterpret_cast<float4*>(p.stats)[row] = make_float4(post.x, post.y, pre.x, pre.y);
+    slot = slot + 1 == p.depth ? 0 : slot + 1;
+    next = next + 1 == p.depth ? 0 : next + 1;
   }
-  if (p.stats != nullptr && t == 0)
-    reinterpret_cast<float4*>(p.stats)[row] = make_float4(post.x, post.y, pre.x, pre.y);
 }
 
-// kMeans: a layer norm takes part (the plain means, T and Q are kept).
+// kMeans: a layer norm takes part or biases have gradients (the plain means, T and Q are kept).
 template <typename T, int kVec, int kNV, bool kWarpTeam, bool kMeans>
-__global__ void __launch_bounds__(kWarpTeam ? 256 : 512) bsa_block_norm_back_kernel(const __grid_constant__ NormParams p,
+__global__ void __launch_bounds__(kWarpTeam ? 128 : 512) bsa_block_norm_back_kernel(const __grid_constant__ NormParams p,
                                                                                     int team_threads) {
   constexpr int kE = kVec * kNV;
   constexpr int kN = kMeans ? 2 : 1;
-  extern __shared__ float smem[];  // [C] sums of the block's teams, then the teams' reduction areas
-  const int team = threadIdx.x / team_threads, teams = blockDim.x / team_threads;
-  const int t = threadIdx.x % team_threads;
-  TeamSum<kN, kWarpTeam> sum{smem + p.C + team * (2 * kN * 32), team_threads, 1 + team};
+  extern __shared__ __align__(16) uint8_t smem[];  // [C] sums, the teams' reduction areas, the ring
+  float* sums = reinterpret_cast<float*>(smem);
+  const int teams = blockDim.x / team_threads, team = threadIdx.x / team_threads, t = threadIdx.x % team_threads;
+  const int cols = (p.C + 3) / 4 * 4;
+  TeamSum<kN, kWarpTeam> sum{sums + cols + team * (2 * kN * 32), team_threads, 1 + team};
+  Ring<T, kVec, kNV, 4> ring;
+  ring.mine = smem + (cols + teams * 2 * kN * 32) * sizeof(float) + threadIdx.x * ring.kPiece;
+  ring.src[0] = static_cast<const T*>(p.dstream), ring.src[1] = static_cast<const T*>(p.y);
+  ring.src[2] = p.dnormed == nullptr ? nullptr : static_cast<const T*>(p.x);
+  ring.src[3] = static_cast<const T*>(p.dnormed);
+  ring.C = p.C, ring.team_threads = team_threads, ring.t = t, ring.depth = p.depth;
   const int64_t r0 = static_cast<int64_t>(blockIdx.x) * p.rows_per_block;
   const int64_t r1 = min(r0 + p.rows_per_block, p.rows);
   const bool f32 = p.params_f32 != 0;
   const bool pre_layer = p.pre == BSA_NORM_LAYER, post_layer = p.post == BSA_NORM_LAYER;
 
-  float accP[kE] = {}, accQ[kMeans ? kE : 1] = {};
+  float accP[kE] = {}, accQ[kMeans ? kE : 1] = {}, accS[kE] = {}, accT[kMeans ? kE : 1] = {};
   // adds the teams' v in shared memory and writes it to C floats at `to`
   auto flush = [&](const float* v, float* to) {
     for (int k = 0; k < teams; ++k) {
@@ -222,15 +296,19 @@ __global__ void __launch_bounds__(kWarpTeam ? 256 : 512) bsa_block_norm_back_ker
           const int c = (i * team_threads + t) * kVec;
           if (c < p.C)
 #pragma unroll
-            for (int j = 0; j < kVec; ++j) smem[c + j] = k == 0 ? v[i * kVec + j] : smem[c + j] + v[i * kVec + j];
+            for (int j = 0; j < kVec; ++j) sums[c + j] = k == 0 ? v[i * kVec + j] : sums[c + j] + v[i * kVec + j];
         }
       }
       __syncthreads();
     }
-    for (int c = threadIdx.x; c < p.C; c += blockDim.x) to[c] = smem[c];
+    for (int c = threadIdx.x; c < p.C; c += blockDim.x) to[c] = sums[c];
     __syncthreads();
   };
-
+  // The block's rows go round its teams; a team's rows are one sequence for the ring, cut
+  // where the gate row changes.
+  int64_t row = r0 + team;
+  int slot = 0, next = p.depth - 1;
+  for (int d = 0; d + 1 < p.depth; ++d) ring.fetch(d, row + d * teams, r1);
   for (int64_t s0 = r0; s0 < r1;) {
     const int64_t gate_row = s0 / p.per_gate;
     const int64_t s1 = min(r1, (gate_row + 1) * p.per_gate);
@@ -238,49 +316,29 @@ __global__ void __launch_bounds__(kWarpTeam ? 256 : 512) bsa_block_norm_back_ker
     const void* gate = p.gate == nullptr ? nullptr
                        : f32             ? static_cast<const void*>(static_cast<const float*>(p.gate) + g0)
                                          : static_cast<const void*>(static_cast<const T*>(p.gate) + g0);
-    float accS[kE] = {}, accT[kMeans ? kE : 1] = {};
-    for (int64_t row = s0 + team; row < s1; row += teams) {
-      const int64_t at = row * p.C;
+    for (; row < s1; row += teams) {
+      ring.fetch(next, row + (p.depth - 1) * teams, r1);
       const float4 st = reinterpret_cast<const float4*>(p.saved)[row];
+      ring.wait();
+      const int64_t at = row * p.C;
       float D[kE];
-#pragma unroll
-      for (int i = 0; i < kNV; ++i) {
-        const int c = (i * team_threads + t) * kVec;
-        float v[kVec] = {};
-        if (p.dstream != nullptr && c < p.C) Elems<kVec, T>::load(static_cast<const T*>(p.dstream) + at + c, v);
-#pragma unroll
-        for (int j = 0; j < kVec; ++j) D[i * kVec + j] = v[j];
-      }
-      float yh[kE];
-      if (p.y != nullptr) {
-#pragma unroll
-        for (int i = 0; i < kNV; ++i) {
-          const int c = (i * team_threads + t) * kVec;
-          float v[kVec] = {};
-          if (c < p.C) Elems<kVec, T>::load(static_cast<const T*>(p.y) + at + c, v);
-#pragma unroll
-          for (int j = 0; j < kVec; ++j)
-            yh[i * kVec + j] = p.post == BSA_NORM_NONE ? v[j] : c < p.C ? (v[j] - st.x) * st.y : 0.f;
-        }
-      }
+      ring.read(slot, 0, D);
       if (p.dnormed != nullptr) {
         float a[kE], xh[kE], m[kN] = {};
+        ring.read(slot, 2, xh);
+        ring.read(slot, 3, a);
 #pragma unroll
         for (int i = 0; i < kNV; ++i) {
           const int c = (i * team_threads + t) * kVec;
-          float v[kVec] = {}, d[kVec] = {}, w[kVec] = {};
-          if (c < p.C) {
-            Elems<kVec, T>::load(static_cast<const T*>(p.x) + at + c, v);
-            Elems<kVec, T>::load(static_cast<const T*>(p.dnormed) + at + c, d);
-            load_param<T, kVec>(p.pre_w, c, f32, 1.f, w);
-          }
+          float w[kVec] = {};
+          if (c < p.C) load_param<T, kVec>(p.pre_w, c, f32, 1.f, w);
 #pragma unroll
           for (int j = 0; j < kVec; ++j) {
             const int e = i * kVec + j;
-            xh[e] = c < p.C ? (v[j] - st.z) * st.w : 0.f;
-            accP[e] = fmaf(d[j], xh[e], accP[e]);
-            if constexpr (kMeans) accQ[e] += d[j];
-            a[e] = d[j] * w[j];
+            xh[e] = c < p.C ? (xh[e] - st.z) * st.w : 0.f;
+            accP[e] = fmaf(a[e], xh[e], accP[e]);
+            if constexpr (kMeans) accQ[e] += a[e];
+            a[e] *= w[j];
             m[0] = fmaf(a[e], xh[e], m[0]);
             if constexpr (kMeans) m[1] += a[e];
           }
@@ -300,48 +358,60 @@ __global__ void __launch_bounds__(kWarpTeam ? 256 : 512) bsa_block_norm_back_ker
         for (int j = 0; j < kVec; ++j) o[j] = p.beta * D[i * kVec + j];
         if (c < p.C) Elems<kVec, T>::store(static_cast<T*>(p.dx) + at + c, o);
       }
-      if (p.y == nullptr) continue;
-      float m[kN] = {};
+      if (p.y != nullptr) {
+        float yh[kE], m[kN] = {};
+        ring.read(slot, 1, yh);
 #pragma unroll
-      for (int i = 0; i < kNV; ++i) {
-        const int c = (i * team_threads + t) * kVec;
-        float w[kVec] = {}, g[kVec] = {};
-        if (c < p.C) {
-          load_param<T, kVec>(p.post_w, c, f32, 1.f, w);
-          load_param<T, kVec>(gate, c, f32, 1.f, g);
-        }
-#pragma unroll
-        for (int j = 0; j < kVec; ++j) {
-          const int e = i * kVec + j;
+        for (int i = 0; i < kNV; ++i) {
+          const int c = (i * team_threads + t) * kVec;
+          float w[kVec] = {}, g[kVec] = {};
           if (c < p.C) {
+            load_param<T, kVec>(p.post_w, c, f32, 1.f, w);
+            load_param<T, kVec>(gate, c, f32, 1.f, g);
+          }
+#pragma unroll
+          for (int j = 0; j < kVec; ++j) {
+            const int e = i * kVec + j;
+            if (c >= p.C) {
+              D[e] = yh[e] = 0.f;
+            } else if (p.post != BSA_NORM_NONE) {
+              yh[e] = (yh[e] - st.x) * st.y;
+            }
             accS[e] = fmaf(D[e], yh[e], accS[e]);
             if constexpr (kMeans) accT[e] += D[e];
+            D[e] *= p.alpha * g[j] * w[j];
+            m[0] = fmaf(D[e], yh[e], m[0]);
+            if constexpr (kMeans) m[1] += D[e];
           }
-          D[e] = c < p.C ? p.alpha * g[j] * w[j] * D[e] : 0.f;
-          m[0] = fmaf(D[e], yh[e], m[0]);
-          if constexpr (kMeans) m[1] += D[e];
+        }
+        float c1 = 0.f, c2 = 0.f, r = 1.f;
+        if (p.post != BSA_NORM_NONE) {
+          sum(m);
+          c1 = m[0] * p.inv_c;
+          if constexpr (kMeans) c2 = post_layer ? m[1] * p.inv_c : 0.f;
+          r = st.y;
+        }
+#pragma unroll
+        for (int i = 0; i < kNV; ++i) {
+          const int c = (i * team_threads + t) * kVec;
+          float o[kVec];
+#pragma unroll
+          for (int j = 0; j < kVec; ++j) o[j] = r * (D[i * kVec + j] - c2 - yh[i * kVec + j] * c1);
+          if (c < p.C) Elems<kVec, T>::store(static_cast<T*>(p.dy) + at + c, o);
         }
       }
-      float c1 = 0.f, c2 = 0.f, r = 1.f;
-      if (p.post != BSA_NORM_NONE) {
-        sum(m);
-        c1 = m[0] * p.inv_c;
-        if constexpr (kMeans) c2 = post_layer ? m[1] * p.inv_c : 0.f;
-        r = st.y;
-      }
-#pragma unroll
-      for (int i = 0; i < kNV; ++i) {
-        const int c = (i * team_threads + t) * kVec;
-        float o[kVec];
-#pragma unroll
-        for (int j = 0; j < kVec; ++j) o[j] = r * (D[i * kVec + j] - c2 - yh[i * kVec + j] * c1);
-        if (c < p.C) Elems<kVec, T>::store(static_cast<T*>(p.dy) + at + c, o);
-      }
+      slot = slot + 1 == p.depth ? 0 : slot + 1;
+      next = next + 1 == p.depth ? 0 : next + 1;
     }
     if (p.part != nullptr && p.y != nullptr) {
       float* to = p.part + (blockIdx.x + gate_row) * kN * p.C;
       flush(accS, to);
       if constexpr (kMeans) flush(accT, to + p.C);
+#pragma unroll
+      for (int e = 0; e < kE; ++e) accS[e] = 0.f;
+      if constexpr (kMeans)
+#pragma unroll
+        for (int e = 0; e < kE; ++e) accT[e] = 0.f;
     }
     s0 = s1;
   }
@@ -448,28 +518,42 @@ __global__ void __launch_bounds__(1024) bsa_block_norm_sum_kernel(const SumParam
 }
 
 // ------------------------------------------------------------ host
-// How a row is laid over threads.  Vectors of eight where every row starts at 16 bytes.
+// How a row is laid over threads and blocks over SMs.
 struct Team {
-  bool vec;
-  int nv, threads;  // vectors (or elements) a thread, threads a team
+  int vec, nv;           // elements a piece, pieces a thread
+  int threads, teams;    // threads a team, teams a block
+  int depth, per_sm;     // slots of the ring, blocks on an SM
+  size_t smem;
+  bool warp() const { return threads == 32; }
 };
 
-Team team_of(int C, bool vec, bool backward, bool means) {
-  Team t{vec, 1, 32};
-  const int n = vec ? C / 8 : C;
-  if (vec) {
-    // a warp takes a row while a lane's share fits its registers (the backward with layer
-    // norms keeps four sums a column), else the fewest vectors a thread that 512 threads allow
-    const int most = backward ? (means ? 1 : 3) : 4;
-    if (n <= 32 * most) {
-      t.nv = (n + 31) / 32;
-      return t;
-    }
-    t.nv = n <= 512 ? 1 : 2;
+// arrays: how many the ring brings; sums: [C] floats and kN areas a team (backward).
+Team team_of(int C, size_t esize, bool aligned, bool backward, bool means) {
+  Team t{};
+  t.vec = aligned && C % 8 == 0 ? 8 : aligned && C % 2 == 0 ? 2 : 1;
+  const int n = C / t.vec;
+  // A warp takes a row while a lane's share fits its registers (the backward keeps two sums
+  // a column, four with plain means), else the fewest pieces a thread that 512 threads allow.
+  const int most = t.vec < 8 ? 0 : !backward ? 4 : means ? 2 : 3;
+  if (n <= 32 * most) {
+    t.nv = (n + 31) / 32;
+    t.threads = 32;
+    t.teams = 4;
   } else {
-    t.nv = n <= 4 * 512 ? 4 : 16;
+    t.nv = t.vec == 8 ? (n <= 512 ? 1 : 2) : t.vec == 2 ? (n <= 2048 ? 4 : 8) : (n <= 4096 ? 8 : 16);
+    t.threads = ((n + t.nv - 1) / t.nv + 31) / 32 * 32;
+    t.teams = std::max(1, 256 / t.threads);
   }
-  t.threads = ((n + t.nv - 1) / t.nv + 31) / 32 * 32;
+  const int block = t.threads * t.teams, nq = means ? 2 : 1;
+  const size_t fixed = backward ? ((C + 3) / 4 * 4 + t.teams * 2 * nq * 32) * sizeof(float) : t.teams * 256;
+  const size_t slot = static_cast<size_t>(block) * (backward ? 4 : 2) * t.nv * t.vec * esize;
+  // blocks on an SM that the registers allow: about 128 a thread, 255 for the backward's warps
+  const int by_regs = std::max(1, (backward && t.warp() ? 256 : 512) / block);
+  t.depth = 3;
+  t.per_sm = by_regs;
+  while (t.depth > 1 && (fixed + t.depth * slot + 1024) * t.per_sm > 220 * 1024) --t.depth;
+  while (t.per_sm > 1 && (fixed + t.depth * slot + 1024) * t.per_sm > 220 * 1024) --t.per_sm;
+  t.smem = fixed + t.depth * slot;
   return t;
 }
 
@@ -513,36 +597,46 @@ void fill(NormParams& p, const bsa_block_norm_args& a) {
   p.inv_c = 1.f / static_cast<float>(a.C);
 }
 
+template <typename F>
+bool start(F* kernel, const NormParams& p, const Team& t, int64_t blocks, cudaStream_t s) {
+  // past 48 KB the size has to be allowed first; the call is cheap and needs no state here
+  if (t.smem > 48 * 1024 &&
+      cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(t.smem)) != cudaSuccess)
+    return false;
+  kernel<<<static_cast<unsigned>(blocks), t.threads * t.teams, t.smem, s>>>(p, t.threads);
+  return true;
+}
+
 template <typename T>
-void launch_norm(const NormParams& p, const Team& t, cudaStream_t s) {
-  if (t.vec && t.threads == 32) {
-    const unsigned grid = static_cast<unsigned>((p.rows + 3) / 4);
-    if (t.nv == 1) bsa_block_norm_kernel<T, 8, 1, true><<<grid, 128, 0, s>>>(p);
-    else if (t.nv == 2) bsa_block_norm_kernel<T, 8, 2, true><<<grid, 128, 0, s>>>(p);
-    else if (t.nv == 3) bsa_block_norm_kernel<T, 8, 3, true><<<grid, 128, 0, s>>>(p);
-    else bsa_block_norm_kernel<T, 8, 4, true><<<grid, 128, 0, s>>>(p);
-    return;
+bool launch_norm(NormParams p, const Team& t, int sms, cudaStream_t s) {
+  p.depth = t.depth;
+  const int64_t blocks = std::min<int64_t>((p.rows + t.teams - 1) / t.teams, static_cast<int64_t>(sms) * t.per_sm);
+  if (t.warp()) {
+    if (t.nv == 1) return start(bsa_block_norm_kernel<T, 8, 1, true>, p, t, blocks, s);
+    if (t.nv == 2) return start(bsa_block_norm_kernel<T, 8, 2, true>, p, t, blocks, s);
+    if (t.nv == 3) return start(bsa_block_norm_kernel<T, 8, 3, true>, p, t, blocks, s);
+    return start(bsa_block_norm_kernel<T, 8, 4, true>, p, t, blocks, s);
   }
-  const unsigned grid = static_cast<unsigned>(p.rows);
-  if (t.vec && t.nv == 1) bsa_block_norm_kernel<T, 8, 1, false><<<grid, t.threads, 0, s>>>(p);
-  else if (t.vec) bsa_block_norm_kernel<T, 8, 2, false><<<grid, t.threads, 0, s>>>(p);
-  else if (t.nv == 4) bsa_block_norm_kernel<T, 1, 4, false><<<grid, t.threads, 0, s>>>(p);
-  else bsa_block_norm_kernel<T, 1, 16, false><<<grid, t.threads, 0, s>>>(p);
+  if (t.vec == 8)
+    return t.nv == 1 ? start(bsa_block_norm_kernel<T, 8, 1, false>, p, t, blocks, s)
+                     : start(bsa_block_norm_kernel<T, 8, 2, false>, p, t, blocks, s);
+  if (t.vec == 2)
+    return t.nv == 4 ? start(bsa_block_norm_kernel<T, 2, 4, false>, p, t, blocks, s)
+                     : start(bsa_block_norm_kernel<T, 2, 8, false>, p, t, blocks, s);
+  return t.nv == 8 ? start(bsa_block_norm_kernel<T, 1, 8, false>, p, t, blocks, s)
+                   : start(bsa_block_norm_kernel<T, 1, 16, false>, p, t, blocks, s);
 }
 
 struct BackPlan {
-  int teams;  // a block
   int64_t blocks, rows_per_block, slots;
   size_t bytes;
 };
 
-// Blocks of about 256 threads, two for each of 148 SMs' places, at least one row a team.
-BackPlan back_plan(const NormParams& p, const Team& t, int gate_rows, bool means) {
+// Contiguous rows for each block, at least one a team.
+BackPlan back_plan(const NormParams& p, const Team& t, int gate_rows, bool means, int sms) {
   BackPlan b;
-  b.teams = std::max(1, 256 / t.threads);
-  const int64_t want = t.threads > 256 ? 148 * 1 : 148 * 2;
-  const int64_t most = std::max<int64_t>(1, (p.rows + b.teams - 1) / b.teams);
-  b.blocks = std::min(want, most);
+  const int64_t most = std::max<int64_t>(1, (p.rows + t.teams - 1) / t.teams);
+  b.blocks = std::min<int64_t>(static_cast<int64_t>(sms) * t.per_sm, most);
   b.rows_per_block = std::max<int64_t>(1, (p.rows + b.blocks - 1) / b.blocks);
   b.blocks = (p.rows + b.rows_per_block - 1) / b.rows_per_block;
   b.slots = b.blocks + gate_rows;
@@ -551,22 +645,21 @@ BackPlan back_plan(const NormParams& p, const Team& t, int gate_rows, bool means
 }
 
 template <typename T, bool kMeans>
-void launch_back(const NormParams& p, const Team& t, const BackPlan& b, cudaStream_t s) {
-  const unsigned grid = static_cast<unsigned>(b.blocks);
-  const int threads = b.teams * t.threads;
-  const size_t smem = (p.C + b.teams * 2 * (kMeans ? 2 : 1) * 32) * sizeof(float);
-  if (t.vec && t.threads == 32) {
-    if (t.nv == 1) bsa_block_norm_back_kernel<T, 8, 1, true, kMeans><<<grid, threads, smem, s>>>(p, 32);
-    else if constexpr (!kMeans) {
-      if (t.nv == 2) bsa_block_norm_back_kernel<T, 8, 2, true, kMeans><<<grid, threads, smem, s>>>(p, 32);
-      else bsa_block_norm_back_kernel<T, 8, 3, true, kMeans><<<grid, threads, smem, s>>>(p, 32);
-    }
-    return;
+bool launch_back(const NormParams& p, const Team& t, const BackPlan& b, cudaStream_t s) {
+  if (t.warp()) {
+    if (t.nv == 1) return start(bsa_block_norm_back_kernel<T, 8, 1, true, kMeans>, p, t, b.blocks, s);
+    if constexpr (!kMeans)
+      if (t.nv == 3) return start(bsa_block_norm_back_kernel<T, 8, 3, true, kMeans>, p, t, b.blocks, s);
+    return start(bsa_block_norm_back_kernel<T, 8, 2, true, kMeans>, p, t, b.blocks, s);
   }
-  if (t.vec && t.nv == 1) bsa_block_norm_back_kernel<T, 8, 1, false, kMeans><<<grid, threads, smem, s>>>(p, t.threads);
-  else if (t.vec) bsa_block_norm_back_kernel<T, 8, 2, false, kMeans><<<grid, threads, smem, s>>>(p, t.threads);
-  else if (t.nv == 4) bsa_block_norm_back_kernel<T, 1, 4, false, kMeans><<<grid, threads, smem, s>>>(p, t.threads);
-  else bsa_block_norm_back_kernel<T, 1, 16, false, kMeans><<<grid, threads, smem, s>>>(p, t.threads);
+  if (t.vec == 8)
+    return t.nv == 1 ? start(bsa_block_norm_back_kernel<T, 8, 1, false, kMeans>, p, t, b.blocks, s)
+                     : start(bsa_block_norm_back_kernel<T, 8, 2, false, kMeans>, p, t, b.blocks, s);
+  if (t.vec == 2)
+    return t.nv == 4 ? start(bsa_block_norm_back_kernel<T, 2, 4, false, kMeans>, p, t, b.blocks, s)
+                     : start(bsa_block_norm_back_kernel<T, 2, 8, false, kMeans>, p, t, b.blocks, s);
+  return t.nv == 8 ? start(bsa_block_norm_back_kernel<T, 1, 8, false, kMeans>, p, t, b.blocks, s)
+                   : start(bsa_block_norm_back_kernel<T, 1, 16, false, kMeans>, p, t, b.blocks, s);
 }
 
 bool takes_means(const bsa_block_norm_args& a) { return a.post == BSA_NORM_LAYER || a.pre == BSA_NORM_LAYER; }
@@ -597,15 +690,17 @@ int bsa_block_norm(const bsa_block_norm_args* args, const void* x, const void* y
   if (p.rows > 0x7fffffff || misaligned(a.type, {x, y, stream_out, normed}) ||
       (stats != nullptr && !aligned16(stats)))
     return BSA_ERR_INVALID_ARG;
-  const bool vec = a.C % 8 == 0 && all_aligned({x, y, stream_out, normed, a.post_weight, a.post_bias, a.gate,
-                                                a.pre_weight, a.pre_bias});
+  const int sms = sm_count();
+  if (sms < 0) return sms;
+  const bool aligned = all_aligned({x, y, stream_out, normed, a.post_weight, a.post_bias, a.gate, a.pre_weight,
+                                    a.pre_bias});
   p.x = x, p.y = y, p.out = stream_out, p.normed = normed, p.stats = stats;
-  const Team t = team_of(a.C, vec, false, takes_means(a));
+  const Team t = team_of(a.C, type_bytes(a.type), aligned, false, takes_means(a));
   cudaStream_t s = static_cast<cudaStream_t>(stream);
-  if (a.type == BSA_BF16) launch_norm<__nv_bfloat16>(p, t, s);
-  else if (a.type == BSA_FP16) launch_norm<__half>(p, t, s);
-  else launch_norm<float>(p, t, s);
-  return cudaGetLastError() == cudaSuccess ? BSA_OK : BSA_ERR_CUDA;
+  const bool ok = a.type == BSA_BF16   ? launch_norm<__nv_bfloat16>(p, t, sms, s)
+                  : a.type == BSA_FP16 ? launch_norm<__half>(p, t, sms, s)
+                                       : launch_norm<float>(p, t, sms, s);
+  return cudaGetLastError() == cudaSuccess && ok ? BSA_OK : BSA_ERR_CUDA;
 }
 
 int bsa_block_norm_backward_workspace_bytes(const bsa_block_norm_args* args, size_t* bytes) {
@@ -614,11 +709,14 @@ int bsa_block_norm_backward_workspace_bytes(const bsa_block_norm_args* args, siz
   if (bytes == nullptr) return BSA_ERR_INVALID_ARG;
   NormParams p{};
   fill(p, *args);
+  const int sms = sm_count();
+  if (sms < 0) return sms;
   // the larger of both layouts: which one runs depends on the alignment of the call
+  const bool means = keeps_means(*args);
   size_t most = 0;
-  for (const bool vec : {false, true})
-    most = std::max(most, back_plan(p, team_of(args->C, vec && args->C % 8 == 0, true, keeps_means(*args)),
-                                    args->gate_rows, keeps_means(*args)).bytes);
+  for (const bool aligned : {false, true})
+    most = std::max(most, back_plan(p, team_of(args->C, type_bytes(args->type), aligned, true, means),
+                                    args->gate_rows, means, sms).bytes);
   *bytes = (most + 255) / 256 * 256;
   return BSA_OK;
 }
@@ -650,9 +748,11 @@ int bsa_block_norm_backward(const bsa_block_norm_args* args, const void* dstream
   }
   if (misaligned(a.param_type, {dpost_weight, dpost_bias, dgate, dpre_weight, dpre_bias})) return BSA_ERR_INVALID_ARG;
   const bool means = keeps_means(a);
-  const bool vec = a.C % 8 == 0 && all_aligned({x, y, dstream, dnormed, dx, dy, a.post_weight, a.gate, a.pre_weight});
-  const Team t = team_of(a.C, vec, true, means);
-  const BackPlan b = back_plan(p, t, a.gate_rows, means);
+  const int sms = sm_count();
+  if (sms < 0) return sms;
+  const bool aligned = all_aligned({x, y, dstream, dnormed, dx, dy, a.post_weight, a.gate, a.pre_weight});
+  const Team t = team_of(a.C, type_bytes(a.type), aligned, true, means);
+  const BackPlan b = back_plan(p, t, a.gate_rows, means, sms);
   if (sums && (workspace == nullptr || reinterpret_cast<uintptr_t>(workspace) % 256 != 0 || workspace_bytes < b.bytes))
     return BSA_ERR_WORKSPACE;
   p.x = x, p.y = y, p.dstream = dstream, p.dnormed = dnormed, p.saved = stats, p.dx = dx, p.dy = dy;
@@ -660,10 +760,15 @@ int bsa_block_norm_backward(const bsa_block_norm_args* args, const void* dstream
   p.part_pre = sums ? p.part + b.slots * (means ? 2 : 1) * a.C : nullptr;
   p.rows_per_block = b.rows_per_block;
   cudaStream_t s = static_cast<cudaStream_t>(stream);
+  p.depth = t.depth;
+  bool ok = true;
   if (p.rows > 0) {
-    if (a.type == BSA_BF16) means ? launch_back<__nv_bfloat16, true>(p, t, b, s) : launch_back<__nv_bfloat16, false>(p, t, b, s);
-    else if (a.type == BSA_FP16) means ? launch_back<__half, true>(p, t, b, s) : launch_back<__half, false>(p, t, b, s);
-    else means ? launch_back<float, true>(p, t, b, s) : launch_back<float, false>(p, t, b, s);
+    if (a.type == BSA_BF16)
+      ok = means ? launch_back<__nv_bfloat16, true>(p, t, b, s) : launch_back<__nv_bfloat16, false>(p, t, b, s);
+    else if (a.type == BSA_FP16)
+      ok = means ? launch_back<__half, true>(p, t, b, s) : launch_back<__half, false>(p, t, b, s);
+    else
+      ok = means ? launch_back<float, true>(p, t, b, s) : launch_back<float, false>(p, t, b, s);
   }
   if (sums) {
     SumParams q{};
@@ -680,7 +785,7 @@ int bsa_block_norm_backward(const bsa_block_norm_args* args, const void* dstream
     q.lanes_per_gate = lanes;
     bsa_block_norm_sum_kernel<<<(a.C + 31) / 32, dim3(32, 32), 0, s>>>(q);
   }
-  return cudaGetLastError() == cudaSuccess ? BSA_OK : BSA_ERR_CUDA;
+  return cudaGetLastError() == cudaSuccess && ok ? BSA_OK : BSA_ERR_CUDA;
 }
 
 }  // extern "C"

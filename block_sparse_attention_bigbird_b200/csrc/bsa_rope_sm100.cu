@@ -12,8 +12,9 @@
 // What bounds it: q and k are read and written once; the arithmetic is 3 operations an
 // element.  The sines are the costly part (about 60 instructions a pair), so a thread keeps
 // the angles of eight pairs of one token and walks over heads with them.  It reads the
-// pairs' two halves as two 16-byte vectors.  The heads are cut into groups (blockIdx.y)
-// only as far as it takes to fill the SMs: with one token a call, one head a thread.
+// pairs' two halves as two 16-byte vectors.  The heads are cut into groups (blockIdx.y) of
+// at least four until the card is filled eight times over, so that the last wave is short;
+// with one token a call a thread takes one head.
 #include <cuda_runtime.h>
 
 #include <algorithm>
@@ -141,8 +142,10 @@ void launch_rope(const RopeParams& p, bool vec, bool adj, dim3 grid, cudaStream_
   }
 }
 
-// Threads that fill the card once (148 SMs x 2048): heads are cut into groups up to here.
+// Threads that fill the card (148 SMs x 2048) once, up to where heads are cut singly, and
+// eight times, up to where they are cut into groups of four or more.
 constexpr int64_t kRopeFill = 148 * 2048;
+constexpr int64_t kRopeGroup = 4;
 
 }  // namespace
 }  // namespace bsa
@@ -235,7 +238,7 @@ int bsa_rope_apply(const void* q, void* q_out, int H, const void* k, void* k_out
     return BSA_ERR_INVALID_ARG;
   RopeParams p;
   const size_t es = type_bytes(type);
-  bool vec = d % 8 == 0 && (rope->adjacent ? pairs % 8 == 0 : pairs % 8 == 0);
+  bool vec = d % 8 == 0 && pairs % 8 == 0;
   bool in_place = true;
   p.in[0] = q, p.in[1] = k, p.out[0] = q_out, p.out[1] = k_out;
   p.heads[0] = H, p.heads[1] = Hk;
@@ -258,6 +261,8 @@ int bsa_rope_apply(const void* q, void* q_out, int H, const void* k, void* k_out
     vec = vec && (bits % 16 == 0) && (any % 16 == 0);
     in_place = in_place && p.in[w] == p.out[w];
   }
+  const int sms = sm_count();
+  if (sms < 0) return sms;
   for (int j = 0; j < pairs; ++j) {
     p.turns[j] = rope->freq[j] / 6.283185307179586476925286766559;
     p.axis[j] = static_cast<uint8_t>(rope->axis[j]);
@@ -274,7 +279,8 @@ int bsa_rope_apply(const void* q, void* q_out, int H, const void* k, void* k_out
   const int64_t blocks = (threads + kRopeThreads - 1) / kRopeThreads;
   const int64_t heads = H + static_cast<int64_t>(Hk);
   if (blocks > 0x7fffffff || heads > 65535) return BSA_ERR_INVALID_ARG;
-  const int64_t groups = std::min<int64_t>(heads, std::max<int64_t>(1, kRopeFill / std::max<int64_t>(1, threads)));
+  const int64_t once = kRopeFill / threads, often = std::min(8 * kRopeFill / threads, (heads + kRopeGroup - 1) / kRopeGroup);
+  const int64_t groups = std::min<int64_t>(heads, std::max<int64_t>({1, once, often}));
   p.group = static_cast<int>((heads + groups - 1) / groups);
   const dim3 grid(static_cast<unsigned>(blocks), static_cast<unsigned>((heads + p.group - 1) / p.group));
   cudaStream_t s = static_cast<cudaStream_t>(stream);
