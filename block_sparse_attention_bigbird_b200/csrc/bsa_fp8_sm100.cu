@@ -332,14 +332,20 @@ __device__ void promoter(const MmaParams& p, uint8_t* smem_gen, uint32_t bars, u
       float v[32];
 #pragma unroll
       for (int j = 0; j < 16; ++j) ptx::unpack2(acc[g * 16 + j], v[2 * j], v[2 * j + 1]);
-      if (p.bias != nullptr) {
+      if (p.bias != nullptr) {  // a lane loads one column's, all read them from shared memory
+        const int n = col0 + 32 * g + lane;
+        float b = 0.f;
+        if (n < p.N)
+          b = p.bias_f32 ? __ldg(static_cast<const float*>(p.bias) + n)
+                         : __bfloat162float(static_cast<const __nv_bfloat16*>(p.bias)[n]);
+        reinterpret_cast<float*>(stg)[lane] = b;
+        __syncwarp();
 #pragma unroll
-        for (int j = 0; j < 32; ++j) {
-          const int n = col0 + 32 * g + j;
-          if (n < p.N)
-            v[j] += p.bias_f32 ? __ldg(static_cast<const float*>(p.bias) + n)
-                               : __bfloat162float(static_cast<const __nv_bfloat16*>(p.bias)[n]);
+        for (int j = 0; j < 32; j += 4) {
+          const float4 b4 = reinterpret_cast<const float4*>(stg)[j / 4];
+          v[j] += b4.x, v[j + 1] += b4.y, v[j + 2] += b4.z, v[j + 3] += b4.w;
         }
+        __syncwarp();
       }
       uint8_t* mine = stg + lane * 64;
       const int x = (lane >> 1) & 3;

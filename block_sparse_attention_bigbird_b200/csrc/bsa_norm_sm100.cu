@@ -10,7 +10,10 @@
 // means, variances (of the centred values), sums and the residual are fp32 in registers.
 // Blocks are persistent.  A thread brings its own pieces of the rows to come into shared
 // memory with cp.async, up to three rows ahead, and reads back only what it brought, so that
-// no barrier is needed and the loads in flight do not depend on the warps that fit.
+// no barrier is needed and the loads in flight do not depend on the warps that fit.  What a
+// column multiplies by (weights, gate, the scales) stays in registers from row to row, and the
+// arithmetic is done on pairs (fma.rn.f32x2): with both the instructions a row stay well
+// below what the SM issues in the time its bytes take.
 //
 // Backward, with D the gradient of the stream by both its uses:
 //     a  = dnormed w_pre,  D = dstream + r (a - mean(a) - xh mean(a xh)),   dx = beta D,
@@ -33,6 +36,7 @@
 #include <initializer_list>
 
 #include "bsa_elem.cuh"
+#include "sm100_ptx.cuh"
 
 namespace bsa {
 namespace {
@@ -56,17 +60,67 @@ struct NormParams {
   int depth;  // slots of the ring, 1 to 3
 };
 
-template <typename T, int kVec>
-__device__ __forceinline__ void load_param(const void* p, int c, bool f32, float dflt, float (&v)[kVec]) {
-  if (p == nullptr) {
+// This thread's elements of a row as pairs: element kVec i + j of piece i, two by two.
+template <int kE>
+struct Pairs {
+  uint64_t v[kE / 2];
+  __device__ __forceinline__ void set(const float (&x)[kE]) {
 #pragma unroll
-    for (int i = 0; i < kVec; ++i) v[i] = dflt;
-  } else if (f32) {
-    Elems<kVec, float>::load(static_cast<const float*>(p) + c, v);
-  } else {
-    Elems<kVec, T>::load(static_cast<const T*>(p) + c, v);
+    for (int e = 0; e < kE / 2; ++e) v[e] = ptx::pack2(x[2 * e], x[2 * e + 1]);
   }
+  __device__ __forceinline__ void get(float (&x)[kE]) const {
+#pragma unroll
+    for (int e = 0; e < kE / 2; ++e) ptx::unpack2(v[e], x[2 * e], x[2 * e + 1]);
+  }
+};
+__device__ __forceinline__ uint64_t twice(float x) { return ptx::pack2(x, x); }
+__device__ __forceinline__ float sum2(uint64_t x) {
+  float a, b;
+  ptx::unpack2(x, a, b);
+  return a + b;
 }
+
+// A thread's columns of a row of C: pieces of kVec, kNV of them.
+template <int kVec, int kNV>
+struct Cols {
+  static constexpr int kE = kVec * kNV;
+  int C, team_threads, t;
+  __device__ __forceinline__ int at(int i) const { return (i * team_threads + t) * kVec; }
+  // a parameter's values at these columns (`dflt` where it is absent), 0 past the row's end
+  template <typename T>
+  __device__ __forceinline__ void param(const void* p, int64_t row, bool f32, float dflt, float (&v)[kE]) const {
+#pragma unroll
+    for (int i = 0; i < kNV; ++i) {
+      const int c = at(i);
+      float e[kVec];
+#pragma unroll
+      for (int j = 0; j < kVec; ++j) e[j] = c < C ? dflt : 0.f;
+      if (p != nullptr && c < C) {
+        if (f32) Elems<kVec, float>::load(static_cast<const float*>(p) + row * C + c, e);
+        else Elems<kVec, T>::load(static_cast<const T*>(p) + row * C + c, e);
+      }
+#pragma unroll
+      for (int j = 0; j < kVec; ++j) v[i * kVec + j] = e[j];
+    }
+  }
+  template <typename T>
+  __device__ __forceinline__ void store(T* row, const Pairs<kE>& x) const {
+    float v[kE];
+    x.get(v);
+#pragma unroll
+    for (int i = 0; i < kNV; ++i) {
+      float e[kVec];
+#pragma unroll
+      for (int j = 0; j < kVec; ++j) e[j] = v[i * kVec + j];
+      if (at(i) < C) Elems<kVec, T>::store(row + at(i), e);
+    }
+  }
+  // x where a piece is inside the row, else 0
+  __device__ __forceinline__ uint64_t inside(int e, float x) const {
+    const float a = at(2 * e / kVec) < C ? x : 0.f, b = at((2 * e + 1) / kVec) < C ? x : 0.f;
+    return ptx::pack2(a, b);
+  }
+};
 
 // Sums of kN values over a team; every thread of the team gets them.  A team of a whole
 // block meets in shared memory, in one of two areas taken in turn so that one barrier a
@@ -99,29 +153,29 @@ struct TeamSum {
   }
 };
 
-// Normalises v (in place) over the team's row: rms or layer; returns (mean, 1 / sqrt(..)).
-template <int kE, bool kWarpTeam>
-__device__ __forceinline__ float2 normalise(float (&v)[kE], int kind, int valid, const NormParams& p,
-                                            TeamSum<1, kWarpTeam>& sum) {
-  float mean = 0.f;
-  float s[1];
+// (mean, 1 / sqrt(mean square of the centred values + eps)) of a row over the team; with a
+// layer norm v is centred.  Past the row's end v holds 0 and keeps it.
+template <int kVec, int kNV, bool kWarpTeam>
+__device__ __forceinline__ float2 statistics(Pairs<kVec * kNV>& v, int kind, const Cols<kVec, kNV>& cols,
+                                             const NormParams& p, TeamSum<1, kWarpTeam>& sum) {
+  constexpr int kP = kVec * kNV / 2;
+  float mean = 0.f, s[1];
   if (kind == BSA_NORM_LAYER) {
-    s[0] = 0.f;
+    uint64_t a = 0ull;
 #pragma unroll
-    for (int i = 0; i < kE; ++i) s[0] += v[i];  // columns past C hold 0
+    for (int e = 0; e < kP; ++e) a = ptx::fadd2(a, v.v[e]);
+    s[0] = sum2(a);
     sum(s);
     mean = s[0] * p.inv_c;
 #pragma unroll
-    for (int i = 0; i < kE; ++i) v[i] = i < valid ? v[i] - mean : 0.f;
+    for (int e = 0; e < kP; ++e) v.v[e] = ptx::fadd2(v.v[e], cols.inside(e, -mean));
   }
-  s[0] = 0.f;
+  uint64_t a = 0ull;
 #pragma unroll
-  for (int i = 0; i < kE; ++i) s[0] = fmaf(v[i], v[i], s[0]);
+  for (int e = 0; e < kP; ++e) a = ptx::ffma2(v.v[e], v.v[e], a);
+  s[0] = sum2(a);
   sum(s);
-  const float r = 1.f / sqrtf(fmaf(s[0], p.inv_c, p.eps));
-#pragma unroll
-  for (int i = 0; i < kE; ++i) v[i] *= r;
-  return make_float2(mean, r);
+  return make_float2(mean, 1.f / sqrtf(fmaf(s[0], p.inv_c, p.eps)));
 }
 
 // Rows on their way to this thread: kNA arrays, kNV pieces of kVec elements of each, `depth`
@@ -172,7 +226,8 @@ struct Ring {
     else asm volatile("cp.async.wait_group 0;" ::: "memory");
   }
   // this thread's elements of array a; 0 past the row's end and of an array that is not there
-  __device__ __forceinline__ void read(int slot, int a, float (&v)[kVec * kNV]) const {
+  __device__ __forceinline__ void read(int slot, int a, Pairs<kVec * kNV>& to) const {
+    float v[kVec * kNV];
 #pragma unroll
     for (int i = 0; i < kNV; ++i) {
       float e[kVec] = {};
@@ -188,17 +243,18 @@ struct Ring {
 #pragma unroll
       for (int j = 0; j < kVec; ++j) v[i * kVec + j] = e[j];
     }
+    to.set(v);
   }
 };
 
-// Thread t of a team owns the columns (i * team + t) * kVec .. + kVec of its row, i < kNV.
 template <typename T, int kVec, int kNV, bool kWarpTeam>
-__global__ void __launch_bounds__(kWarpTeam ? 128 : 512) bsa_block_norm_kernel(const __grid_constant__ NormParams p,
+__global__ void __launch_bounds__(kWarpTeam ? 128 : 512, kWarpTeam ? 4 : 1) bsa_block_norm_kernel(const __grid_constant__ NormParams p,
                                                                                int team_threads) {
-  constexpr int kE = kVec * kNV;
+  constexpr int kE = kVec * kNV, kP = kE / 2;
   extern __shared__ __align__(16) uint8_t smem[];  // the reduction areas, then the ring
   const int teams = blockDim.x / team_threads, team = threadIdx.x / team_threads, t = threadIdx.x % team_threads;
   TeamSum<1, kWarpTeam> sum{reinterpret_cast<float*>(smem) + team * 64, team_threads, 1 + team};
+  const Cols<kVec, kNV> cols{p.C, team_threads, t};
   Ring<T, kVec, kNV, 2> ring;
   ring.mine = smem + teams * 256 + threadIdx.x * ring.kPiece;
   ring.src[0] = static_cast<const T*>(p.x), ring.src[1] = static_cast<const T*>(p.y);
@@ -207,55 +263,69 @@ __global__ void __launch_bounds__(kWarpTeam ? 128 : 512) bsa_block_norm_kernel(c
   int64_t row = static_cast<int64_t>(blockIdx.x) * teams + team;
   int slot = 0, next = p.depth - 1;
   for (int d = 0; d + 1 < p.depth; ++d) ring.fetch(d, row + d * step, p.rows);
-  int valid = 0;  // elements of this thread inside the row
-#pragma unroll
-  for (int i = 0; i < kNV; ++i)
-    if ((i * team_threads + t) * kVec < p.C) valid = (i + 1) * kVec;
   const bool f32 = p.params_f32 != 0;
+  Pairs<kE> wpre, coef;  // pre weight; branch_scale gate post_weight of the gate row at hand
+  {
+    float w[kE];
+    cols.template param<T>(p.pre_w, 0, f32, 1.f, w);
+    wpre.set(w);
+  }
+  int64_t gate_end = row;  // rows from here on have another gate row than coef's
   for (; row < p.rows; row += step) {
     ring.fetch(next, row + (p.depth - 1) * step, p.rows);
+    const int64_t gate_row = row >= gate_end ? static_cast<uint32_t>(row) / static_cast<uint32_t>(p.per_gate) : 0;
+    if (p.y != nullptr && row >= gate_end) {
+      gate_end = (gate_row + 1) * p.per_gate;
+      float w[kE], g[kE];
+      cols.template param<T>(p.post_w, 0, f32, 1.f, w);
+      cols.template param<T>(p.gate, gate_row, f32, 1.f, g);
+#pragma unroll
+      for (int e = 0; e < kE; ++e) w[e] *= p.alpha * g[e];
+      coef.set(w);
+    }
     ring.wait();
-    const int64_t at = row * p.C;
-    float st[kE];
+    Pairs<kE> st;
     ring.read(slot, 0, st);
     float2 post = make_float2(0.f, 0.f), pre = make_float2(0.f, 0.f);
     if (p.y != nullptr) {
-      float y[kE];
+      Pairs<kE> y;
       ring.read(slot, 1, y);
-      if (p.post != BSA_NORM_NONE) post = normalise<kE, kWarpTeam>(y, p.post, valid, p, sum);
-      const int64_t g0 = row / p.per_gate * p.C;
-      const void* gate = p.gate == nullptr ? nullptr
-                         : f32             ? static_cast<const void*>(static_cast<const float*>(p.gate) + g0)
-                                           : static_cast<const void*>(static_cast<const T*>(p.gate) + g0);
-#pragma unroll
-      for (int i = 0; i < kNV; ++i) {
-        const int c = (i * team_threads + t) * kVec;
-        if (c >= p.C) continue;
-        float w[kVec], b[kVec], g[kVec], o[kVec];
-        load_param<T, kVec>(p.post_w, c, f32, 1.f, w);
-        load_param<T, kVec>(p.post_b, c, f32, 0.f, b);
-        load_param<T, kVec>(gate, c, f32, 1.f, g);
-#pragma unroll
-        for (int j = 0; j < kVec; ++j) {
-          const float z = fmaf(y[i * kVec + j], w[j], b[j]);
-          o[j] = st[i * kVec + j] = fmaf(p.alpha * g[j], z, p.beta * st[i * kVec + j]);
-        }
-        Elems<kVec, T>::store(static_cast<T*>(p.out) + at + c, o);
+      float r = 1.f;
+      if (p.post != BSA_NORM_NONE) {
+        post = statistics<kVec, kNV, kWarpTeam>(y, p.post, cols, p, sum);
+        r = post.y;
       }
+      const uint64_t r2 = twice(r), beta = twice(p.beta);
+#pragma unroll
+      for (int e = 0; e < kP; ++e)
+        st.v[e] = ptx::ffma2(ptx::fmul2(y.v[e], r2), coef.v[e], ptx::fmul2(st.v[e], beta));
+      if (p.post_b != nullptr) {
+        float b[kE], g[kE];
+        Pairs<kE> add;
+        cols.template param<T>(p.post_b, 0, f32, 0.f, b);
+        cols.template param<T>(p.gate, static_cast<uint32_t>(row) / static_cast<uint32_t>(p.per_gate), f32, 1.f, g);
+#pragma unroll
+        for (int e = 0; e < kE; ++e) b[e] *= p.alpha * g[e];
+        add.set(b);
+#pragma unroll
+        for (int e = 0; e < kP; ++e) st.v[e] = ptx::fadd2(st.v[e], add.v[e]);
+      }
+      cols.store(static_cast<T*>(p.out) + row * p.C, st);
     }
     if (p.pre != BSA_NORM_NONE) {
-      pre = normalise<kE, kWarpTeam>(st, p.pre, valid, p, sum);
+      pre = statistics<kVec, kNV, kWarpTeam>(st, p.pre, cols, p, sum);
+      const uint64_t r2 = twice(pre.y);
 #pragma unroll
-      for (int i = 0; i < kNV; ++i) {
-        const int c = (i * team_threads + t) * kVec;
-        if (c >= p.C) continue;
-        float w[kVec], b[kVec], o[kVec];
-        load_param<T, kVec>(p.pre_w, c, f32, 1.f, w);
-        load_param<T, kVec>(p.pre_b, c, f32, 0.f, b);
+      for (int e = 0; e < kP; ++e) st.v[e] = ptx::fmul2(ptx::fmul2(st.v[e], r2), wpre.v[e]);
+      if (p.pre_b != nullptr) {
+        float b[kE];
+        Pairs<kE> add;
+        cols.template param<T>(p.pre_b, 0, f32, 0.f, b);
+        add.set(b);
 #pragma unroll
-        for (int j = 0; j < kVec; ++j) o[j] = fmaf(st[i * kVec + j], w[j], b[j]);
-        Elems<kVec, T>::store(static_cast<T*>(p.normed) + at + c, o);
+        for (int e = 0; e < kP; ++e) st.v[e] = ptx::fadd2(st.v[e], add.v[e]);
       }
+      cols.store(static_cast<T*>(p.normed) + row * p.C, st);
     }
     if (p.stats != nullptr && t == 0)
       reinterpret_cast<float4*>(p.stats)[row] = make_float4(post.x, post.y, pre.x, pre.y);
@@ -266,17 +336,18 @@ __global__ void __launch_bounds__(kWarpTeam ? 128 : 512) bsa_block_norm_kernel(c
 
 // kMeans: a layer norm takes part or biases have gradients (the plain means, T and Q are kept).
 template <typename T, int kVec, int kNV, bool kWarpTeam, bool kMeans>
-__global__ void __launch_bounds__(kWarpTeam ? 128 : 512) bsa_block_norm_back_kernel(const __grid_constant__ NormParams p,
+__global__ void __launch_bounds__(kWarpTeam ? 128 : 512, kWarpTeam ? 2 : 1) bsa_block_norm_back_kernel(const __grid_constant__ NormParams p,
                                                                                     int team_threads) {
-  constexpr int kE = kVec * kNV;
+  constexpr int kE = kVec * kNV, kP = kE / 2;
   constexpr int kN = kMeans ? 2 : 1;
   extern __shared__ __align__(16) uint8_t smem[];  // [C] sums, the teams' reduction areas, the ring
   float* sums = reinterpret_cast<float*>(smem);
   const int teams = blockDim.x / team_threads, team = threadIdx.x / team_threads, t = threadIdx.x % team_threads;
-  const int cols = (p.C + 3) / 4 * 4;
-  TeamSum<kN, kWarpTeam> sum{sums + cols + team * (2 * kN * 32), team_threads, 1 + team};
+  const int cpad = (p.C + 3) / 4 * 4;
+  TeamSum<kN, kWarpTeam> sum{sums + cpad + team * (2 * kN * 32), team_threads, 1 + team};
+  const Cols<kVec, kNV> cols{p.C, team_threads, t};
   Ring<T, kVec, kNV, 4> ring;
-  ring.mine = smem + (cols + teams * 2 * kN * 32) * sizeof(float) + threadIdx.x * ring.kPiece;
+  ring.mine = smem + (cpad + teams * 2 * kN * 32) * sizeof(float) + threadIdx.x * ring.kPiece;
   ring.src[0] = static_cast<const T*>(p.dstream), ring.src[1] = static_cast<const T*>(p.y);
   ring.src[2] = p.dnormed == nullptr ? nullptr : static_cast<const T*>(p.x);
   ring.src[3] = static_cast<const T*>(p.dnormed);
@@ -286,14 +357,22 @@ __global__ void __launch_bounds__(kWarpTeam ? 128 : 512) bsa_block_norm_back_ker
   const bool f32 = p.params_f32 != 0;
   const bool pre_layer = p.pre == BSA_NORM_LAYER, post_layer = p.post == BSA_NORM_LAYER;
 
-  float accP[kE] = {}, accQ[kMeans ? kE : 1] = {}, accS[kE] = {}, accT[kMeans ? kE : 1] = {};
-  // adds the teams' v in shared memory and writes it to C floats at `to`
-  auto flush = [&](const float* v, float* to) {
+  Pairs<kE> accP{}, accS{}, wpre, coef;
+  Pairs<kMeans ? kE : 2> accQ{}, accT{};
+  {
+    float w[kE];
+    cols.template param<T>(p.pre_w, 0, f32, 1.f, w);
+    wpre.set(w);
+  }
+  // adds the teams' x in shared memory and writes it to C floats at `to`
+  auto flush = [&](const Pairs<kE>& x, float* to) {
+    float v[kE];
+    x.get(v);
     for (int k = 0; k < teams; ++k) {
       if (team == k) {
 #pragma unroll
         for (int i = 0; i < kNV; ++i) {
-          const int c = (i * team_threads + t) * kVec;
+          const int c = cols.at(i);
           if (c < p.C)
 #pragma unroll
             for (int j = 0; j < kVec; ++j) sums[c + j] = k == 0 ? v[i * kVec + j] : sums[c + j] + v[i * kVec + j];
@@ -312,93 +391,84 @@ __global__ void __launch_bounds__(kWarpTeam ? 128 : 512) bsa_block_norm_back_ker
   for (int64_t s0 = r0; s0 < r1;) {
     const int64_t gate_row = s0 / p.per_gate;
     const int64_t s1 = min(r1, (gate_row + 1) * p.per_gate);
-    const int64_t g0 = gate_row * p.C;
-    const void* gate = p.gate == nullptr ? nullptr
-                       : f32             ? static_cast<const void*>(static_cast<const float*>(p.gate) + g0)
-                                         : static_cast<const void*>(static_cast<const T*>(p.gate) + g0);
+    {
+      float w[kE], g[kE];
+      cols.template param<T>(p.post_w, 0, f32, 1.f, w);
+      cols.template param<T>(p.gate, gate_row, f32, 1.f, g);
+#pragma unroll
+      for (int e = 0; e < kE; ++e) w[e] *= p.alpha * g[e];
+      coef.set(w);
+    }
     for (; row < s1; row += teams) {
       ring.fetch(next, row + (p.depth - 1) * teams, r1);
       const float4 st = reinterpret_cast<const float4*>(p.saved)[row];
       ring.wait();
-      const int64_t at = row * p.C;
-      float D[kE];
+      Pairs<kE> D;
       ring.read(slot, 0, D);
       if (p.dnormed != nullptr) {
-        float a[kE], xh[kE], m[kN] = {};
+        Pairs<kE> a, xh;
         ring.read(slot, 2, xh);
         ring.read(slot, 3, a);
+        const uint64_t r2 = twice(st.w);
+        uint64_t m0 = 0ull, m1 = 0ull;
 #pragma unroll
-        for (int i = 0; i < kNV; ++i) {
-          const int c = (i * team_threads + t) * kVec;
-          float w[kVec] = {};
-          if (c < p.C) load_param<T, kVec>(p.pre_w, c, f32, 1.f, w);
-#pragma unroll
-          for (int j = 0; j < kVec; ++j) {
-            const int e = i * kVec + j;
-            xh[e] = c < p.C ? (xh[e] - st.z) * st.w : 0.f;
-            accP[e] = fmaf(a[e], xh[e], accP[e]);
-            if constexpr (kMeans) accQ[e] += a[e];
-            a[e] *= w[j];
-            m[0] = fmaf(a[e], xh[e], m[0]);
-            if constexpr (kMeans) m[1] += a[e];
-          }
+        for (int e = 0; e < kP; ++e) {
+          if constexpr (kMeans) xh.v[e] = ptx::fadd2(xh.v[e], cols.inside(e, -st.z));
+          xh.v[e] = ptx::fmul2(xh.v[e], r2);
+          accP.v[e] = ptx::ffma2(a.v[e], xh.v[e], accP.v[e]);
+          if constexpr (kMeans) accQ.v[e] = ptx::fadd2(accQ.v[e], a.v[e]);
+          a.v[e] = ptx::fmul2(a.v[e], wpre.v[e]);
+          m0 = ptx::ffma2(a.v[e], xh.v[e], m0);
+          if constexpr (kMeans) m1 = ptx::fadd2(m1, a.v[e]);
         }
+        float m[kN];
+        m[0] = sum2(m0);
+        if constexpr (kMeans) m[1] = sum2(m1);
         sum(m);
-        const float c1 = m[0] * p.inv_c;
-        float c2 = 0.f;
-        if constexpr (kMeans) c2 = pre_layer ? m[1] * p.inv_c : 0.f;
+        const uint64_t c1 = twice(-m[0] * p.inv_c);
 #pragma unroll
-        for (int e = 0; e < kE; ++e) D[e] = fmaf(st.w, a[e] - c2 - xh[e] * c1, D[e]);
+        for (int e = 0; e < kP; ++e) {
+          uint64_t x = ptx::ffma2(xh.v[e], c1, a.v[e]);
+          if constexpr (kMeans) x = ptx::fadd2(x, cols.inside(e, pre_layer ? -m[1] * p.inv_c : 0.f));
+          D.v[e] = ptx::ffma2(x, r2, D.v[e]);
+        }
       }
+      {
+        Pairs<kE> o;
+        const uint64_t beta = twice(p.beta);
 #pragma unroll
-      for (int i = 0; i < kNV; ++i) {
-        const int c = (i * team_threads + t) * kVec;
-        float o[kVec];
-#pragma unroll
-        for (int j = 0; j < kVec; ++j) o[j] = p.beta * D[i * kVec + j];
-        if (c < p.C) Elems<kVec, T>::store(static_cast<T*>(p.dx) + at + c, o);
+        for (int e = 0; e < kP; ++e) o.v[e] = ptx::fmul2(D.v[e], beta);
+        cols.store(static_cast<T*>(p.dx) + row * p.C, o);
       }
       if (p.y != nullptr) {
-        float yh[kE], m[kN] = {};
+        Pairs<kE> yh;
         ring.read(slot, 1, yh);
+        const uint64_t r2 = twice(p.post != BSA_NORM_NONE ? st.y : 1.f);
+        uint64_t m0 = 0ull, m1 = 0ull;
 #pragma unroll
-        for (int i = 0; i < kNV; ++i) {
-          const int c = (i * team_threads + t) * kVec;
-          float w[kVec] = {}, g[kVec] = {};
-          if (c < p.C) {
-            load_param<T, kVec>(p.post_w, c, f32, 1.f, w);
-            load_param<T, kVec>(gate, c, f32, 1.f, g);
-          }
-#pragma unroll
-          for (int j = 0; j < kVec; ++j) {
-            const int e = i * kVec + j;
-            if (c >= p.C) {
-              D[e] = yh[e] = 0.f;
-            } else if (p.post != BSA_NORM_NONE) {
-              yh[e] = (yh[e] - st.x) * st.y;
-            }
-            accS[e] = fmaf(D[e], yh[e], accS[e]);
-            if constexpr (kMeans) accT[e] += D[e];
-            D[e] *= p.alpha * g[j] * w[j];
-            m[0] = fmaf(D[e], yh[e], m[0]);
-            if constexpr (kMeans) m[1] += D[e];
-          }
+        for (int e = 0; e < kP; ++e) {
+          if constexpr (kMeans) yh.v[e] = ptx::fadd2(yh.v[e], cols.inside(e, post_layer ? -st.x : 0.f));
+          yh.v[e] = ptx::fmul2(yh.v[e], r2);
+          accS.v[e] = ptx::ffma2(D.v[e], yh.v[e], accS.v[e]);
+          if constexpr (kMeans) accT.v[e] = ptx::fadd2(accT.v[e], D.v[e]);
+          D.v[e] = ptx::fmul2(D.v[e], coef.v[e]);
+          m0 = ptx::ffma2(D.v[e], yh.v[e], m0);
+          if constexpr (kMeans) m1 = ptx::fadd2(m1, D.v[e]);
         }
-        float c1 = 0.f, c2 = 0.f, r = 1.f;
         if (p.post != BSA_NORM_NONE) {
+          float m[kN];
+          m[0] = sum2(m0);
+          if constexpr (kMeans) m[1] = sum2(m1);
           sum(m);
-          c1 = m[0] * p.inv_c;
-          if constexpr (kMeans) c2 = post_layer ? m[1] * p.inv_c : 0.f;
-          r = st.y;
-        }
+          const uint64_t c1 = twice(-m[0] * p.inv_c);
 #pragma unroll
-        for (int i = 0; i < kNV; ++i) {
-          const int c = (i * team_threads + t) * kVec;
-          float o[kVec];
-#pragma unroll
-          for (int j = 0; j < kVec; ++j) o[j] = r * (D[i * kVec + j] - c2 - yh[i * kVec + j] * c1);
-          if (c < p.C) Elems<kVec, T>::store(static_cast<T*>(p.dy) + at + c, o);
+          for (int e = 0; e < kP; ++e) {
+            D.v[e] = ptx::ffma2(yh.v[e], c1, D.v[e]);
+            if constexpr (kMeans) D.v[e] = ptx::fadd2(D.v[e], twice(post_layer ? -m[1] * p.inv_c : 0.f));
+            D.v[e] = ptx::fmul2(D.v[e], r2);
+          }
         }
+        cols.store(static_cast<T*>(p.dy) + row * p.C, D);
       }
       slot = slot + 1 == p.depth ? 0 : slot + 1;
       next = next + 1 == p.depth ? 0 : next + 1;
@@ -406,12 +476,11 @@ __global__ void __launch_bounds__(kWarpTeam ? 128 : 512) bsa_block_norm_back_ker
     if (p.part != nullptr && p.y != nullptr) {
       float* to = p.part + (blockIdx.x + gate_row) * kN * p.C;
       flush(accS, to);
-      if constexpr (kMeans) flush(accT, to + p.C);
-#pragma unroll
-      for (int e = 0; e < kE; ++e) accS[e] = 0.f;
-      if constexpr (kMeans)
-#pragma unroll
-        for (int e = 0; e < kE; ++e) accT[e] = 0.f;
+      accS = Pairs<kE>{};
+      if constexpr (kMeans) {
+        flush(accT, to + p.C);
+        accT = Pairs<kE>{};
+      }
     }
     s0 = s1;
   }
@@ -524,7 +593,7 @@ struct Team {
   int threads, teams;    // threads a team, teams a block
   int depth, per_sm;     // slots of the ring, blocks on an SM
   size_t smem;
-  bool warp() const { return threads == 32; }
+  bool warp;             // a warp a row, without barriers
 };
 
 // arrays: how many the ring brings; sums: [C] floats and kN areas a team (backward).
@@ -534,11 +603,12 @@ Team team_of(int C, size_t esize, bool aligned, bool backward, bool means) {
   const int n = C / t.vec;
   // A warp takes a row while a lane's share fits its registers (the backward keeps two sums
   // a column, four with plain means), else the fewest pieces a thread that 512 threads allow.
-  const int most = t.vec < 8 ? 0 : !backward ? 4 : means ? 2 : 3;
+  const int most = t.vec < 8 ? 0 : backward && means ? 2 : 3;
   if (n <= 32 * most) {
     t.nv = (n + 31) / 32;
     t.threads = 32;
     t.teams = 4;
+    t.warp = true;
   } else {
     t.nv = t.vec == 8 ? (n <= 512 ? 1 : 2) : t.vec == 2 ? (n <= 2048 ? 4 : 8) : (n <= 4096 ? 8 : 16);
     t.threads = ((n + t.nv - 1) / t.nv + 31) / 32 * 32;
@@ -548,7 +618,7 @@ Team team_of(int C, size_t esize, bool aligned, bool backward, bool means) {
   const size_t fixed = backward ? ((C + 3) / 4 * 4 + t.teams * 2 * nq * 32) * sizeof(float) : t.teams * 256;
   const size_t slot = static_cast<size_t>(block) * (backward ? 4 : 2) * t.nv * t.vec * esize;
   // blocks on an SM that the registers allow: about 128 a thread, 255 for the backward's warps
-  const int by_regs = std::max(1, (backward && t.warp() ? 256 : 512) / block);
+  const int by_regs = std::max(1, (backward && t.warp ? 256 : 512) / block);
   t.depth = 3;
   t.per_sm = by_regs;
   while (t.depth > 1 && (fixed + t.depth * slot + 1024) * t.per_sm > 220 * 1024) --t.depth;
@@ -611,11 +681,10 @@ template <typename T>
 bool launch_norm(NormParams p, const Team& t, int sms, cudaStream_t s) {
   p.depth = t.depth;
   const int64_t blocks = std::min<int64_t>((p.rows + t.teams - 1) / t.teams, static_cast<int64_t>(sms) * t.per_sm);
-  if (t.warp()) {
+  if (t.warp) {
     if (t.nv == 1) return start(bsa_block_norm_kernel<T, 8, 1, true>, p, t, blocks, s);
     if (t.nv == 2) return start(bsa_block_norm_kernel<T, 8, 2, true>, p, t, blocks, s);
-    if (t.nv == 3) return start(bsa_block_norm_kernel<T, 8, 3, true>, p, t, blocks, s);
-    return start(bsa_block_norm_kernel<T, 8, 4, true>, p, t, blocks, s);
+    return start(bsa_block_norm_kernel<T, 8, 3, true>, p, t, blocks, s);
   }
   if (t.vec == 8)
     return t.nv == 1 ? start(bsa_block_norm_kernel<T, 8, 1, false>, p, t, blocks, s)
@@ -646,7 +715,7 @@ BackPlan back_plan(const NormParams& p, const Team& t, int gate_rows, bool means
 
 template <typename T, bool kMeans>
 bool launch_back(const NormParams& p, const Team& t, const BackPlan& b, cudaStream_t s) {
-  if (t.warp()) {
+  if (t.warp) {
     if (t.nv == 1) return start(bsa_block_norm_back_kernel<T, 8, 1, true, kMeans>, p, t, b.blocks, s);
     if constexpr (!kMeans)
       if (t.nv == 3) return start(bsa_block_norm_back_kernel<T, 8, 3, true, kMeans>, p, t, b.blocks, s);
