@@ -81,11 +81,18 @@ __device__ __forceinline__ float sum2(uint64_t x) {
 }
 
 // A thread's columns of a row of C: pieces of kVec, kNV of them.
-template <int kVec, int kNV>
+template <int kVec, int kNV, bool kWarp>
 struct Cols {
   static constexpr int kE = kVec * kNV;
   int C, team_threads, t;
-  __device__ __forceinline__ int at(int i) const { return (i * team_threads + t) * kVec; }
+  uint32_t in;  // bit i: piece i lies in the row
+  __device__ __forceinline__ Cols(int C_, int team_, int t_) : C(C_), team_threads(team_), t(t_), in(0) {
+#pragma unroll
+    for (int i = 0; i < kNV; ++i) in |= at(i) < C ? 1u << i : 0u;
+  }
+  __device__ __forceinline__ int team() const { return kWarp ? 32 : team_threads; }
+  __device__ __forceinline__ int at(int i) const { return (i * team() + t) * kVec; }
+  __device__ __forceinline__ bool has(int i) const { return in >> i & 1u; }
   // a parameter's values at these columns (`dflt` where it is absent), 0 past the row's end
   template <typename T>
   __device__ __forceinline__ void param(const void* p, int64_t row, bool f32, float dflt, float (&v)[kE]) const {
@@ -94,8 +101,8 @@ struct Cols {
       const int c = at(i);
       float e[kVec];
 #pragma unroll
-      for (int j = 0; j < kVec; ++j) e[j] = c < C ? dflt : 0.f;
-      if (p != nullptr && c < C) {
+      for (int j = 0; j < kVec; ++j) e[j] = has(i) ? dflt : 0.f;
+      if (p != nullptr && has(i)) {
         if (f32) Elems<kVec, float>::load(static_cast<const float*>(p) + row * C + c, e);
         else Elems<kVec, T>::load(static_cast<const T*>(p) + row * C + c, e);
       }
@@ -104,7 +111,7 @@ struct Cols {
     }
   }
   template <typename T>
-  __device__ __forceinline__ void store(T* row, const Pairs<kE>& x) const {
+  __device__ __forceinline__ void store(T* mine, const Pairs<kE>& x) const {  // mine: at column at(0) of the row
     float v[kE];
     x.get(v);
 #pragma unroll
@@ -112,12 +119,12 @@ struct Cols {
       float e[kVec];
 #pragma unroll
       for (int j = 0; j < kVec; ++j) e[j] = v[i * kVec + j];
-      if (at(i) < C) Elems<kVec, T>::store(row + at(i), e);
+      if (has(i)) Elems<kVec, T>::store(mine + i * team() * kVec, e);
     }
   }
   // x where a piece is inside the row, else 0
   __device__ __forceinline__ uint64_t inside(int e, float x) const {
-    const float a = at(2 * e / kVec) < C ? x : 0.f, b = at((2 * e + 1) / kVec) < C ? x : 0.f;
+    const float a = has(2 * e / kVec) ? x : 0.f, b = has((2 * e + 1) / kVec) ? x : 0.f;
     return ptx::pack2(a, b);
   }
 };
@@ -156,7 +163,7 @@ struct TeamSum {
 // (mean, 1 / sqrt(mean square of the centred values + eps)) of a row over the team; with a
 // layer norm v is centred.  Past the row's end v holds 0 and keeps it.
 template <int kVec, int kNV, bool kWarpTeam>
-__device__ __forceinline__ float2 statistics(Pairs<kVec * kNV>& v, int kind, const Cols<kVec, kNV>& cols,
+__device__ __forceinline__ float2 statistics(Pairs<kVec * kNV>& v, int kind, const Cols<kVec, kNV, kWarpTeam>& cols,
                                              const NormParams& p, TeamSum<1, kWarpTeam>& sum) {
   constexpr int kP = kVec * kNV / 2;
   float mean = 0.f, s[1];
@@ -178,66 +185,124 @@ __device__ __forceinline__ float2 statistics(Pairs<kVec * kNV>& v, int kind, con
   return make_float2(mean, 1.f / sqrtf(fmaf(s[0], p.inv_c, p.eps)));
 }
 
+constexpr int kWarpBlock = 128;  // threads of a block whose teams are warps
+
+__device__ __forceinline__ uint4 lds16(uint32_t a) {
+  uint4 v;
+  asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(a));
+  return v;
+}
+__device__ __forceinline__ uint2 lds8(uint32_t a) {
+  uint2 v;
+  asm volatile("ld.shared.v2.u32 {%0, %1}, [%2];" : "=r"(v.x), "=r"(v.y) : "r"(a));
+  return v;
+}
+__device__ __forceinline__ uint32_t lds4(uint32_t a) {
+  uint32_t v;
+  asm volatile("ld.shared.u32 %0, [%1];" : "=r"(v) : "r"(a));
+  return v;
+}
+__device__ __forceinline__ uint16_t lds2(uint32_t a) {
+  uint16_t v;
+  asm volatile("ld.shared.u16 %0, [%1];" : "=h"(v) : "r"(a));
+  return v;
+}
+
 // Rows on their way to this thread: kNA arrays, kNV pieces of kVec elements of each, `depth`
-// slots.  Pieces of two bytes (an odd row of 16-bit elements) are copied at once instead.
-template <typename T, int kVec, int kNV, int kNA>
+// slots.  Rows come in the order of the fetches, `stride` bytes apart.  Pieces of two bytes
+// (an odd row of 16-bit elements) are copied at once instead.
+template <typename T, int kVec, int kNV, int kNA, bool kWarpTeam>
 struct Ring {
   static constexpr int kBytes = kVec * static_cast<int>(sizeof(T));
   static constexpr int kPiece = kBytes > 16 ? 16 : kBytes;
-  uint8_t* mine;  // this thread's first piece; pieces of a thread are kPiece * blockDim.x apart
-  const T* src[kNA];
-  int C, team_threads, t, depth;
-  __device__ __forceinline__ uint8_t* at(int slot, int a, int i, int h) const {
-    return mine + ((((slot * kNA + a) * kNV + i) * (kBytes / kPiece) + h) * blockDim.x) * kPiece;
+  static constexpr int kSplit = kBytes / kPiece;
+  const char* src[kNA];  // this thread's first piece in the next row to fetch, or null
+  int64_t stride;
+  uint32_t base, slot_bytes, cur, nxt;  // shared-memory addresses of this thread's pieces
+  int depth;
+  __device__ __forceinline__ uint32_t gap() const {  // between a thread's pieces in shared memory
+    return (kWarpTeam ? kWarpBlock : blockDim.x) * kPiece;
   }
-  // starts bringing row `row` (nothing past the last) into `slot`, as one group
-  __device__ __forceinline__ void fetch(int slot, int64_t row, int64_t rows) {
-    if (row < rows) {
+  __device__ __forceinline__ void init(uint32_t smem, const Cols<kVec, kNV, kWarpTeam>& cols, int64_t row, int64_t step,
+                                       int slots, const void* const (&from)[kNA]) {
+    depth = slots;
+    base = smem + threadIdx.x * kPiece;
+    slot_bytes = kNA * kNV * kSplit * gap();
+    cur = base;
+    nxt = base;
+    stride = step * cols.C * static_cast<int64_t>(sizeof(T));
 #pragma unroll
-      for (int a = 0; a < kNA; ++a) {
-        if (src[a] == nullptr) continue;
+    for (int a = 0; a < kNA; ++a)
+      src[a] = from[a] == nullptr ? nullptr
+                                  : static_cast<const char*>(from[a]) + (row * cols.C + cols.at(0)) * static_cast<int64_t>(sizeof(T));
+  }
+  __device__ __forceinline__ uint32_t after(uint32_t slot) const {
+    return slot + slot_bytes == base + depth * slot_bytes ? base : slot + slot_bytes;
+  }
+  // starts bringing the next row (nothing if it is not `there`) into the next slot, as one group
+  __device__ __forceinline__ void fetch(const Cols<kVec, kNV, kWarpTeam>& cols, bool there) {
+#pragma unroll
+    for (int a = 0; a < kNA; ++a) {
+      if (src[a] == nullptr) continue;
+      if (there)
 #pragma unroll
         for (int i = 0; i < kNV; ++i) {
-          const int c = (i * team_threads + t) * kVec;
-          if (c >= C) continue;
-          const T* p = src[a] + row * C + c;
+          if (!cols.has(i)) continue;
+          const char* p = src[a] + static_cast<int64_t>(i) * cols.team() * kBytes;
+          const uint32_t dst = nxt + (a * kNV + i) * kSplit * gap();
           if constexpr (kBytes < 4) {
-            *reinterpret_cast<T*>(at(slot, a, i, 0)) = *p;
+            asm volatile("st.shared.u16 [%0], %1;" ::"r"(dst), "h"(*reinterpret_cast<const uint16_t*>(p)) : "memory");
           } else {
 #pragma unroll
-            for (int h = 0; h < kBytes / kPiece; ++h) {
-              const uint32_t dst = static_cast<uint32_t>(__cvta_generic_to_shared(at(slot, a, i, h)));
-              const uint8_t* from = reinterpret_cast<const uint8_t*>(p) + h * kPiece;
+            for (int h = 0; h < kSplit; ++h) {
               if constexpr (kPiece == 16)
-                asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(from) : "memory");
+                asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst + h * gap()), "l"(p + 16 * h) : "memory");
               else
-                asm volatile("cp.async.ca.shared.global [%0], [%1], %2;" ::"r"(dst), "l"(from), "n"(kPiece) : "memory");
+                asm volatile("cp.async.ca.shared.global [%0], [%1], %2;" ::"r"(dst), "l"(p), "n"(kPiece) : "memory");
             }
           }
         }
-      }
+      src[a] += stride;
     }
     asm volatile("cp.async.commit_group;" ::: "memory");
+    nxt = after(nxt);
   }
-  // all but the newest depth - 1 groups have landed
+  // the oldest row has landed
   __device__ __forceinline__ void wait() const {
     if (depth == 3) asm volatile("cp.async.wait_group 2;" ::: "memory");
     else if (depth == 2) asm volatile("cp.async.wait_group 1;" ::: "memory");
     else asm volatile("cp.async.wait_group 0;" ::: "memory");
   }
-  // this thread's elements of array a; 0 past the row's end and of an array that is not there
-  __device__ __forceinline__ void read(int slot, int a, Pairs<kVec * kNV>& to) const {
+  __device__ __forceinline__ void done() { cur = after(cur); }
+  // this thread's elements of array a in the oldest row; 0 past the row's end and of an array
+  // that is not there
+  __device__ __forceinline__ void read(const Cols<kVec, kNV, kWarpTeam>& cols, int a, Pairs<kVec * kNV>& to) const {
     float v[kVec * kNV];
 #pragma unroll
     for (int i = 0; i < kNV; ++i) {
       float e[kVec] = {};
-      if (src[a] != nullptr && (i * team_threads + t) * kVec < C) {
-        if constexpr (kBytes <= 16) {
-          Elems<kVec, T>::load(reinterpret_cast<const T*>(at(slot, a, i, 0)), e);
+      const uint32_t at = cur + (a * kNV + i) * kSplit * gap();
+      if (src[a] != nullptr && cols.has(i)) {
+        if constexpr (kBytes == 2) {
+          const uint16_t w = lds2(at);
+          e[0] = to_f32(*reinterpret_cast<const T*>(&w));
+        } else if constexpr (kVec == 1) {
+          e[0] = __uint_as_float(lds4(at));
+        } else if constexpr (kBytes == 4) {
+          unpack(lds4(at), T(), e[0], e[1]);
+        } else if constexpr (kBytes == 8) {
+          const uint2 w = lds8(at);
+          e[0] = __uint_as_float(w.x), e[1] = __uint_as_float(w.y);
+        } else if constexpr (kBytes == 16) {
+          const uint4 w = lds16(at);
+          unpack(w.x, T(), e[0], e[1]);
+          unpack(w.y, T(), e[2], e[3]);
+          unpack(w.z, T(), e[4], e[5]);
+          unpack(w.w, T(), e[6], e[7]);
         } else {
-          const float4 lo = *reinterpret_cast<const float4*>(at(slot, a, i, 0));
-          const float4 hi = *reinterpret_cast<const float4*>(at(slot, a, i, 1));
-          e[0] = lo.x, e[1] = lo.y, e[2] = lo.z, e[3] = lo.w, e[4] = hi.x, e[5] = hi.y, e[6] = hi.z, e[7] = hi.w;
+          const uint4 w = lds16(at), z = lds16(at + gap());
+          e[0] = __uint_as_float(w.x), e[1] = __uint_as_float(w.y), e[2] = __uint_as_float(w.z), e[3] = __uint_as_float(w.w);
+          e[4] = __uint_as_float(z.x), e[5] = __uint_as_float(z.y), e[6] = __uint_as_float(z.z), e[7] = __uint_as_float(z.w);
         }
       }
 #pragma unroll
@@ -247,22 +312,23 @@ struct Ring {
   }
 };
 
-template <typename T, int kVec, int kNV, bool kWarpTeam>
+template <typename T, int kVec, int kNV, bool kWarpTeam, bool kBias>
 __global__ void __launch_bounds__(kWarpTeam ? 128 : 512, kWarpTeam ? 4 : 1) bsa_block_norm_kernel(const __grid_constant__ NormParams p,
                                                                                int team_threads) {
   constexpr int kE = kVec * kNV, kP = kE / 2;
   extern __shared__ __align__(16) uint8_t smem[];  // the reduction areas, then the ring
   const int teams = blockDim.x / team_threads, team = threadIdx.x / team_threads, t = threadIdx.x % team_threads;
   TeamSum<1, kWarpTeam> sum{reinterpret_cast<float*>(smem) + team * 64, team_threads, 1 + team};
-  const Cols<kVec, kNV> cols{p.C, team_threads, t};
-  Ring<T, kVec, kNV, 2> ring;
-  ring.mine = smem + teams * 256 + threadIdx.x * ring.kPiece;
-  ring.src[0] = static_cast<const T*>(p.x), ring.src[1] = static_cast<const T*>(p.y);
-  ring.C = p.C, ring.team_threads = team_threads, ring.t = t, ring.depth = p.depth;
-  const int64_t step = static_cast<int64_t>(gridDim.x) * teams;
-  int64_t row = static_cast<int64_t>(blockIdx.x) * teams + team;
-  int slot = 0, next = p.depth - 1;
-  for (int d = 0; d + 1 < p.depth; ++d) ring.fetch(d, row + d * step, p.rows);
+  const Cols<kVec, kNV, kWarpTeam> cols(p.C, team_threads, t);
+  const int step = gridDim.x * teams, rows = static_cast<int>(p.rows);  // rows and steps fit 31 bits
+  int row = blockIdx.x * teams + team;
+  Ring<T, kVec, kNV, 2, kWarpTeam> ring;
+  ring.init(ptx::smem_addr(smem) + teams * 256, cols, row, step, p.depth, {p.x, p.y});
+  int64_t ahead = row;  // the next row to fetch
+  for (int d = 0; d + 1 < p.depth; ++d, ahead += step) ring.fetch(cols, ahead < rows);
+  T* out = static_cast<T*>(p.out) + static_cast<int64_t>(row) * p.C + cols.at(0);
+  T* normed = static_cast<T*>(p.normed) + static_cast<int64_t>(row) * p.C + cols.at(0);
+  const int64_t stride = static_cast<int64_t>(step) * p.C;
   const bool f32 = p.params_f32 != 0;
   Pairs<kE> wpre, coef;  // pre weight; branch_scale gate post_weight of the gate row at hand
   {
@@ -270,11 +336,12 @@ __global__ void __launch_bounds__(kWarpTeam ? 128 : 512, kWarpTeam ? 4 : 1) bsa_
     cols.template param<T>(p.pre_w, 0, f32, 1.f, w);
     wpre.set(w);
   }
-  int64_t gate_end = row;  // rows from here on have another gate row than coef's
-  for (; row < p.rows; row += step) {
-    ring.fetch(next, row + (p.depth - 1) * step, p.rows);
-    const int64_t gate_row = row >= gate_end ? static_cast<uint32_t>(row) / static_cast<uint32_t>(p.per_gate) : 0;
+  int64_t gate_end = 0;  // rows from here on have another gate row than coef's
+  for (; row < rows; row = step > rows - row ? rows : row + step, out += stride, normed += stride) {
+    ring.fetch(cols, ahead < rows);
+    ahead += step;
     if (p.y != nullptr && row >= gate_end) {
+      const uint32_t gate_row = static_cast<uint32_t>(row) / static_cast<uint32_t>(p.per_gate);
       gate_end = (gate_row + 1) * p.per_gate;
       float w[kE], g[kE];
       cols.template param<T>(p.post_w, 0, f32, 1.f, w);
@@ -285,11 +352,11 @@ __global__ void __launch_bounds__(kWarpTeam ? 128 : 512, kWarpTeam ? 4 : 1) bsa_
     }
     ring.wait();
     Pairs<kE> st;
-    ring.read(slot, 0, st);
+    ring.read(cols, 0, st);
     float2 post = make_float2(0.f, 0.f), pre = make_float2(0.f, 0.f);
     if (p.y != nullptr) {
       Pairs<kE> y;
-      ring.read(slot, 1, y);
+      ring.read(cols, 1, y);
       float r = 1.f;
       if (p.post != BSA_NORM_NONE) {
         post = statistics<kVec, kNV, kWarpTeam>(y, p.post, cols, p, sum);
@@ -299,7 +366,7 @@ __global__ void __launch_bounds__(kWarpTeam ? 128 : 512, kWarpTeam ? 4 : 1) bsa_
 #pragma unroll
       for (int e = 0; e < kP; ++e)
         st.v[e] = ptx::ffma2(ptx::fmul2(y.v[e], r2), coef.v[e], ptx::fmul2(st.v[e], beta));
-      if (p.post_b != nullptr) {
+      if (kBias && p.post_b != nullptr) {
         float b[kE], g[kE];
         Pairs<kE> add;
         cols.template param<T>(p.post_b, 0, f32, 0.f, b);
@@ -310,14 +377,14 @@ __global__ void __launch_bounds__(kWarpTeam ? 128 : 512, kWarpTeam ? 4 : 1) bsa_
 #pragma unroll
         for (int e = 0; e < kP; ++e) st.v[e] = ptx::fadd2(st.v[e], add.v[e]);
       }
-      cols.store(static_cast<T*>(p.out) + row * p.C, st);
+      cols.store(out, st);
     }
     if (p.pre != BSA_NORM_NONE) {
       pre = statistics<kVec, kNV, kWarpTeam>(st, p.pre, cols, p, sum);
       const uint64_t r2 = twice(pre.y);
 #pragma unroll
       for (int e = 0; e < kP; ++e) st.v[e] = ptx::fmul2(ptx::fmul2(st.v[e], r2), wpre.v[e]);
-      if (p.pre_b != nullptr) {
+      if (kBias && p.pre_b != nullptr) {
         float b[kE];
         Pairs<kE> add;
         cols.template param<T>(p.pre_b, 0, f32, 0.f, b);
@@ -325,12 +392,11 @@ __global__ void __launch_bounds__(kWarpTeam ? 128 : 512, kWarpTeam ? 4 : 1) bsa_
 #pragma unroll
         for (int e = 0; e < kP; ++e) st.v[e] = ptx::fadd2(st.v[e], add.v[e]);
       }
-      cols.store(static_cast<T*>(p.normed) + row * p.C, st);
+      cols.store(normed, st);
     }
     if (p.stats != nullptr && t == 0)
       reinterpret_cast<float4*>(p.stats)[row] = make_float4(post.x, post.y, pre.x, pre.y);
-    slot = slot + 1 == p.depth ? 0 : slot + 1;
-    next = next + 1 == p.depth ? 0 : next + 1;
+    ring.done();
   }
 }
 
@@ -345,15 +411,10 @@ __global__ void __launch_bounds__(kWarpTeam ? 128 : 512, kWarpTeam ? 2 : 1) bsa_
   const int teams = blockDim.x / team_threads, team = threadIdx.x / team_threads, t = threadIdx.x % team_threads;
   const int cpad = (p.C + 3) / 4 * 4;
   TeamSum<kN, kWarpTeam> sum{sums + cpad + team * (2 * kN * 32), team_threads, 1 + team};
-  const Cols<kVec, kNV> cols{p.C, team_threads, t};
-  Ring<T, kVec, kNV, 4> ring;
-  ring.mine = smem + (cpad + teams * 2 * kN * 32) * sizeof(float) + threadIdx.x * ring.kPiece;
-  ring.src[0] = static_cast<const T*>(p.dstream), ring.src[1] = static_cast<const T*>(p.y);
-  ring.src[2] = p.dnormed == nullptr ? nullptr : static_cast<const T*>(p.x);
-  ring.src[3] = static_cast<const T*>(p.dnormed);
-  ring.C = p.C, ring.team_threads = team_threads, ring.t = t, ring.depth = p.depth;
-  const int64_t r0 = static_cast<int64_t>(blockIdx.x) * p.rows_per_block;
-  const int64_t r1 = min(r0 + p.rows_per_block, p.rows);
+  const Cols<kVec, kNV, kWarpTeam> cols(p.C, team_threads, t);
+  // rows fit 31 bits
+  const int r0 = static_cast<int>(blockIdx.x * p.rows_per_block);
+  const int r1 = static_cast<int>(min(blockIdx.x * p.rows_per_block + p.rows_per_block, p.rows));
   const bool f32 = p.params_f32 != 0;
   const bool pre_layer = p.pre == BSA_NORM_LAYER, post_layer = p.post == BSA_NORM_LAYER;
 
@@ -385,12 +446,18 @@ __global__ void __launch_bounds__(kWarpTeam ? 128 : 512, kWarpTeam ? 2 : 1) bsa_
   };
   // The block's rows go round its teams; a team's rows are one sequence for the ring, cut
   // where the gate row changes.
-  int64_t row = r0 + team;
-  int slot = 0, next = p.depth - 1;
-  for (int d = 0; d + 1 < p.depth; ++d) ring.fetch(d, row + d * teams, r1);
+  int64_t row = r0 + team, ahead = row;
+  Ring<T, kVec, kNV, 4, kWarpTeam> ring;
+  ring.init(ptx::smem_addr(smem) + (cpad + teams * 2 * kN * 32) * static_cast<uint32_t>(sizeof(float)), cols, row,
+            teams, p.depth, {p.dstream, p.y, p.dnormed == nullptr ? nullptr : p.x, p.dnormed});
+  for (int d = 0; d + 1 < p.depth; ++d, ahead += teams) ring.fetch(cols, ahead < r1);
+  T* dx = static_cast<T*>(p.dx) + row * p.C + cols.at(0);
+  T* dy = static_cast<T*>(p.dy) + row * p.C + cols.at(0);
+  const float4* saved = reinterpret_cast<const float4*>(p.saved);
+  const int stride = teams * p.C;
   for (int64_t s0 = r0; s0 < r1;) {
     const int64_t gate_row = s0 / p.per_gate;
-    const int64_t s1 = min(r1, (gate_row + 1) * p.per_gate);
+    const int64_t s1 = min(static_cast<int64_t>(r1), (gate_row + 1) * p.per_gate);
     {
       float w[kE], g[kE];
       cols.template param<T>(p.post_w, 0, f32, 1.f, w);
@@ -399,16 +466,17 @@ __global__ void __launch_bounds__(kWarpTeam ? 128 : 512, kWarpTeam ? 2 : 1) bsa_
       for (int e = 0; e < kE; ++e) w[e] *= p.alpha * g[e];
       coef.set(w);
     }
-    for (; row < s1; row += teams) {
-      ring.fetch(next, row + (p.depth - 1) * teams, r1);
-      const float4 st = reinterpret_cast<const float4*>(p.saved)[row];
+    for (; row < s1; row += teams, dx += stride, dy += stride) {
+      ring.fetch(cols, ahead < r1);
+      ahead += teams;
+      const float4 st = __ldg(saved + row);
       ring.wait();
       Pairs<kE> D;
-      ring.read(slot, 0, D);
+      ring.read(cols, 0, D);
       if (p.dnormed != nullptr) {
         Pairs<kE> a, xh;
-        ring.read(slot, 2, xh);
-        ring.read(slot, 3, a);
+        ring.read(cols, 2, xh);
+        ring.read(cols, 3, a);
         const uint64_t r2 = twice(st.w);
         uint64_t m0 = 0ull, m1 = 0ull;
 #pragma unroll
@@ -438,11 +506,11 @@ __global__ void __launch_bounds__(kWarpTeam ? 128 : 512, kWarpTeam ? 2 : 1) bsa_
         const uint64_t beta = twice(p.beta);
 #pragma unroll
         for (int e = 0; e < kP; ++e) o.v[e] = ptx::fmul2(D.v[e], beta);
-        cols.store(static_cast<T*>(p.dx) + row * p.C, o);
+        cols.store(dx, o);
       }
       if (p.y != nullptr) {
         Pairs<kE> yh;
-        ring.read(slot, 1, yh);
+        ring.read(cols, 1, yh);
         const uint64_t r2 = twice(p.post != BSA_NORM_NONE ? st.y : 1.f);
         uint64_t m0 = 0ull, m1 = 0ull;
 #pragma unroll
@@ -468,10 +536,9 @@ __global__ void __launch_bounds__(kWarpTeam ? 128 : 512, kWarpTeam ? 2 : 1) bsa_
             D.v[e] = ptx::fmul2(D.v[e], r2);
           }
         }
-        cols.store(static_cast<T*>(p.dy) + row * p.C, D);
+        cols.store(dy, D);
       }
-      slot = slot + 1 == p.depth ? 0 : slot + 1;
-      next = next + 1 == p.depth ? 0 : next + 1;
+      ring.done();
     }
     if (p.part != nullptr && p.y != nullptr) {
       float* to = p.part + (blockIdx.x + gate_row) * kN * p.C;
@@ -677,23 +744,28 @@ bool start(F* kernel, const NormParams& p, const Team& t, int64_t blocks, cudaSt
   return true;
 }
 
+template <typename T, bool kBias>
+bool launch_norm(const NormParams& p, const Team& t, int64_t blocks, cudaStream_t s) {
+  if (t.warp) {
+    if (t.nv == 1) return start(bsa_block_norm_kernel<T, 8, 1, true, kBias>, p, t, blocks, s);
+    if (t.nv == 2) return start(bsa_block_norm_kernel<T, 8, 2, true, kBias>, p, t, blocks, s);
+    return start(bsa_block_norm_kernel<T, 8, 3, true, kBias>, p, t, blocks, s);
+  }
+  if (t.vec == 8)
+    return t.nv == 1 ? start(bsa_block_norm_kernel<T, 8, 1, false, kBias>, p, t, blocks, s)
+                     : start(bsa_block_norm_kernel<T, 8, 2, false, kBias>, p, t, blocks, s);
+  if (t.vec == 2)
+    return t.nv == 4 ? start(bsa_block_norm_kernel<T, 2, 4, false, kBias>, p, t, blocks, s)
+                     : start(bsa_block_norm_kernel<T, 2, 8, false, kBias>, p, t, blocks, s);
+  return t.nv == 8 ? start(bsa_block_norm_kernel<T, 1, 8, false, kBias>, p, t, blocks, s)
+                   : start(bsa_block_norm_kernel<T, 1, 16, false, kBias>, p, t, blocks, s);
+}
 template <typename T>
 bool launch_norm(NormParams p, const Team& t, int sms, cudaStream_t s) {
   p.depth = t.depth;
   const int64_t blocks = std::min<int64_t>((p.rows + t.teams - 1) / t.teams, static_cast<int64_t>(sms) * t.per_sm);
-  if (t.warp) {
-    if (t.nv == 1) return start(bsa_block_norm_kernel<T, 8, 1, true>, p, t, blocks, s);
-    if (t.nv == 2) return start(bsa_block_norm_kernel<T, 8, 2, true>, p, t, blocks, s);
-    return start(bsa_block_norm_kernel<T, 8, 3, true>, p, t, blocks, s);
-  }
-  if (t.vec == 8)
-    return t.nv == 1 ? start(bsa_block_norm_kernel<T, 8, 1, false>, p, t, blocks, s)
-                     : start(bsa_block_norm_kernel<T, 8, 2, false>, p, t, blocks, s);
-  if (t.vec == 2)
-    return t.nv == 4 ? start(bsa_block_norm_kernel<T, 2, 4, false>, p, t, blocks, s)
-                     : start(bsa_block_norm_kernel<T, 2, 8, false>, p, t, blocks, s);
-  return t.nv == 8 ? start(bsa_block_norm_kernel<T, 1, 8, false>, p, t, blocks, s)
-                   : start(bsa_block_norm_kernel<T, 1, 16, false>, p, t, blocks, s);
+  return p.post_b != nullptr || p.pre_b != nullptr ? launch_norm<T, true>(p, t, blocks, s)
+                                                   : launch_norm<T, false>(p, t, blocks, s);
 }
 
 struct BackPlan {

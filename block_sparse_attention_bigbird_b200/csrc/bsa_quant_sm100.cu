@@ -112,7 +112,7 @@ __device__ __forceinline__ uint2 codes8(const float (&v)[8]) {
 
 // kForm: 0 rows, 1 columns, 2 both
 template <typename T, bool kE5, bool kSquare, int kForm>
-__global__ void __launch_bounds__(256) bsa_fp8_quantize_kernel(const __grid_constant__ QuantParams p) {
+__global__ void __launch_bounds__(256, sizeof(T) == 2 ? 3 : 2) bsa_fp8_quantize_kernel(const __grid_constant__ QuantParams p) {
   constexpr float kTop = kE5 ? 57344.f : 448.f;
   constexpr bool kRows = kForm != 1, kCols = kForm != 0;
   // maxima of the warps' columns (or of the warps), and the columns' top / m

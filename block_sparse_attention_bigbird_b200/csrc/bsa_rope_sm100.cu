@@ -36,6 +36,7 @@ namespace {
 constexpr int kMaxPairs = 128;
 constexpr int kMaxAxes = 8;
 constexpr int kRopeThreads = 128;
+constexpr int kBatch = 4;  // heads a thread has on their way at once
 
 struct RopeParams {
   double turns[kMaxPairs];  // frequency in turns per position
@@ -98,36 +99,39 @@ __global__ void __launch_bounds__(kRopeThreads) bsa_rope_kernel(const __grid_con
       sn[i] *= p.sign;
     }
   }
-#pragma unroll 4
-  for (int h = h0; h < h1; ++h) {
-    const int w = h >= p.heads[0], hh = w ? h - p.heads[0] : h;
-    const T* in = static_cast<const T*>(p.in[w]) + b * p.is[w][0] + hh * p.is[w][1] + l * p.is[w][2];
-    T* out = static_cast<T*>(p.out[w]) + b * p.os[w][0] + hh * p.os[w][1] + l * p.os[w][2];
-    float u[kVec], v[kVec];
-    Elems<kVec, T>::load(in + c0, u);
-    if (second) Elems<kVec, T>::load(in + c1, v);
-    if (turn) {
-      if constexpr (kAdj) {
-        // the 2 kVec columns hold kVec pairs (u, v) side by side
+  // kBatch heads' loads are issued before the first store, which the compiler could not move
+  // them over (the results may lie where the inputs are)
+  for (int first = h0; first < h1; first += kBatch) {
+    float u[kBatch][kVec], v[kBatch][kVec];
 #pragma unroll
-        for (int i = 0; i < kVec; ++i) {
-          float& x = 2 * i < kVec ? u[(2 * i) % kVec] : v[(2 * i) % kVec];
-          float& y = 2 * i + 1 < kVec ? u[(2 * i + 1) % kVec] : v[(2 * i + 1) % kVec];
-          const float a = x * cs[i] - y * sn[i], c = x * sn[i] + y * cs[i];
+    for (int i = 0; i < kBatch; ++i) {
+      const int h = first + i;
+      if (h >= h1) break;
+      const int w = h >= p.heads[0], hh = w ? h - p.heads[0] : h;
+      const T* in = static_cast<const T*>(p.in[w]) + b * p.is[w][0] + hh * p.is[w][1] + l * p.is[w][2];
+      Elems<kVec, T>::load(in + c0, u[i]);
+      if (second) Elems<kVec, T>::load(in + c1, v[i]);
+    }
+#pragma unroll
+    for (int i = 0; i < kBatch; ++i) {
+      const int h = first + i;
+      if (h >= h1) break;
+      const int w = h >= p.heads[0], hh = w ? h - p.heads[0] : h;
+      T* out = static_cast<T*>(p.out[w]) + b * p.os[w][0] + hh * p.os[w][1] + l * p.os[w][2];
+      if (turn) {
+#pragma unroll
+        for (int e = 0; e < kVec; ++e) {
+          // kAdj: the 2 kVec columns hold kVec pairs side by side
+          float& x = !kAdj ? u[i][e] : 2 * e < kVec ? u[i][(2 * e) % kVec] : v[i][(2 * e) % kVec];
+          float& y = !kAdj ? v[i][e] : 2 * e + 1 < kVec ? u[i][(2 * e + 1) % kVec] : v[i][(2 * e + 1) % kVec];
+          const float a = x * cs[e] - y * sn[e];
+          y = x * sn[e] + y * cs[e];
           x = a;
-          y = c;
-        }
-      } else {
-#pragma unroll
-        for (int i = 0; i < kVec; ++i) {
-          const float a = u[i] * cs[i] - v[i] * sn[i];
-          v[i] = u[i] * sn[i] + v[i] * cs[i];
-          u[i] = a;
         }
       }
+      Elems<kVec, T>::store(out + c0, u[i]);
+      if (second) Elems<kVec, T>::store(out + c1, v[i]);
     }
-    Elems<kVec, T>::store(out + c0, u);
-    if (second) Elems<kVec, T>::store(out + c1, v);
   }
 }
 
