@@ -11,16 +11,21 @@
 // of blocks.
 //   warp 0     TMA producer: per block of K (128 bytes: one 128-byte swizzle atom) the A box
 //              (128 rows) and the B box (kBN rows) into a ring of shared-memory stages.
-//   warp 1     owns TMEM; lane 0 issues four tcgen05.mma (kind::f8f6f4, M = 128, N = kBN,
-//              K = 32) a block into one of 512 / kBN accumulators, each block starting from 0.
-//   warps 2-3  with a scale for each row of b: bring a block's kBN scales into shared memory.
-//   warps 4-11 two warpgroups; each takes half of the tile's columns and keeps their sums in
-//              registers (kBN / 2 a thread, a thread owning one row), reading an accumulator
-//              with tcgen05.ld as its MMAs complete and handing it back before the fmas.
-//              At a tile's end they add the bias and write rows through shared memory.
-// While they add one block the MMAs of the next run: at kBN = 256 the MMAs of a block take
-// 512 cycles of the tensor pipe and the fmas 256 of the fp32 pipes (512 with a scale for
-// each row of b, which costs a multiplication more).
+//   warps 1-2  MMA issuers, taking blocks in turn: four tcgen05.mma (kind::f8f6f4, M = 128,
+//              N = kBN, K = 32) a block into one of 512 / kBN accumulators, from 0 each.
+//   warp 3     scales, four blocks at a time, two such batches in shared memory.
+//   warps 4-11 keep the tile's sums in registers, read each accumulator with tcgen05.ld as its
+//              MMAs complete, hand it back and add it with its scales; at a tile's end they
+//              add the bias and write.  With a scale for 128 rows of b a thread owns a row of
+//              half the columns and its scale is one number a block; with a scale for each
+//              row of b (kBRows) the accumulator is read in the 16x256b form, in which a
+//              thread holds two neighbouring columns of every eight and four rows: 32 column
+//              scales to read a block instead of 128.
+// At kBN = 256 a block's MMAs take 512 cycles of the tensor pipe.  Everything else has to stay
+// below that.  An issuer whose loop is uniform over the warp and elects a lane for the MMAs
+// alone takes half the time of a single thread's loop, whose descriptors have to be moved to
+// uniform registers after every wait; two of them hide the waits.  No register may spill: with
+// the shared memory taken, L1 is too small to hold them.
 //
 // bsa_fp8_rows_kernel, for up to 32 rows (tokens).  There the time is that of reading b
 // once.  A block of threads takes 16 rows of b, its warps an equal share of K's blocks each;
@@ -52,7 +57,8 @@ namespace {
 constexpr int kMThreads = 384;
 constexpr int kMB = 128;   // tile rows (TMEM lanes)
 constexpr int kKB = 128;   // block of K: bytes, products and scales
-constexpr int kPromoteWarp0 = 4, kPromoteWarps = 8;
+constexpr int kIssueWarp0 = 1, kIssuers = 2, kScaleWarp = 3, kPromoteWarp0 = 4, kPromoteWarps = 8;
+constexpr int kBatch = 4;  // blocks whose scales come together
 constexpr uint32_t kStgBytes = 2048;  // one warp's 32 rows of 64 bytes
 constexpr uint32_t kTmem = 512;
 
@@ -62,15 +68,19 @@ struct MmaCfg {
   static constexpr int kAcc = static_cast<int>(kTmem) / kBN;  // accumulators
   static constexpr uint32_t kABytes = kMB * kKB, kBBytes = kBN * kKB, kStageBytes = kABytes + kBBytes;
   static constexpr uint32_t kStg = kStages * kStageBytes;
-  static constexpr uint32_t kScale = kStg + kPromoteWarps * kStgBytes;  // [kAcc][kBN] fp32
-  static constexpr uint32_t kBar = kScale + kAcc * kBN * 4;
+  // a block's scales: of 128 rows of a and kBN rows of b, or their products for two halves
+  static constexpr int kScales = kMB + kBN;
+  static constexpr uint32_t kScale = kStg + kPromoteWarps * kStgBytes;  // [2][kBatch][kScales] fp32
+  static constexpr uint32_t kBar = kScale + 2 * kBatch * kScales * 4;
   // barriers: stage full, stage empty, accumulator full, accumulator empty, scales full, scales empty, final
   static constexpr int kFull = 0, kEmpty = kStages, kAccFull = 2 * kStages, kAccEmpty = kAccFull + kAcc,
-                       kScFull = kAccEmpty + kAcc, kScEmpty = kScFull + kAcc, kFinal = kScEmpty + kAcc,
+                       kScFull = kAccEmpty + kAcc, kScEmpty = kScFull + 2, kFinal = kScEmpty + 2,
                        kBars = kFinal + 1;
   static constexpr uint32_t kMisc = kBar + 8 * kBars;
   static constexpr uint32_t kAlloc = kMisc + 16 + 1024;  // + slack for 1024-byte alignment
   static_assert(kAlloc <= 227 * 1024, "shared memory budget");
+  static_assert(kScales >= 2 * kMB, "products of two halves");
+  static_assert(kIssuers <= kAcc, "an issuer's wait is never a phase behind");
   static_assert(kStageBytes % 1024 == 0, "swizzle atoms must stay 1024-byte aligned");
 };
 
@@ -106,15 +116,44 @@ __device__ __forceinline__ void mma_f8(uint32_t d_tmem, uint64_t a_desc, uint64_
 // MMAs.
 constexpr int kPolls = 64;
 template <int kRegion>
-__device__ __forceinline__ bool ready_warp(uint32_t bar, uint32_t parity, volatile int* abort_flag, uint64_t timeout_ns) {
+__device__ __forceinline__ bool ready(uint32_t bar, uint32_t parity, volatile int* abort_flag, uint64_t timeout_ns) {
   for (int i = 0; i < kPolls; ++i)
     if (__all_sync(0xffffffffu, ptx::mbar_try_wait(bar, parity))) return true;
   return wait_warp<kRegion>(bar, parity, abort_flag, timeout_ns);
 }
-__device__ __forceinline__ bool ready_one(uint32_t bar, uint32_t parity, volatile int* abort_flag, uint64_t timeout_ns) {
-  for (int i = 0; i < kPolls; ++i)
-    if (ptx::mbar_try_wait(bar, parity)) return true;
-  return wait_one(bar, parity, abort_flag, timeout_ns);
+
+// True in one lane of a converged warp.
+__device__ __forceinline__ bool elected() {
+  uint32_t p;
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "elect.sync _|p, 0xffffffff;\n\t"
+      "selp.u32 %0, 1, 0, p;\n\t}"
+      : "=r"(p));
+  return p != 0;
+}
+
+// 16 TMEM columns of this thread's lane (32x32b).
+__device__ __forceinline__ void tmem_ld16(uint32_t taddr, uint32_t (&r)[16]) {
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15}, [%16];"
+      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]),
+        "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
+      : "r"(taddr));
+}
+// 16 lanes of 32 TMEM columns (16x256b, four times): of columns 8 i + 2 (lane % 4), + 1 the
+// words 4 i, + 1 in row lane / 4 and 4 i + 2, + 3 in row lane / 4 + 8.
+__device__ __forceinline__ void tmem_ld_frag(uint32_t taddr, uint32_t (&r)[16]) {
+  asm volatile(
+      "tcgen05.ld.sync.aligned.16x256b.x4.b32 {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15}, [%16];"
+      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]),
+        "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
+      : "r"(taddr));
+}
+// Ties registers to the preceding tcgen05.wait::ld so their uses stay below it.
+__device__ __forceinline__ void reg_fence16(uint32_t (&r)[16]) {
+  asm volatile("" : "+r"(r[0]), "+r"(r[1]), "+r"(r[2]), "+r"(r[3]), "+r"(r[4]), "+r"(r[5]), "+r"(r[6]), "+r"(r[7]),
+               "+r"(r[8]), "+r"(r[9]), "+r"(r[10]), "+r"(r[11]), "+r"(r[12]), "+r"(r[13]), "+r"(r[14]), "+r"(r[15]));
 }
 
 // A unit of work: tile (m0, n0) over the blocks [k0, k1) of K.  Column tiles go fastest, so
@@ -134,6 +173,8 @@ __device__ __forceinline__ Unit unit_of(const MmaParams& p, int u) {
   return t;
 }
 
+// The roles below are run by whole warps (one loop, uniform over the warp); an elected lane
+// issues.
 template <int kBN>
 __device__ void mma_producer(const MmaParams& p, uint32_t smem, uint32_t bars, volatile int* abort_flag) {
   using C = MmaCfg<kBN>;
@@ -145,14 +186,17 @@ __device__ void mma_producer(const MmaParams& p, uint32_t smem, uint32_t bars, v
     for (int kb = t.k0; kb < t.k1; ++kb, ++it) {
       const uint32_t s = it % C::kStages;
       if (it >= C::kStages &&
-          !ready_one(bar_at(bars, C::kEmpty + s), ((it / C::kStages) - 1u) & 1u, abort_flag, p.timeout_ns)) {
+          !ready<0>(bar_at(bars, C::kEmpty + s), ((it / C::kStages) - 1u) & 1u, abort_flag, p.timeout_ns)) {
         alive = false;
         break;
       }
       const uint32_t full = bar_at(bars, C::kFull + s), dst = smem + s * C::kStageBytes;
-      ptx::mbar_arrive_expect_tx(full, C::kStageBytes);
-      ptx::tma_load_2d(dst, &p.tm_a, full, kb * kKB, t.m0, pol_a);
-      ptx::tma_load_2d(dst + C::kABytes, &p.tm_b, full, kb * kKB, t.n0, pol_b);
+      if (elected()) {
+        ptx::mbar_arrive_expect_tx(full, C::kStageBytes);
+        ptx::tma_load_2d(dst, &p.tm_a, full, kb * kKB, t.m0, pol_a);
+        ptx::tma_load_2d(dst + C::kABytes, &p.tm_b, full, kb * kKB, t.n0, pol_b);
+      }
+      __syncwarp();
     }
   }
   // the last load of each stage has landed before the CTA may exit
@@ -162,7 +206,8 @@ __device__ void mma_producer(const MmaParams& p, uint32_t smem, uint32_t bars, v
 }
 
 template <int kBN>
-__device__ void mma_issuer(const MmaParams& p, uint32_t smem, uint32_t bars, uint32_t tmem, volatile int* abort_flag) {
+__device__ void mma_issuer(const MmaParams& p, uint32_t smem, uint32_t bars, uint32_t tmem, uint32_t which,
+                           volatile int* abort_flag) {
   using C = MmaCfg<kBN>;
   // bits 4-5 D format (1 = fp32), 7-9 and 10-12 A and B formats, 17-22 N >> 3, 24-28 M >> 4
   const uint32_t idesc = (1u << 4) | static_cast<uint32_t>(p.idesc_formats) | (static_cast<uint32_t>(kBN >> 3) << 17) |
@@ -172,126 +217,158 @@ __device__ void mma_issuer(const MmaParams& p, uint32_t smem, uint32_t bars, uin
   for (int u = blockIdx.x; alive && u < p.units; u += gridDim.x) {
     const Unit t = unit_of<kBN>(p, u);
     for (int kb = t.k0; kb < t.k1; ++kb, ++it) {
+      if (it % kIssuers != which) continue;
       const uint32_t s = it % C::kStages, as = it % C::kAcc;
       if ((it >= C::kAcc &&
-           !ready_one(bar_at(bars, C::kAccEmpty + as), ((it / C::kAcc) - 1u) & 1u, abort_flag, p.timeout_ns)) ||
-          !ready_one(bar_at(bars, C::kFull + s), (it / C::kStages) & 1u, abort_flag, p.timeout_ns)) {
+           !ready<0>(bar_at(bars, C::kAccEmpty + as), ((it / C::kAcc) - 1u) & 1u, abort_flag, p.timeout_ns)) ||
+          !ready<0>(bar_at(bars, C::kFull + s), (it / C::kStages) & 1u, abort_flag, p.timeout_ns)) {
         alive = false;
         break;
       }
       ptx::tc_fence_after();
       const uint32_t sa = smem + s * C::kStageBytes;
       const uint64_t da = ptx::smem_desc_sw128(sa, 16), db = ptx::smem_desc_sw128(sa + C::kABytes, 16);
+      if (elected()) {
 #pragma unroll
-      for (int j = 0; j < kKB / 32; ++j) mma_f8(tmem + as * kBN, da + 2u * j, db + 2u * j, idesc, j > 0 ? 1u : 0u);
-      ptx::mma_commit(bar_at(bars, C::kEmpty + s));
-      ptx::mma_commit(bar_at(bars, C::kAccFull + as));
+        for (int j = 0; j < kKB / 32; ++j) mma_f8(tmem + as * kBN, da + 2u * j, db + 2u * j, idesc, j > 0 ? 1u : 0u);
+        ptx::mma_commit(bar_at(bars, C::kEmpty + s));
+        ptx::mma_commit(bar_at(bars, C::kAccFull + as));
+      }
+      __syncwarp();
     }
   }
-  ptx::mma_commit(bar_at(bars, C::kFinal));
+  // every MMA of this warp is done before TMEM is released (the elected lane is always the same)
+  if (elected()) ptx::mma_commit(bar_at(bars, C::kFinal));
+  __syncwarp();
   wait_force(bar_at(bars, C::kFinal), 0u, abort_flag, p.timeout_ns);
 }
 
-// Two warps bring each block's kBN scales of b's rows into the buffer of its accumulator.
-template <int kBN>
-__device__ void scale_loader(const MmaParams& p, uint8_t* smem_gen, uint32_t bars, int t64, volatile int* abort_flag) {
+// Brings the scales of kBatch blocks at a time: with a scale for 128 rows of b the products
+// with the 128 scales of a for both halves of the columns, else a's and then b's own.
+template <int kBN, bool kBRows>
+__device__ void scale_loader(const MmaParams& p, uint8_t* smem_gen, uint32_t bars, int lane, volatile int* abort_flag) {
   using C = MmaCfg<kBN>;
-  uint32_t it = 0;
+  constexpr int kHalf = kBN / 2, kNB = kBRows ? kBN / 32 : 2;
+  uint32_t bt = 0;
   for (int u = blockIdx.x; u < p.units; u += gridDim.x) {
     const Unit t = unit_of<kBN>(p, u);
-    for (int kb = t.k0; kb < t.k1; ++kb, ++it) {
-      const uint32_t as = it % C::kAcc;
-      float v[kBN / 64];
+    for (int k = t.k0; k < t.k1; k += kBatch, ++bt) {
+      const int n = min(kBatch, t.k1 - k);
+      float* dst = reinterpret_cast<float*>(smem_gen + C::kScale) + (bt & 1u) * (kBatch * C::kScales);
+      float a[kBatch][kMB / 32], b[kBatch][kBRows ? 1 : kNB];
 #pragma unroll
-      for (int i = 0; i < kBN / 64; ++i) {
-        const int n = t.n0 + i * 64 + t64;
-        v[i] = n < p.N ? __ldg(p.sb + static_cast<int64_t>(n) * p.kb + kb) : 0.f;
+      for (int i = 0; i < kMB / 32; ++i) {
+        const float* from = p.sa + static_cast<int64_t>(min(t.m0 + 32 * i + lane, p.M - 1) >> p.a_shift) * p.kb + k;
+#pragma unroll
+        for (int e = 0; e < kBatch; ++e) a[e][i] = e < n ? __ldg(from + e) : 0.f;
       }
-      if (it >= C::kAcc &&
-          !ready_warp<0>(bar_at(bars, C::kScEmpty + as), ((it / C::kAcc) - 1u) & 1u, abort_flag, p.timeout_ns))
-        return;
-      float* dst = reinterpret_cast<float*>(smem_gen + C::kScale) + as * kBN;
+      if constexpr (!kBRows) {
 #pragma unroll
-      for (int i = 0; i < kBN / 64; ++i) dst[i * 64 + t64] = v[i];
+        for (int h = 0; h < 2; ++h) {
+          const float* from = p.sb + static_cast<int64_t>(min(t.n0 + h * kHalf, p.N - 1) >> 7) * p.kb + k;
+#pragma unroll
+          for (int e = 0; e < kBatch; ++e) b[e][h] = e < n ? __ldg(from + e) : 0.f;
+        }
+      }
+      // b's own scales come 128 rows at a time, the first of them before the wait for the slot
+      float v[kBRows ? 4 : 1][kBatch];
+      auto load_b = [&](int i0) {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const float* from = p.sb + static_cast<int64_t>(min(t.n0 + 32 * (i0 + i) + lane, p.N - 1)) * p.kb + k;
+#pragma unroll
+          for (int e = 0; e < kBatch; ++e) v[i][e] = e < n ? __ldg(from + e) : 0.f;
+        }
+      };
+      if constexpr (kBRows) load_b(0);
+      if (bt >= 2 && !ready<0>(bar_at(bars, C::kScEmpty + (bt & 1u)), ((bt >> 1) - 1u) & 1u, abort_flag, p.timeout_ns))
+        return;
+      if constexpr (kBRows) {
+#pragma unroll
+        for (int i0 = 0; i0 < kNB; i0 += 4) {
+          if (i0 > 0) load_b(i0);
+#pragma unroll
+          for (int i = 0; i < 4; ++i)
+#pragma unroll
+            for (int e = 0; e < kBatch; ++e) dst[e * C::kScales + kMB + 32 * (i0 + i) + lane] = v[i][e];
+        }
+      }
+#pragma unroll
+      for (int e = 0; e < kBatch; ++e)
+#pragma unroll
+        for (int i = 0; i < kMB / 32; ++i) {
+          float* to = dst + e * C::kScales + 32 * i + lane;
+          if constexpr (kBRows) {
+            to[0] = a[e][i];
+          } else {
+            to[0] = a[e][i] * b[e][0];
+            to[kMB] = a[e][i] * b[e][1];
+          }
+        }
       __syncwarp();
-      if ((t64 & 31) == 0) ptx::mbar_arrive(bar_at(bars, C::kScFull + as));
+      if (lane == 0) ptx::mbar_arrive(bar_at(bars, C::kScFull + (bt & 1u)));
     }
   }
 }
 
 // Adds the blocks of this thread's row and half of the columns, and writes them.
-template <int kBN, bool kBRows>
+template <int kBN>
 __device__ void promoter(const MmaParams& p, uint8_t* smem_gen, uint32_t bars, uint32_t tmem, int warp, int lane,
                          volatile int* abort_flag) {
   using C = MmaCfg<kBN>;
-  constexpr int kCols = kBN / 2;
+  constexpr int kCols = kBN / 2, kGroups = kCols / 16;
   const int half = (warp - kPromoteWarp0) >> 2, quad = warp & 3;
   const uint32_t taddr = tmem + (static_cast<uint32_t>(quad * 32) << 16) + half * kCols;
   uint8_t* stg = smem_gen + C::kStg + (warp - kPromoteWarp0) * kStgBytes;
-  uint32_t it = 0;
+  const float* scales = reinterpret_cast<const float*>(smem_gen + C::kScale) + half * kMB + quad * 32 + lane;
+  uint32_t it = 0, bt = 0;
   for (int u = blockIdx.x; u < p.units; u += gridDim.x) {
     const Unit t = unit_of<kBN>(p, u);
-    const int row = t.m0 + quad * 32 + lane, col0 = t.n0 + half * kCols;
-    const float* sa = p.sa + static_cast<int64_t>(min(row, p.M - 1) >> p.a_shift) * p.kb;
-    const float* sb = p.sb + static_cast<int64_t>(min(col0, p.N - 1) >> 7) * p.kb;  // kBRows: unused
+    const int n = t.k1 - t.k0, col0 = t.n0 + half * kCols;
     uint64_t acc[kCols / 2];
 #pragma unroll
     for (int i = 0; i < kCols / 2; ++i) acc[i] = 0ull;
-    // An accumulator is read in groups of 32 columns, the next group (of the next block after
-    // the last) on its way while one is added.
-    constexpr int kGroups = kCols / 32;
+    // 16 columns at a time, the next 16 (of the next block after the last) on their way while
+    // some are added
     static_assert(kGroups % 2 == 0, "a block starts in the first buffer");
-    uint32_t r[2][32];
-    auto open = [&](uint32_t i) {  // waits for block i and starts reading its first group
-      const uint32_t as = i % C::kAcc, parity = (i / C::kAcc) & 1u;
-      if (kBRows && !ready_warp<1>(bar_at(bars, C::kScFull + as), parity, abort_flag, p.timeout_ns)) return false;
-      if (!ready_warp<1>(bar_at(bars, C::kAccFull + as), parity, abort_flag, p.timeout_ns)) return false;
+    uint32_t r[2][16];
+    auto open = [&](uint32_t i) {  // waits for block i and starts reading it
+      const uint32_t as = i % C::kAcc;
+      if (!ready<1>(bar_at(bars, C::kAccFull + as), (i / C::kAcc) & 1u, abort_flag, p.timeout_ns)) return false;
       ptx::tc_fence_after();
-      ptx::tmem_ld32(taddr + as * kBN, r[0]);
+      tmem_ld16(taddr + as * kBN, r[0]);
       return true;
     };
     if (!open(it)) return;
-    float next_a = __ldg(sa + t.k0), next_b = kBRows ? 1.f : __ldg(sb + t.k0);
-    for (int kb = t.k0; kb < t.k1; ++kb, ++it) {
+    for (int k = 0; k < n; ++k, ++it) {
       const uint32_t as = it % C::kAcc;
-      const float s = kBRows ? next_a : next_a * next_b;
-      if (kb + 1 < t.k1) {
-        next_a = __ldg(sa + kb + 1);
-        if (!kBRows) next_b = __ldg(sb + kb + 1);
-      }
+      if (k % kBatch == 0 && !ready<1>(bar_at(bars, C::kScFull + (bt & 1u)), (bt >> 1) & 1u, abort_flag, p.timeout_ns))
+        return;
+      const float s = scales[((bt & 1u) * kBatch + k % kBatch) * C::kScales];
       const uint64_t s2 = ptx::pack2(s, s);
-      const float4* sc = reinterpret_cast<const float4*>(smem_gen + C::kScale) + as * (kBN / 4) + half * (kCols / 4);
 #pragma unroll
       for (int g = 0; g < kGroups; ++g) {
         ptx::tmem_wait_ld();
-        ptx::reg_fence(r[g & 1]);
+        reg_fence16(r[g & 1]);
         if (g + 1 < kGroups) {
-          ptx::tmem_ld32(taddr + as * kBN + 32u * (g + 1), r[(g + 1) & 1]);
+          tmem_ld16(taddr + as * kBN + 16u * (g + 1), r[(g + 1) & 1]);
         } else {
           ptx::tc_fence_before();
           __syncwarp();
           if (lane == 0) ptx::mbar_arrive(bar_at(bars, C::kAccEmpty + as));
-          if (kb + 1 < t.k1 && !open(it + 1)) return;
+          if (k + 1 < n && !open(it + 1)) return;
         }
 #pragma unroll
-        for (int j = 0; j < 32; j += 4) {
-          const uint32_t(&x)[32] = r[g & 1];
-          uint64_t lo = ptx::pack2(__uint_as_float(x[j]), __uint_as_float(x[j + 1]));
-          uint64_t hi = ptx::pack2(__uint_as_float(x[j + 2]), __uint_as_float(x[j + 3]));
-          if constexpr (kBRows) {
-            const float4 b = sc[g * 8 + j / 4];
-            lo = ptx::fmul2(lo, ptx::pack2(b.x, b.y));
-            hi = ptx::fmul2(hi, ptx::pack2(b.z, b.w));
-          }
-          uint64_t& a0 = acc[(g * 32 + j) / 2];
-          uint64_t& a1 = acc[(g * 32 + j) / 2 + 1];
-          a0 = ptx::ffma2(lo, s2, a0);
-          a1 = ptx::ffma2(hi, s2, a1);
+        for (int j = 0; j < 8; ++j) {
+          const uint32_t(&x)[16] = r[g & 1];
+          acc[g * 8 + j] =
+              ptx::ffma2(ptx::pack2(__uint_as_float(x[2 * j]), __uint_as_float(x[2 * j + 1])), s2, acc[g * 8 + j]);
         }
       }
-      if constexpr (kBRows) {
+      if (k % kBatch == kBatch - 1 || k + 1 == n) {
         __syncwarp();
-        if (lane == 0) ptx::mbar_arrive(bar_at(bars, C::kScEmpty + as));
+        if (lane == 0) ptx::mbar_arrive(bar_at(bars, C::kScEmpty + (bt & 1u)));
+        ++bt;
       }
     }
     // ---- write: 64 bytes of each of the warp's 32 rows at a time, through shared memory
@@ -370,6 +447,121 @@ __device__ void promoter(const MmaParams& p, uint8_t* smem_gen, uint32_t bars, u
   }
 }
 
+// The same with a scale for each row of b: of every eight columns a thread has two, of rows
+// lane / 4, + 8, + 16 and + 24 of its warp's 32.
+template <int kBN>
+__device__ void promoter_rows(const MmaParams& p, uint8_t* smem_gen, uint32_t bars, uint32_t tmem, int warp, int lane,
+                              volatile int* abort_flag) {
+  using C = MmaCfg<kBN>;
+  constexpr int kCols = kBN / 2, kGroups = kCols / 32;
+  const int half = (warp - kPromoteWarp0) >> 2, quad = warp & 3;
+  const uint32_t taddr = tmem + (static_cast<uint32_t>(quad * 32) << 16) + half * kCols;
+  const float* scales = reinterpret_cast<const float*>(smem_gen + C::kScale);
+  uint32_t it = 0, bt = 0;
+  for (int u = blockIdx.x; u < p.units; u += gridDim.x) {
+    const Unit t = unit_of<kBN>(p, u);
+    const int n = t.k1 - t.k0;
+    // [32-column group][8-column group][upper or lower 16 rows][row, row + 8]
+    uint64_t acc[kGroups][4][2][2];
+#pragma unroll
+    for (int i = 0; i < kGroups * 16; ++i) (&acc[0][0][0][0])[i] = 0ull;
+    for (int k = 0; k < n; ++k, ++it) {
+      const uint32_t as = it % C::kAcc;
+      if (k % kBatch == 0 && !ready<1>(bar_at(bars, C::kScFull + (bt & 1u)), (bt >> 1) & 1u, abort_flag, p.timeout_ns))
+        return;
+      const float* sc = scales + ((bt & 1u) * kBatch + k % kBatch) * C::kScales;
+      uint64_t sa2[4];
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const float s = sc[quad * 32 + 8 * i + (lane >> 2)];
+        sa2[i] = ptx::pack2(s, s);
+      }
+      const float2* sb = reinterpret_cast<const float2*>(sc + kMB + half * kCols) + (lane & 3);
+      if (!ready<1>(bar_at(bars, C::kAccFull + as), (it / C::kAcc) & 1u, abort_flag, p.timeout_ns)) return;
+      ptx::tc_fence_after();
+#pragma unroll
+      for (int g = 0; g < kGroups; ++g) {
+        uint32_t r[2][16];
+        tmem_ld_frag(taddr + as * kBN + 32u * g, r[0]);
+        tmem_ld_frag(taddr + as * kBN + 32u * g + (16u << 16), r[1]);
+        float2 b[4];
+#pragma unroll
+        for (int c = 0; c < 4; ++c) b[c] = sb[(32 * g + 8 * c) / 2];
+        ptx::tmem_wait_ld();
+        reg_fence16(r[0]);
+        reg_fence16(r[1]);
+        if (g + 1 == kGroups) {
+          ptx::tc_fence_before();
+          __syncwarp();
+          if (lane == 0) ptx::mbar_arrive(bar_at(bars, C::kAccEmpty + as));
+        }
+#pragma unroll
+        for (int c = 0; c < 4; ++c) {
+          const uint64_t b2 = ptx::pack2(b[c].x, b[c].y);
+#pragma unroll
+          for (int h = 0; h < 2; ++h)
+#pragma unroll
+            for (int e = 0; e < 2; ++e) {
+              const uint64_t x = ptx::pack2(__uint_as_float(r[h][4 * c + 2 * e]), __uint_as_float(r[h][4 * c + 2 * e + 1]));
+              acc[g][c][h][e] = ptx::ffma2(ptx::fmul2(x, b2), sa2[2 * h + e], acc[g][c][h][e]);
+            }
+        }
+      }
+      if (k % kBatch == kBatch - 1 || k + 1 == n) {
+        __syncwarp();
+        if (lane == 0) ptx::mbar_arrive(bar_at(bars, C::kScEmpty + (bt & 1u)));
+        ++bt;
+      }
+    }
+    // four lanes write eight neighbouring columns of a row
+    const int esize = p.out_f32 ? 4 : 2;
+    uint8_t* out = static_cast<uint8_t*>(p.out) + t.split * p.split_stride * esize;
+    const bool pairs = (p.N & 1) == 0 && (reinterpret_cast<uintptr_t>(p.out) & 7u) == 0;
+#pragma unroll
+    for (int g = 0; g < kGroups; ++g)
+#pragma unroll
+      for (int c = 0; c < 4; ++c) {
+        const int col = t.n0 + half * kCols + 32 * g + 8 * c + 2 * (lane & 3);
+        float b0 = 0.f, b1 = 0.f;
+        if (p.bias != nullptr) {
+          if (col < p.N)
+            b0 = p.bias_f32 ? __ldg(static_cast<const float*>(p.bias) + col)
+                            : __bfloat162float(static_cast<const __nv_bfloat16*>(p.bias)[col]);
+          if (col + 1 < p.N)
+            b1 = p.bias_f32 ? __ldg(static_cast<const float*>(p.bias) + col + 1)
+                            : __bfloat162float(static_cast<const __nv_bfloat16*>(p.bias)[col + 1]);
+        }
+#pragma unroll
+        for (int h = 0; h < 2; ++h)
+#pragma unroll
+          for (int e = 0; e < 2; ++e) {
+            const int row = t.m0 + quad * 32 + 16 * h + 8 * e + (lane >> 2);
+            if (row >= p.M || col >= p.N) continue;
+            float v0, v1;
+            ptx::unpack2(acc[g][c][h][e], v0, v1);
+            v0 += b0;
+            v1 += b1;
+            const int64_t at = static_cast<int64_t>(row) * p.N + col;
+            if (p.out_f32) {
+              float* to = reinterpret_cast<float*>(out) + at;
+              if (pairs) *reinterpret_cast<float2*>(to) = make_float2(v0, v1);
+              else {
+                to[0] = v0;
+                if (col + 1 < p.N) to[1] = v1;
+              }
+            } else {
+              __nv_bfloat16* to = reinterpret_cast<__nv_bfloat16*>(out) + at;
+              if (pairs) *reinterpret_cast<uint32_t*>(to) = pack_bf16x2(v0, v1);
+              else {
+                to[0] = __float2bfloat16_rn(v0);
+                if (col + 1 < p.N) to[1] = __float2bfloat16_rn(v1);
+              }
+            }
+          }
+      }
+  }
+}
+
 template <int kBN, bool kBRows>
 __global__ void __launch_bounds__(kMThreads, 1) bsa_fp8_mma_kernel(const __grid_constant__ MmaParams p) {
   using C = MmaCfg<kBN>;
@@ -380,13 +572,12 @@ __global__ void __launch_bounds__(kMThreads, 1) bsa_fp8_mma_kernel(const __grid_
   volatile uint32_t* misc = reinterpret_cast<volatile uint32_t*>(smem + C::kMisc);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + C::kMisc + 4);
   const uint32_t bars = base + C::kBar;
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int warp = __shfl_sync(0xffffffffu, threadIdx.x >> 5, 0), lane = threadIdx.x & 31;
   if (threadIdx.x == 0) {
     for (int i = 0; i < C::kBars; ++i) {
       const bool acc_empty = i >= C::kAccEmpty && i < C::kAccEmpty + C::kAcc;
-      const bool sc_empty = i >= C::kScEmpty && i < C::kScEmpty + C::kAcc;
-      const bool sc_full = i >= C::kScFull && i < C::kScFull + C::kAcc;
-      ptx::mbar_init(bar_at(bars, i), acc_empty || sc_empty ? kPromoteWarps : sc_full ? 2u : 1u);
+      const bool sc_empty = i >= C::kScEmpty && i < C::kScEmpty + 2;
+      ptx::mbar_init(bar_at(bars, i), acc_empty || sc_empty ? kPromoteWarps : i == C::kFinal ? kIssuers : 1u);
     }
     *abort_flag = 0;
     ptx::fence_barrier_init();
@@ -404,17 +595,14 @@ __global__ void __launch_bounds__(kMThreads, 1) bsa_fp8_mma_kernel(const __grid_
   // the launch's 168 registers a thread, split: 128 * 56 + 256 * 216 <= 384 * 168
   if (warp < kPromoteWarp0) {
     ptx::setmaxnreg_dec<56>();
-    if (warp == 0) {
-      if (lane == 0) mma_producer<kBN>(p, base, bars, abort_flag);
-    } else if (warp == 1) {
-      if (lane == 0) mma_issuer<kBN>(p, base, bars, tmem, abort_flag);
-    } else if (kBRows) {
-      scale_loader<kBN>(p, smem, bars, static_cast<int>(threadIdx.x) - 64, abort_flag);
-    }
+    if (warp == 0) mma_producer<kBN>(p, base, bars, abort_flag);
+    else if (warp == kScaleWarp) scale_loader<kBN, kBRows>(p, smem, bars, lane, abort_flag);
+    else mma_issuer<kBN>(p, base, bars, tmem, static_cast<uint32_t>(warp - kIssueWarp0), abort_flag);
     __syncwarp();
   } else {
     ptx::setmaxnreg_inc<216>();
-    promoter<kBN, kBRows>(p, smem, bars, tmem, warp, lane, abort_flag);
+    if constexpr (kBRows) promoter_rows<kBN>(p, smem, bars, tmem, warp, lane, abort_flag);
+    else promoter<kBN>(p, smem, bars, tmem, warp, lane, abort_flag);
   }
   ptx::tc_fence_before();
   __syncthreads();
