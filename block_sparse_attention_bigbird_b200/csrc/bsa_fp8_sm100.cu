@@ -59,19 +59,25 @@ constexpr int kMB = 128;   // tile rows (TMEM lanes)
 constexpr int kKB = 128;   // block of K: bytes, products and scales
 constexpr int kIssueWarp0 = 1, kIssuers = 2, kScaleWarp = 3, kPromoteWarp0 = 4, kPromoteWarps = 8;
 constexpr int kBatch = 4;  // blocks whose scales come together
-constexpr uint32_t kStgBytes = 2048;  // one warp's 32 rows of 64 bytes
 constexpr uint32_t kTmem = 512;
 
-template <int kBN>
+template <int kBN, bool kBRows>
 struct MmaCfg {
-  static constexpr int kStages = kBN == 256 ? 4 : 6;
+  // With kBRows results leave from registers; else a warp's 32 rows of bf16 results have room
+  // in shared memory and leave by TMA while the next tile is added, for which a stage is given
+  // up (K is short where results are most of the bytes).
+  static constexpr int kStages = kBN == 256 ? (kBRows ? 4 : 3) : 5;
+  static constexpr uint32_t kStgBytes = kBRows ? 0 : 32 * (kBN / 2) * 2;  // a promoting warp's
   static constexpr int kAcc = static_cast<int>(kTmem) / kBN;  // accumulators
   static constexpr uint32_t kABytes = kMB * kKB, kBBytes = kBN * kKB, kStageBytes = kABytes + kBBytes;
   static constexpr uint32_t kStg = kStages * kStageBytes;
   // a block's scales: of 128 rows of a and kBN rows of b, or their products for two halves
-  static constexpr int kScales = kMB + kBN;
+  static constexpr int kScales = kBRows ? kMB + kBN : 2 * kMB;
   static constexpr uint32_t kScale = kStg + kPromoteWarps * kStgBytes;  // [2][kBatch][kScales] fp32
-  static constexpr uint32_t kBar = kScale + 2 * kBatch * kScales * 4;
+  // The bias of a unit's columns, brought with its first batch.  Batches run at most two ahead,
+  // so at most two units ahead of the one whose bias is read.
+  static constexpr uint32_t kBias = kScale + 2 * kBatch * kScales * 4;  // [4][kBN] fp32
+  static constexpr uint32_t kBar = kBias + (kBRows ? 0 : 4 * kBN * 4);
   // barriers: stage full, stage empty, accumulator full, accumulator empty, scales full, scales empty, final
   static constexpr int kFull = 0, kEmpty = kStages, kAccFull = 2 * kStages, kAccEmpty = kAccFull + kAcc,
                        kScFull = kAccEmpty + kAcc, kScEmpty = kScFull + 2, kFinal = kScEmpty + 2,
@@ -79,13 +85,14 @@ struct MmaCfg {
   static constexpr uint32_t kMisc = kBar + 8 * kBars;
   static constexpr uint32_t kAlloc = kMisc + 16 + 1024;  // + slack for 1024-byte alignment
   static_assert(kAlloc <= 227 * 1024, "shared memory budget");
-  static_assert(kScales >= 2 * kMB, "products of two halves");
   static_assert(kIssuers <= kAcc, "an issuer's wait is never a phase behind");
-  static_assert(kStageBytes % 1024 == 0, "swizzle atoms must stay 1024-byte aligned");
+  static_assert(kStageBytes % 1024 == 0 && kStgBytes % 1024 == 0, "swizzle atoms must stay 1024-byte aligned");
 };
 
 struct MmaParams {
   CUtensorMap tm_a, tm_b;
+  CUtensorMap tm_out;  // boxes of 128 bytes by 32 rows; unused where rows are not multiples of 16 bytes
+  int tma_out;
   const float *sa, *sb;
   const void* bias;
   void* out;
@@ -115,11 +122,17 @@ __device__ __forceinline__ void mma_f8(uint32_t d_tmem, uint64_t a_desc, uint64_
 // time) before they take the timed path, whose clock read and call cost more than a block's
 // MMAs.
 constexpr int kPolls = 64;
-template <int kRegion>
 __device__ __forceinline__ bool ready(uint32_t bar, uint32_t parity, volatile int* abort_flag, uint64_t timeout_ns) {
   for (int i = 0; i < kPolls; ++i)
     if (__all_sync(0xffffffffu, ptx::mbar_try_wait(bar, parity))) return true;
-  return wait_warp<kRegion>(bar, parity, abort_flag, timeout_ns);
+  return wait_warp(bar, parity, abort_flag, timeout_ns);
+}
+
+__device__ __forceinline__ void tma_store_3d(const void* map, uint32_t src, int x, int y, int z) {
+  asm volatile("cp.async.bulk.tensor.3d.global.shared::cta.bulk_group [%0, {%2, %3, %4}], [%1];" ::"l"(
+                   reinterpret_cast<uint64_t>(map)),
+               "r"(src), "r"(x), "r"(y), "r"(z)
+               : "memory");
 }
 
 // True in one lane of a converged warp.
@@ -175,9 +188,9 @@ __device__ __forceinline__ Unit unit_of(const MmaParams& p, int u) {
 
 // The roles below are run by whole warps (one loop, uniform over the warp); an elected lane
 // issues.
-template <int kBN>
+template <int kBN, bool kBRows>
 __device__ void mma_producer(const MmaParams& p, uint32_t smem, uint32_t bars, volatile int* abort_flag) {
-  using C = MmaCfg<kBN>;
+  using C = MmaCfg<kBN, kBRows>;
   const uint64_t pol_a = ptx::policy_evict_first(), pol_b = ptx::policy_evict_last();
   uint32_t it = 0;
   bool alive = true;
@@ -186,7 +199,7 @@ __device__ void mma_producer(const MmaParams& p, uint32_t smem, uint32_t bars, v
     for (int kb = t.k0; kb < t.k1; ++kb, ++it) {
       const uint32_t s = it % C::kStages;
       if (it >= C::kStages &&
-          !ready<0>(bar_at(bars, C::kEmpty + s), ((it / C::kStages) - 1u) & 1u, abort_flag, p.timeout_ns)) {
+          !ready(bar_at(bars, C::kEmpty + s), ((it / C::kStages) - 1u) & 1u, abort_flag, p.timeout_ns)) {
         alive = false;
         break;
       }
@@ -205,10 +218,10 @@ __device__ void mma_producer(const MmaParams& p, uint32_t smem, uint32_t bars, v
                p.timeout_ns);
 }
 
-template <int kBN>
+template <int kBN, bool kBRows>
 __device__ void mma_issuer(const MmaParams& p, uint32_t smem, uint32_t bars, uint32_t tmem, uint32_t which,
                            volatile int* abort_flag) {
-  using C = MmaCfg<kBN>;
+  using C = MmaCfg<kBN, kBRows>;
   // bits 4-5 D format (1 = fp32), 7-9 and 10-12 A and B formats, 17-22 N >> 3, 24-28 M >> 4
   const uint32_t idesc = (1u << 4) | static_cast<uint32_t>(p.idesc_formats) | (static_cast<uint32_t>(kBN >> 3) << 17) |
                          (static_cast<uint32_t>(kMB >> 4) << 24);
@@ -220,8 +233,8 @@ __device__ void mma_issuer(const MmaParams& p, uint32_t smem, uint32_t bars, uin
       if (it % kIssuers != which) continue;
       const uint32_t s = it % C::kStages, as = it % C::kAcc;
       if ((it >= C::kAcc &&
-           !ready<0>(bar_at(bars, C::kAccEmpty + as), ((it / C::kAcc) - 1u) & 1u, abort_flag, p.timeout_ns)) ||
-          !ready<0>(bar_at(bars, C::kFull + s), (it / C::kStages) & 1u, abort_flag, p.timeout_ns)) {
+           !ready(bar_at(bars, C::kAccEmpty + as), ((it / C::kAcc) - 1u) & 1u, abort_flag, p.timeout_ns)) ||
+          !ready(bar_at(bars, C::kFull + s), (it / C::kStages) & 1u, abort_flag, p.timeout_ns)) {
         alive = false;
         break;
       }
@@ -247,10 +260,10 @@ __device__ void mma_issuer(const MmaParams& p, uint32_t smem, uint32_t bars, uin
 // with the 128 scales of a for both halves of the columns, else a's and then b's own.
 template <int kBN, bool kBRows>
 __device__ void scale_loader(const MmaParams& p, uint8_t* smem_gen, uint32_t bars, int lane, volatile int* abort_flag) {
-  using C = MmaCfg<kBN>;
+  using C = MmaCfg<kBN, kBRows>;
   constexpr int kHalf = kBN / 2, kNB = kBRows ? kBN / 32 : 2;
-  uint32_t bt = 0;
-  for (int u = blockIdx.x; u < p.units; u += gridDim.x) {
+  uint32_t bt = 0, un = 0;
+  for (int u = blockIdx.x; u < p.units; u += gridDim.x, ++un) {
     const Unit t = unit_of<kBN>(p, u);
     for (int k = t.k0; k < t.k1; k += kBatch, ++bt) {
       const int n = min(kBatch, t.k1 - k);
@@ -281,8 +294,22 @@ __device__ void scale_loader(const MmaParams& p, uint8_t* smem_gen, uint32_t bar
         }
       };
       if constexpr (kBRows) load_b(0);
-      if (bt >= 2 && !ready<0>(bar_at(bars, C::kScEmpty + (bt & 1u)), ((bt >> 1) - 1u) & 1u, abort_flag, p.timeout_ns))
+      float bias[kBRows ? 1 : kBN / 32];
+      const bool first = !kBRows && k == t.k0 && p.bias != nullptr;
+      if (first)
+#pragma unroll
+        for (int i = 0; i < (kBRows ? 0 : kBN / 32); ++i) {
+          const int c = t.n0 + 32 * i + lane;
+          bias[i] = c >= p.N       ? 0.f
+                    : p.bias_f32 ? __ldg(static_cast<const float*>(p.bias) + c)
+                                 : __bfloat162float(static_cast<const __nv_bfloat16*>(p.bias)[c]);
+        }
+      if (bt >= 2 && !ready(bar_at(bars, C::kScEmpty + (bt & 1u)), ((bt >> 1) - 1u) & 1u, abort_flag, p.timeout_ns))
         return;
+      if (first)
+#pragma unroll
+        for (int i = 0; i < (kBRows ? 0 : kBN / 32); ++i)
+          reinterpret_cast<float*>(smem_gen + C::kBias)[(un & 3u) * kBN + 32 * i + lane] = bias[i];
       if constexpr (kBRows) {
 #pragma unroll
         for (int i0 = 0; i0 < kNB; i0 += 4) {
@@ -313,57 +340,61 @@ __device__ void scale_loader(const MmaParams& p, uint8_t* smem_gen, uint32_t bar
 
 // Adds the blocks of this thread's row and half of the columns, and writes them.
 template <int kBN>
-__device__ void promoter(const MmaParams& p, uint8_t* smem_gen, uint32_t bars, uint32_t tmem, int warp, int lane,
-                         volatile int* abort_flag) {
-  using C = MmaCfg<kBN>;
-  constexpr int kCols = kBN / 2, kGroups = kCols / 16;
+__device__ void promoter(const MmaParams& p, uint32_t smem, uint8_t* smem_gen, uint32_t bars, uint32_t tmem, int warp,
+                         int lane, volatile int* abort_flag) {
+  constexpr bool kBRows = false;
+  using C = MmaCfg<kBN, kBRows>;
+  constexpr int kCols = kBN / 2, kGroups = kCols / 32;
   const int half = (warp - kPromoteWarp0) >> 2, quad = warp & 3;
   const uint32_t taddr = tmem + (static_cast<uint32_t>(quad * 32) << 16) + half * kCols;
-  uint8_t* stg = smem_gen + C::kStg + (warp - kPromoteWarp0) * kStgBytes;
+  const uint32_t stg = C::kStg + (warp - kPromoteWarp0) * C::kStgBytes;
   const float* scales = reinterpret_cast<const float*>(smem_gen + C::kScale) + half * kMB + quad * 32 + lane;
-  uint32_t it = 0, bt = 0;
-  for (int u = blockIdx.x; u < p.units; u += gridDim.x) {
+  const float* bias = reinterpret_cast<const float*>(smem_gen + C::kBias) + half * kCols;
+  uint32_t it = 0, bt = 0, un = 0;
+  auto give_up = [&] {  // this warp's stores are done with their shared memory
+    if (lane == 0) ptx::bulk_wait_all();
+  };
+  for (int u = blockIdx.x; u < p.units; u += gridDim.x, ++un) {
     const Unit t = unit_of<kBN>(p, u);
     const int n = t.k1 - t.k0, col0 = t.n0 + half * kCols;
+    // the sums start from the bias, which came with the first scales
+    if (!ready(bar_at(bars, C::kScFull + (bt & 1u)), (bt >> 1) & 1u, abort_flag, p.timeout_ns)) return give_up();
     uint64_t acc[kCols / 2];
+    if (p.bias != nullptr) {
+      const float4* from = reinterpret_cast<const float4*>(bias + (un & 3u) * kBN);
 #pragma unroll
-    for (int i = 0; i < kCols / 2; ++i) acc[i] = 0ull;
-    // 16 columns at a time, the next 16 (of the next block after the last) on their way while
-    // some are added
-    static_assert(kGroups % 2 == 0, "a block starts in the first buffer");
-    uint32_t r[2][16];
-    auto open = [&](uint32_t i) {  // waits for block i and starts reading it
-      const uint32_t as = i % C::kAcc;
-      if (!ready<1>(bar_at(bars, C::kAccFull + as), (i / C::kAcc) & 1u, abort_flag, p.timeout_ns)) return false;
-      ptx::tc_fence_after();
-      tmem_ld16(taddr + as * kBN, r[0]);
-      return true;
-    };
-    if (!open(it)) return;
+      for (int i = 0; i < kCols / 4; ++i) {
+        const float4 b = from[i];
+        acc[2 * i] = ptx::pack2(b.x, b.y);
+        acc[2 * i + 1] = ptx::pack2(b.z, b.w);
+      }
+    } else {
+#pragma unroll
+      for (int i = 0; i < kCols / 2; ++i) acc[i] = 0ull;
+    }
     for (int k = 0; k < n; ++k, ++it) {
       const uint32_t as = it % C::kAcc;
-      if (k % kBatch == 0 && !ready<1>(bar_at(bars, C::kScFull + (bt & 1u)), (bt >> 1) & 1u, abort_flag, p.timeout_ns))
-        return;
+      if (k > 0 && k % kBatch == 0 && !ready(bar_at(bars, C::kScFull + (bt & 1u)), (bt >> 1) & 1u, abort_flag, p.timeout_ns))
+        return give_up();
       const float s = scales[((bt & 1u) * kBatch + k % kBatch) * C::kScales];
       const uint64_t s2 = ptx::pack2(s, s);
+      if (!ready(bar_at(bars, C::kAccFull + as), (it / C::kAcc) & 1u, abort_flag, p.timeout_ns)) return give_up();
+      ptx::tc_fence_after();
 #pragma unroll
       for (int g = 0; g < kGroups; ++g) {
+        uint32_t r[32];
+        ptx::tmem_ld32(taddr + as * kBN + 32u * g, r);
         ptx::tmem_wait_ld();
-        reg_fence16(r[g & 1]);
-        if (g + 1 < kGroups) {
-          tmem_ld16(taddr + as * kBN + 16u * (g + 1), r[(g + 1) & 1]);
-        } else {
+        ptx::reg_fence(r);
+        if (g + 1 == kGroups) {
           ptx::tc_fence_before();
           __syncwarp();
           if (lane == 0) ptx::mbar_arrive(bar_at(bars, C::kAccEmpty + as));
-          if (k + 1 < n && !open(it + 1)) return;
         }
 #pragma unroll
-        for (int j = 0; j < 8; ++j) {
-          const uint32_t(&x)[16] = r[g & 1];
-          acc[g * 8 + j] =
-              ptx::ffma2(ptx::pack2(__uint_as_float(x[2 * j]), __uint_as_float(x[2 * j + 1])), s2, acc[g * 8 + j]);
-        }
+        for (int j = 0; j < 16; ++j)
+          acc[g * 16 + j] =
+              ptx::ffma2(ptx::pack2(__uint_as_float(r[2 * j]), __uint_as_float(r[2 * j + 1])), s2, acc[g * 16 + j]);
       }
       if (k % kBatch == kBatch - 1 || k + 1 == n) {
         __syncwarp();
@@ -371,80 +402,76 @@ __device__ void promoter(const MmaParams& p, uint8_t* smem_gen, uint32_t bars, u
         ++bt;
       }
     }
-    // ---- write: 64 bytes of each of the warp's 32 rows at a time, through shared memory
-    // (16-byte chunk j of row r at chunk j ^ (r / 2 % 4), so that neither side conflicts)
+    // ---- the warp's 32 rows go through its shared memory, a bf16 row (or half an fp32 row) at
+    // a time, in boxes of 128 bytes a row: 16-byte chunk j of a box's row r at chunk j ^ (r % 8)
+    // (the 128-byte swizzle of the TMA store, and free of bank conflicts)
     const int esize = p.out_f32 ? 4 : 2;
-    uint8_t* out = static_cast<uint8_t*>(p.out) + t.split * p.split_stride * esize;
-    const bool whole = (static_cast<int64_t>(p.N) * esize) % 16 == 0 && (reinterpret_cast<uintptr_t>(p.out) & 15u) == 0;
-    auto put = [&](int c, int cols) {  // columns c .. c + cols of the tile's half are staged
-      __syncwarp();
-      const int n0 = col0 + c;
-#pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        const int r = i * 8 + (lane >> 2), j = lane & 3, m = t.m0 + quad * 32 + r;
-        const int per = cols / 4;  // elements of a 16-byte chunk
-        const uint4 w = *reinterpret_cast<const uint4*>(stg + r * 64 + ((j ^ ((r >> 1) & 3)) << 4));
-        const int n = n0 + j * per;
-        if (m >= p.M || n >= p.N) continue;
-        uint8_t* dst = out + (static_cast<int64_t>(m) * p.N + n) * esize;
-        if (whole) {
-          *reinterpret_cast<uint4*>(dst) = w;
-        } else if (p.out_f32) {
-          const uint32_t x[4] = {w.x, w.y, w.z, w.w};
-#pragma unroll
-          for (int e = 0; e < 4; ++e)
-            if (n + e < p.N) reinterpret_cast<uint32_t*>(dst)[e] = x[e];
-        } else {
-          const uint32_t x[4] = {w.x, w.y, w.z, w.w};
-#pragma unroll
-          for (int e = 0; e < 8; ++e)
-            if (n + e < p.N) reinterpret_cast<uint16_t*>(dst)[e] = static_cast<uint16_t>(x[e >> 1] >> ((e & 1) * 16));
+    const int row0 = t.m0 + quad * 32;
+    // writes the staged boxes of `cols` columns each from column c0 on, and hands them over
+    auto leave = [&](int c0, int boxes, int cols) {
+      if (p.tma_out) {
+        ptx::fence_proxy_async_smem();
+        __syncwarp();
+        if (lane == 0) {
+          for (int b = 0; b < boxes; ++b)
+            if (c0 + b * cols < p.N && row0 < p.M)
+              tma_store_3d(&p.tm_out, smem + stg + b * 4096u, c0 + b * cols, row0, t.split);
+          ptx::bulk_commit_group();
         }
+        return;
       }
+      __syncwarp();
+      uint8_t* out = static_cast<uint8_t*>(p.out) + t.split * p.split_stride * esize;
+      for (int b = 0; b < boxes; ++b)
+        for (int r = 0; r < 32 && row0 + r < p.M; ++r) {
+          const uint8_t* from = smem_gen + stg + b * 4096u + r * 128;
+          for (int e = lane; e < cols; e += 32) {
+            const int col = c0 + b * cols + e, at = e * esize;
+            if (col >= p.N) continue;
+            const uint8_t* x = from + (((at >> 4) ^ (r & 7)) << 4) + (at & 15);
+            uint8_t* to = out + (static_cast<int64_t>(row0 + r) * p.N + col) * esize;
+            if (p.out_f32) *reinterpret_cast<uint32_t*>(to) = *reinterpret_cast<const uint32_t*>(x);
+            else *reinterpret_cast<uint16_t*>(to) = *reinterpret_cast<const uint16_t*>(x);
+          }
+        }
       __syncwarp();
     };
+    uint8_t* mine = smem_gen + stg + lane * 128;
+    if (lane == 0) ptx::bulk_wait_read_all();  // the last tile's stores have read the room
+    __syncwarp();
+    if (p.out_f32) {
 #pragma unroll
-    for (int g = 0; g < kCols / 32; ++g) {
-      if (col0 + 32 * g >= p.N) break;
-      float v[32];
-#pragma unroll
-      for (int j = 0; j < 16; ++j) ptx::unpack2(acc[g * 16 + j], v[2 * j], v[2 * j + 1]);
-      if (p.bias != nullptr) {  // a lane loads one column's, all read them from shared memory
-        const int n = col0 + 32 * g + lane;
-        float b = 0.f;
-        if (n < p.N)
-          b = p.bias_f32 ? __ldg(static_cast<const float*>(p.bias) + n)
-                         : __bfloat162float(static_cast<const __nv_bfloat16*>(p.bias)[n]);
-        reinterpret_cast<float*>(stg)[lane] = b;
-        __syncwarp();
-#pragma unroll
-        for (int j = 0; j < 32; j += 4) {
-          const float4 b4 = reinterpret_cast<const float4*>(stg)[j / 4];
-          v[j] += b4.x, v[j + 1] += b4.y, v[j + 2] += b4.z, v[j + 3] += b4.w;
+      for (int h = 0; h < 2; ++h) {  // the room holds half the columns
+        if (h == 1) {
+          if (lane == 0) ptx::bulk_wait_read_all();
+          __syncwarp();
         }
-        __syncwarp();
-      }
-      uint8_t* mine = stg + lane * 64;
-      const int x = (lane >> 1) & 3;
-      if (p.out_f32) {
 #pragma unroll
-        for (int h = 0; h < 2; ++h) {
-#pragma unroll
-          for (int j = 0; j < 4; ++j)
-            *reinterpret_cast<float4*>(mine + ((j ^ x) << 4)) =
-                make_float4(v[h * 16 + 4 * j], v[h * 16 + 4 * j + 1], v[h * 16 + 4 * j + 2], v[h * 16 + 4 * j + 3]);
-          put(32 * g + 16 * h, 16);
+        for (int q = 0; q < kCols / 8; ++q) {
+          const int e = (h * kCols / 8 + q) * 2;
+          float4 v;
+          ptx::unpack2(acc[e], v.x, v.y);
+          ptx::unpack2(acc[e + 1], v.z, v.w);
+          *reinterpret_cast<float4*>(mine + (q / 8) * 4096 + (((q % 8) ^ (lane & 7)) << 4)) = v;
         }
-      } else {
-#pragma unroll
-        for (int j = 0; j < 4; ++j)
-          *reinterpret_cast<uint4*>(mine + ((j ^ x) << 4)) =
-              make_uint4(pack_bf16x2(v[8 * j], v[8 * j + 1]), pack_bf16x2(v[8 * j + 2], v[8 * j + 3]),
-                         pack_bf16x2(v[8 * j + 4], v[8 * j + 5]), pack_bf16x2(v[8 * j + 6], v[8 * j + 7]));
-        put(32 * g, 32);
+        leave(col0 + h * (kCols / 2), kCols / 64, 32);
       }
+    } else {
+#pragma unroll
+      for (int q = 0; q < kCols / 8; ++q) {
+        uint32_t w[4];
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          float lo, hi;
+          ptx::unpack2(acc[4 * q + e], lo, hi);
+          w[e] = pack_bf16x2(lo, hi);
+        }
+        *reinterpret_cast<uint4*>(mine + (q / 8) * 4096 + (((q % 8) ^ (lane & 7)) << 4)) = make_uint4(w[0], w[1], w[2], w[3]);
+      }
+      leave(col0, kCols / 64, 64);
     }
   }
+  give_up();
 }
 
 // The same with a scale for each row of b: of every eight columns a thread has two, of rows
@@ -452,7 +479,8 @@ __device__ void promoter(const MmaParams& p, uint8_t* smem_gen, uint32_t bars, u
 template <int kBN>
 __device__ void promoter_rows(const MmaParams& p, uint8_t* smem_gen, uint32_t bars, uint32_t tmem, int warp, int lane,
                               volatile int* abort_flag) {
-  using C = MmaCfg<kBN>;
+  constexpr bool kBRows = true;
+  using C = MmaCfg<kBN, kBRows>;
   constexpr int kCols = kBN / 2, kGroups = kCols / 32;
   const int half = (warp - kPromoteWarp0) >> 2, quad = warp & 3;
   const uint32_t taddr = tmem + (static_cast<uint32_t>(quad * 32) << 16) + half * kCols;
@@ -467,7 +495,7 @@ __device__ void promoter_rows(const MmaParams& p, uint8_t* smem_gen, uint32_t ba
     for (int i = 0; i < kGroups * 16; ++i) (&acc[0][0][0][0])[i] = 0ull;
     for (int k = 0; k < n; ++k, ++it) {
       const uint32_t as = it % C::kAcc;
-      if (k % kBatch == 0 && !ready<1>(bar_at(bars, C::kScFull + (bt & 1u)), (bt >> 1) & 1u, abort_flag, p.timeout_ns))
+      if (k % kBatch == 0 && !ready(bar_at(bars, C::kScFull + (bt & 1u)), (bt >> 1) & 1u, abort_flag, p.timeout_ns))
         return;
       const float* sc = scales + ((bt & 1u) * kBatch + k % kBatch) * C::kScales;
       uint64_t sa2[4];
@@ -477,7 +505,7 @@ __device__ void promoter_rows(const MmaParams& p, uint8_t* smem_gen, uint32_t ba
         sa2[i] = ptx::pack2(s, s);
       }
       const float2* sb = reinterpret_cast<const float2*>(sc + kMB + half * kCols) + (lane & 3);
-      if (!ready<1>(bar_at(bars, C::kAccFull + as), (it / C::kAcc) & 1u, abort_flag, p.timeout_ns)) return;
+      if (!ready(bar_at(bars, C::kAccFull + as), (it / C::kAcc) & 1u, abort_flag, p.timeout_ns)) return;
       ptx::tc_fence_after();
 #pragma unroll
       for (int g = 0; g < kGroups; ++g) {
@@ -564,7 +592,7 @@ __device__ void promoter_rows(const MmaParams& p, uint8_t* smem_gen, uint32_t ba
 
 template <int kBN, bool kBRows>
 __global__ void __launch_bounds__(kMThreads, 1) bsa_fp8_mma_kernel(const __grid_constant__ MmaParams p) {
-  using C = MmaCfg<kBN>;
+  using C = MmaCfg<kBN, kBRows>;
   extern __shared__ uint8_t smem_raw[];
   const uint32_t raw = ptx::smem_addr(smem_raw);
   const uint32_t base = (raw + 1023u) & ~1023u;
@@ -592,17 +620,15 @@ __global__ void __launch_bounds__(kMThreads, 1) bsa_fp8_mma_kernel(const __grid_
   __syncthreads();
   ptx::tc_fence_after();
   const uint32_t tmem = misc[0];
-  // the launch's 168 registers a thread, split: 128 * 56 + 256 * 216 <= 384 * 168
+  // 384 threads have 168 registers each, which the adding warps use nearly in full
   if (warp < kPromoteWarp0) {
-    ptx::setmaxnreg_dec<56>();
-    if (warp == 0) mma_producer<kBN>(p, base, bars, abort_flag);
+    if (warp == 0) mma_producer<kBN, kBRows>(p, base, bars, abort_flag);
     else if (warp == kScaleWarp) scale_loader<kBN, kBRows>(p, smem, bars, lane, abort_flag);
-    else mma_issuer<kBN>(p, base, bars, tmem, static_cast<uint32_t>(warp - kIssueWarp0), abort_flag);
+    else mma_issuer<kBN, kBRows>(p, base, bars, tmem, static_cast<uint32_t>(warp - kIssueWarp0), abort_flag);
     __syncwarp();
   } else {
-    ptx::setmaxnreg_inc<216>();
     if constexpr (kBRows) promoter_rows<kBN>(p, smem, bars, tmem, warp, lane, abort_flag);
-    else promoter<kBN>(p, smem, bars, tmem, warp, lane, abort_flag);
+    else promoter<kBN>(p, base, smem, bars, tmem, warp, lane, abort_flag);
   }
   ptx::tc_fence_before();
   __syncthreads();
@@ -782,6 +808,18 @@ bool map_codes(CUtensorMap* m, const void* ptr, uint64_t rows, uint64_t cols, ui
             CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
+// The result [splits, M, N] of esize-byte elements, boxes of 128 bytes by 32 rows.
+bool map_result(CUtensorMap* m, void* ptr, uint64_t splits, uint64_t rows, uint64_t cols, int f32) {
+  auto fn = encode_fn();
+  if (fn == nullptr) return false;
+  const uint64_t esize = f32 ? 4 : 2;
+  const cuuint64_t dims[3] = {cols, rows, splits}, strides[2] = {cols * esize, rows * cols * esize};
+  const cuuint32_t box[3] = {static_cast<cuuint32_t>(128 / esize), 32, 1}, estr[3] = {1, 1, 1};
+  return fn(m, f32 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT32 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, ptr, dims, strides, box,
+            estr, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_NONE,
+            CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
 // Per device, once: whether it is an sm_100 part, its SM count, and the kernels' shared-
 // memory attributes set.  A failed setup is not cached.
 constexpr int kMaxFp8Devices = 64;
@@ -791,7 +829,7 @@ std::mutex g_fp8_mu;
 template <int kBN, bool kBRows>
 bool allow_smem() {
   return cudaFuncSetAttribute(bsa_fp8_mma_kernel<kBN, kBRows>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                              static_cast<int>(MmaCfg<kBN>::kAlloc)) == cudaSuccess;
+                              static_cast<int>(MmaCfg<kBN, kBRows>::kAlloc)) == cudaSuccess;
 }
 
 int fp8_device_sms() {
@@ -848,8 +886,8 @@ int format_bits(int type) { return type == BSA_E5M2 ? 1 : 0; }
 
 template <int kBN>
 void launch_mma(const MmaParams& p, int grid, cudaStream_t s) {
-  if (p.b_rows) bsa_fp8_mma_kernel<kBN, true><<<grid, kMThreads, MmaCfg<kBN>::kAlloc, s>>>(p);
-  else bsa_fp8_mma_kernel<kBN, false><<<grid, kMThreads, MmaCfg<kBN>::kAlloc, s>>>(p);
+  if (p.b_rows) bsa_fp8_mma_kernel<kBN, true><<<grid, kMThreads, MmaCfg<kBN, true>::kAlloc, s>>>(p);
+  else bsa_fp8_mma_kernel<kBN, false><<<grid, kMThreads, MmaCfg<kBN, false>::kAlloc, s>>>(p);
 }
 
 }  // namespace
@@ -946,6 +984,8 @@ int bsa_fp8_matmul(const void* a, int a_type, int64_t lda, const float* a_scale,
   p.out_f32 = split || out_f32;
   p.bias = split ? nullptr : bias;
   p.bias_f32 = bias_f32;
+  p.tma_out = aligned16(p.out) && static_cast<int64_t>(N) * type_bytes(p.out_f32 ? BSA_FP32 : BSA_BF16) % 16 == 0;
+  if (p.tma_out && !map_result(&p.tm_out, p.out, plan.splits, M, N, p.out_f32)) return BSA_ERR_CUDA;
   const int grid = static_cast<int>(std::min<int64_t>(units, sms));
   if (plan.bn == 256) launch_mma<256>(p, grid, s);
   else launch_mma<128>(p, grid, s);
