@@ -9,6 +9,7 @@ from __future__ import annotations
 
 import ctypes
 import os
+import struct
 from typing import Optional
 
 import numpy as np
@@ -104,9 +105,8 @@ _SIGNATURES = {
     "bsa_rope_free": (None, [ctypes.c_void_p]),
     "bsa_rope_apply": (ctypes.c_int, [ctypes.c_void_p, ctypes.c_void_p, ctypes.c_int, ctypes.c_void_p,
                                       ctypes.c_void_p, ctypes.c_int, ctypes.c_int, ctypes.c_int, ctypes.c_int,
-                                      ctypes.c_int, ctypes.POINTER(ctypes.c_int64), ctypes.c_void_p, ctypes.c_int,
-                                      ctypes.POINTER(ctypes.c_int64), ctypes.c_void_p, ctypes.c_int,
-                                      ctypes.c_void_p]),
+                                      ctypes.c_int, ctypes.c_void_p, ctypes.c_void_p, ctypes.c_int,
+                                      ctypes.c_void_p, ctypes.c_void_p, ctypes.c_int, ctypes.c_void_p]),
     "bsa_block_norm": (ctypes.c_int, [ctypes.POINTER(BlockNormArgs), ctypes.c_void_p, ctypes.c_void_p,
                                       ctypes.c_void_p, ctypes.c_void_p, ctypes.c_void_p, ctypes.c_void_p]),
     "bsa_block_norm_backward_workspace_bytes": (ctypes.c_int, [ctypes.POINTER(BlockNormArgs),
@@ -498,11 +498,17 @@ def _type_of(dtype) -> Optional[int]:
     return _type_codes.get(dtype)
 
 
+_current_raw = None
+
+
 def _raw_stream(index: int) -> int:
     """The current stream's pointer (without building a stream object, where torch allows)."""
-    import torch
-    raw = getattr(torch._C, "_cuda_getCurrentRawStream", None)
-    return raw(index) if raw is not None else torch.cuda.current_stream(index).cuda_stream
+    global _current_raw
+    if _current_raw is None:
+        import torch
+        _current_raw = getattr(torch._C, "_cuda_getCurrentRawStream",
+                               lambda i: torch.cuda.current_stream(i).cuda_stream)
+    return _current_raw(index)
 
 
 def _on(device, stream, call):
@@ -589,8 +595,11 @@ def bsa_rope_table(rope: Rope):
             np.ctypeslib.as_array(ctypes.cast(f, ctypes.POINTER(ctypes.c_double)), n).copy())
 
 
-_Strides3 = ctypes.c_int64 * 3
-_Strides12 = ctypes.c_int64 * 12
+_pack3, _pack12 = struct.Struct("3q").pack, struct.Struct("12q").pack  # host int64 arrays
+
+
+def _columns_lie(t, d: int) -> bool:
+    return d == 1 or t.stride(3) == 1
 
 
 def bsa_rope_apply(q, k, positions, rope: Rope, inverse: bool = False, q_out=None, k_out=None, stream=None):
@@ -601,60 +610,61 @@ def bsa_rope_apply(q, k, positions, rope: Rope, inverse: bool = False, q_out=Non
     [axes, B, L].  ``inverse`` turns back (the gradient).  Results are new contiguous tensors,
     or q_out and k_out, which may be q and k themselves; other overlaps are not allowed.
     """
-    import torch
-    B, H, L, d = q.shape if q.dim() == 4 else (0, 0, 0, 0)
-    ty, pt = _type_of(q.dtype), _type_of(positions.dtype)
-    if q.dim() != 4 or ty not in (BF16, FP16, FP32) or not q.is_cuda or (d > 1 and q.stride(3) != 1):
+    device, dtype = q.device, q.dtype
+    ty, pt = _type_of(dtype), _type_of(positions.dtype)
+    if q.dim() != 4 or ty not in (BF16, FP16, FP32) or device.type != "cuda" or not _columns_lie(q, q.shape[3]):
         raise ValueError("q must be a bf16, fp16 or fp32 CUDA tensor [B, H, L, d] with contiguous columns")
-    if k is not None and (k.dim() != 4 or k.dtype != q.dtype or k.shape[0] != B or k.shape[2] != L or
-                          k.shape[3] != d or (d > 1 and k.stride(3) != 1)):
-        raise ValueError("k must be like q, [B, Hk, L, d]")
-    if pt not in (INT32, INT64, FP32) or positions.dim() not in (2, 3) or positions.shape[0] < rope.n_axes or \
-            positions.shape[-1] != L or (positions.dim() == 3 and positions.shape[1] != B):
-        raise ValueError(f"positions must be int32, int64 or fp32 [axes, L] or [axes, B, L] with at least "
-                         f"{rope.n_axes} axes")
-    device = q.device
-    if positions.device != device or (k is not None and k.device != device):
-        raise ValueError("q, k and positions must be on one device")
+    B, H, L, d = q.shape
+    Hk = 0
+    if k is not None:
+        if k.dim() != 4 or k.dtype is not dtype or k.shape[0] != B or k.shape[2] != L or k.shape[3] != d or \
+                not _columns_lie(k, d) or k.device != device:
+            raise ValueError("k must be like q, [B, Hk, L, d]")
+        Hk = k.shape[1]
+    pd = positions.dim()
+    if pt not in (INT32, INT64, FP32) or pd not in (2, 3) or positions.shape[0] < rope.n_axes or \
+            positions.shape[-1] != L or (pd == 3 and positions.shape[1] != B) or positions.device != device:
+        raise ValueError(f"positions must be int32, int64 or fp32 [axes, L] or [axes, B, L] on q's device with at "
+                         f"least {rope.n_axes} axes")
     for name, t, src in (("q_out", q_out, q), ("k_out", k_out, k)):
-        if t is not None and (src is None or t.dtype != q.dtype or t.shape != src.shape or t.device != device or
-                              (d > 1 and t.stride(3) != 1) or
-                              any(n > 1 and s == 0 for n, s in zip(t.shape, t.stride()))):
+        if t is not None and (src is None or t.dtype is not dtype or t.shape != src.shape or t.device != device or
+                              not _columns_lie(t, d) or any(n > 1 and s == 0 for n, s in zip(t.shape, t.stride()))):
             raise ValueError(f"{name} must have its input's type and shape, contiguous columns and no shared rows")
 
     def call(ptr):
         qo = q.new_empty((B, H, L, d)) if q_out is None else q_out
-        ko = k_out
-        if k is not None and k_out is None:
-            ko = k.new_empty(k.shape)
-        ks = (0,) * 6 if k is None else (*k.stride()[:3], *ko.stride()[:3])
+        a, b, c, _ = q.stride()
+        e, f, g, _ = qo.stride()
+        ko, kp, kop, ks = k_out, None, None, (0, 0, 0, 0, 0, 0)
+        if k is not None:
+            if ko is None:
+                ko = k.new_empty((B, Hk, L, d))
+            ks = k.stride()[:3] + ko.stride()[:3]
+            kp, kop = k.data_ptr(), ko.data_ptr()
         ps = positions.stride()
-        _check(lib.bsa_rope_apply(q.data_ptr(), qo.data_ptr(), H, _ptr(k), _ptr(ko), 0 if k is None else k.shape[1],
-                                  B, L, d, ty, _Strides12(*q.stride()[:3], *qo.stride()[:3], *ks),
-                                  positions.data_ptr(), pt,
-                                  _Strides3(ps[0], ps[1] if len(ps) == 3 else 0, ps[-1]), rope.handle, int(inverse),
-                                  ptr), "bsa_rope_apply")
+        _check(lib.bsa_rope_apply(q.data_ptr(), qo.data_ptr(), H, kp, kop, Hk, B, L, d, ty,
+                                  _pack12(a, b, c, e, f, g, *ks), positions.data_ptr(), pt,
+                                  _pack3(ps[0], ps[1] if pd == 3 else 0, ps[-1]), rope._h, inverse, ptr),
+               "bsa_rope_apply")
         return qo, ko
-    return _on(q.device, stream, call)
+    return _on(device, stream, call)
 
 
 # ---------------------------------------------------------------- norms and residual of a block
 def _norm_args(x, y, post, post_weight, post_bias, gate, branch_scale, stream_scale, pre, pre_weight, pre_bias, eps):
-    ty = _type_of(x.dtype)
-    if ty not in (BF16, FP16, FP32) or not x.is_cuda or not x.is_contiguous() or x.dim() < 1 or x.shape[-1] < 1:
+    ty, device, shape = _type_of(x.dtype), x.device, x.shape
+    if ty not in (BF16, FP16, FP32) or device.type != "cuda" or not x.is_contiguous() or not shape or shape[-1] < 1:
         raise ValueError("x must be a contiguous bf16, fp16 or fp32 CUDA tensor [.., C]")
-    C = x.shape[-1]
-    B = x.shape[0] if x.dim() > 1 else 1
+    C = shape[-1]
+    B = shape[0] if len(shape) > 1 else 1
     if post not in NORMS or pre not in NORMS:
         raise ValueError('post and pre must be "rms", "layer" or None')
-    if y is not None and (y.shape != x.shape or y.dtype != x.dtype or not y.is_contiguous()):
+    if y is not None and (y.shape != shape or y.dtype is not x.dtype or not y.is_contiguous() or y.device != device):
         raise ValueError("y must be like x")
     if y is None and (post is not None or gate is not None or pre is None or branch_scale != 1.0 or
                       stream_scale != 1.0):
         raise ValueError("without y there is the pre norm alone")
-    device, pt, gate_rows = x.device, None, 1
-    if y is not None and y.device != device:
-        raise ValueError("y is on another device than x")
+    pt, gate_rows = None, 1
     for name, t in (("post_weight", post_weight), ("post_bias", post_bias), ("gate", gate),
                     ("pre_weight", pre_weight), ("pre_bias", pre_bias)):
         if t is None:

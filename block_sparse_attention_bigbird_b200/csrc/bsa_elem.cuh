@@ -45,6 +45,38 @@ __device__ __forceinline__ uint32_t pack(float lo, float hi, __half) {
   return *reinterpret_cast<const uint32_t*>(&v);
 }
 
+// kVec elements as they lie in memory, in words.
+template <int kVec, typename T>
+struct RawElems {
+  static constexpr int kWords = (kVec * static_cast<int>(sizeof(T)) + 3) / 4;
+  uint32_t w[kWords];
+  __device__ __forceinline__ void load(const T* p) {
+    if constexpr (kVec == 1) {
+      if constexpr (sizeof(T) == 4) w[0] = *reinterpret_cast<const uint32_t*>(p);
+      else w[0] = *reinterpret_cast<const uint16_t*>(p);
+    } else {
+      static_assert(kWords % 4 == 0, "whole 16-byte words");
+#pragma unroll
+      for (int i = 0; i < kWords / 4; ++i) {
+        const uint4 a = reinterpret_cast<const uint4*>(p)[i];
+        w[4 * i] = a.x, w[4 * i + 1] = a.y, w[4 * i + 2] = a.z, w[4 * i + 3] = a.w;
+      }
+    }
+  }
+  __device__ __forceinline__ void widen(float (&v)[kVec]) const {
+    if constexpr (sizeof(T) == 4) {
+#pragma unroll
+      for (int i = 0; i < kVec; ++i) v[i] = __uint_as_float(w[i]);
+    } else if constexpr (kVec == 1) {
+      float hi;
+      unpack(w[0], T(), v[0], hi);
+    } else {
+#pragma unroll
+      for (int i = 0; i < kWords; ++i) unpack(w[i], T(), v[2 * i], v[2 * i + 1]);
+    }
+  }
+};
+
 // kVec consecutive elements; kVec = 8 needs a 16-byte aligned address, 2 one of two elements.
 template <int kVec, typename T>
 struct Elems {

@@ -13,7 +13,7 @@
 // element.  The sines are the costly part (about 60 instructions a pair), so a thread keeps
 // the angles of eight pairs of one token and walks over heads with them.  It reads the
 // pairs' two halves as two 16-byte vectors.  The heads are cut into groups (blockIdx.y) of
-// at least four until the card is filled eight times over, so that the last wave is short;
+// at least twelve while the card is filled more than once, so that the last wave is short;
 // with one token a call a thread takes one head.
 #include <cuda_runtime.h>
 
@@ -23,6 +23,7 @@
 #include <vector>
 
 #include "bsa_elem.cuh"
+#include "sm100_ptx.cuh"
 
 struct bsa_rope {
   std::vector<int32_t> axis;
@@ -36,7 +37,9 @@ namespace {
 constexpr int kMaxPairs = 128;
 constexpr int kMaxAxes = 8;
 constexpr int kRopeThreads = 128;
-constexpr int kBatch = 4;  // heads a thread has on their way at once
+// Heads a thread has on their way at once: their raw words take 32 registers.
+template <typename T, int kVec>
+constexpr int kBatchOf = kVec == 1 ? 4 : sizeof(T) == 2 ? 4 : 2;
 
 struct RopeParams {
   double turns[kMaxPairs];  // frequency in turns per position
@@ -63,7 +66,7 @@ __device__ __forceinline__ double position(const RopeParams& p, int axis, int b,
 }
 
 template <typename T, int kVec, bool kAdj>
-__global__ void __launch_bounds__(kRopeThreads) bsa_rope_kernel(const __grid_constant__ RopeParams p) {
+__global__ void __launch_bounds__(kRopeThreads, 6) bsa_rope_kernel(const __grid_constant__ RopeParams p) {
   const int64_t idx = static_cast<int64_t>(blockIdx.x) * kRopeThreads + threadIdx.x;
   const int64_t tok = idx / p.units;
   const int unit = static_cast<int>(idx - tok * p.units);
@@ -99,18 +102,19 @@ __global__ void __launch_bounds__(kRopeThreads) bsa_rope_kernel(const __grid_con
       sn[i] *= p.sign;
     }
   }
+  constexpr int kBatch = kBatchOf<T, kVec>;
   // kBatch heads' loads are issued before the first store, which the compiler could not move
   // them over (the results may lie where the inputs are)
   for (int first = h0; first < h1; first += kBatch) {
-    float u[kBatch][kVec], v[kBatch][kVec];
+    RawElems<kVec, T> ru[kBatch], rv[kBatch];
 #pragma unroll
     for (int i = 0; i < kBatch; ++i) {
       const int h = first + i;
       if (h >= h1) break;
       const int w = h >= p.heads[0], hh = w ? h - p.heads[0] : h;
       const T* in = static_cast<const T*>(p.in[w]) + b * p.is[w][0] + hh * p.is[w][1] + l * p.is[w][2];
-      Elems<kVec, T>::load(in + c0, u[i]);
-      if (second) Elems<kVec, T>::load(in + c1, v[i]);
+      ru[i].load(in + c0);
+      if (second) rv[i].load(in + c1);
     }
 #pragma unroll
     for (int i = 0; i < kBatch; ++i) {
@@ -118,19 +122,31 @@ __global__ void __launch_bounds__(kRopeThreads) bsa_rope_kernel(const __grid_con
       if (h >= h1) break;
       const int w = h >= p.heads[0], hh = w ? h - p.heads[0] : h;
       T* out = static_cast<T*>(p.out[w]) + b * p.os[w][0] + hh * p.os[w][1] + l * p.os[w][2];
-      if (turn) {
+      float u[kVec], v[kVec];
+      ru[i].widen(u);
+      rv[i].widen(v);
+      if (turn && !kAdj && kVec > 1) {
+#pragma unroll
+        for (int e = 0; e + 1 < kVec; e += 2) {  // two pairs at a time
+          const uint64_t x = ptx::pack2(u[e], u[e + 1]), y = ptx::pack2(v[e], v[e + 1]);
+          const uint64_t c2 = ptx::pack2(cs[e], cs[e + 1]), s2 = ptx::pack2(sn[e], sn[e + 1]);
+          const uint64_t n2 = ptx::pack2(-sn[e], -sn[e + 1]);
+          ptx::unpack2(ptx::ffma2(y, n2, ptx::fmul2(x, c2)), u[e], u[e + 1]);
+          ptx::unpack2(ptx::ffma2(y, c2, ptx::fmul2(x, s2)), v[e], v[e + 1]);
+        }
+      } else if (turn) {
 #pragma unroll
         for (int e = 0; e < kVec; ++e) {
           // kAdj: the 2 kVec columns hold kVec pairs side by side
-          float& x = !kAdj ? u[i][e] : 2 * e < kVec ? u[i][(2 * e) % kVec] : v[i][(2 * e) % kVec];
-          float& y = !kAdj ? v[i][e] : 2 * e + 1 < kVec ? u[i][(2 * e + 1) % kVec] : v[i][(2 * e + 1) % kVec];
+          float& x = !kAdj ? u[e] : 2 * e < kVec ? u[(2 * e) % kVec] : v[(2 * e) % kVec];
+          float& y = !kAdj ? v[e] : 2 * e + 1 < kVec ? u[(2 * e + 1) % kVec] : v[(2 * e + 1) % kVec];
           const float a = x * cs[e] - y * sn[e];
           y = x * sn[e] + y * cs[e];
           x = a;
         }
       }
-      Elems<kVec, T>::store(out + c0, u[i]);
-      if (second) Elems<kVec, T>::store(out + c1, v[i]);
+      Elems<kVec, T>::store(out + c0, u);
+      if (second) Elems<kVec, T>::store(out + c1, v);
     }
   }
 }
@@ -146,10 +162,11 @@ void launch_rope(const RopeParams& p, bool vec, bool adj, dim3 grid, cudaStream_
   }
 }
 
-// Threads that fill the card (148 SMs x 2048) once, up to where heads are cut singly, and
-// eight times, up to where they are cut into groups of four or more.
+// Threads that fill the card (148 SMs x 2048) once, up to where heads are cut singly; up to
+// eight times they are cut into groups of twelve or more (B = 4, L = 16384, 12 + 12 heads of
+// 64: groups of 24, 12, 8, 6 and 4 took 76, 73, 74, 80 and 82 us).
 constexpr int64_t kRopeFill = 148 * 2048;
-constexpr int64_t kRopeGroup = 4;
+constexpr int64_t kRopeGroup = 12;
 
 }  // namespace
 }  // namespace bsa
