@@ -11,9 +11,10 @@
 // Blocks are persistent.  A thread brings its own pieces of the rows to come into shared
 // memory with cp.async, up to three rows ahead, and reads back only what it brought, so that
 // no barrier is needed and the loads in flight do not depend on the warps that fit.  What a
-// column multiplies by (weights, gate, the scales) stays in registers from row to row, and the
-// arithmetic is done on pairs (fma.rn.f32x2): with both the instructions a row stay well
-// below what the SM issues in the time its bytes take.
+// column multiplies by (weights, gate, the scales) stays in registers from row to row (in the
+// backward, whose sums need the registers, in shared memory), and the arithmetic is done on
+// pairs (fma.rn.f32x2): with both the instructions a row stay well below what the SM issues
+// in the time its bytes take.
 //
 // Backward, with D the gradient of the stream by both its uses:
 //     a  = dnormed w_pre,  D = dstream + r (a - mean(a) - xh mean(a xh)),   dx = beta D,
@@ -23,9 +24,9 @@
 //     S = sum D yh, T = sum D  (over the rows of one gate row),
 //     P = sum dnormed xh, Q = sum dnormed,
 // because dgate = alpha (w_post S + b_post T), dw_post = alpha sum_b g_b S_b,
-// db_post = alpha sum_b g_b T_b, dw_pre = P, db_pre = Q.  A block keeps them in registers
-// over its contiguous rows (every thread owns fixed columns), adds its teams' sums in shared
-// memory when the gate row changes or its rows end, and writes them to slot
+// db_post = alpha sum_b g_b T_b, dw_pre = P, db_pre = Q.  A block (one an SM, so that there are
+// few partial sums) keeps them in registers over its contiguous rows, adds its teams' sums in
+// shared memory when the gate row changes or its rows end, and writes them to slot
 // (block + gate row), which no two (block, gate row) pairs share.  A second kernel adds the
 // slots in a fixed order.
 //
@@ -85,14 +86,14 @@ template <int kVec, int kNV, bool kWarp>
 struct Cols {
   static constexpr int kE = kVec * kNV;
   int C, team_threads, t;
-  uint32_t in;  // bit i: piece i lies in the row
-  __device__ __forceinline__ Cols(int C_, int team_, int t_) : C(C_), team_threads(team_), t(t_), in(0) {
+  bool in[kNV];  // piece i lies in the row
+  __device__ __forceinline__ Cols(int C_, int team_, int t_) : C(C_), team_threads(team_), t(t_) {
 #pragma unroll
-    for (int i = 0; i < kNV; ++i) in |= at(i) < C ? 1u << i : 0u;
+    for (int i = 0; i < kNV; ++i) in[i] = at(i) < C;
   }
   __device__ __forceinline__ int team() const { return kWarp ? 32 : team_threads; }
   __device__ __forceinline__ int at(int i) const { return (i * team() + t) * kVec; }
-  __device__ __forceinline__ bool has(int i) const { return in >> i & 1u; }
+  __device__ __forceinline__ bool has(int i) const { return in[i]; }
   // a parameter's values at these columns (`dflt` where it is absent), 0 past the row's end
   template <typename T>
   __device__ __forceinline__ void param(const void* p, int64_t row, bool f32, float dflt, float (&v)[kE]) const {
@@ -114,12 +115,13 @@ struct Cols {
   __device__ __forceinline__ void store(T* mine, const Pairs<kE>& x) const {  // mine: at column at(0) of the row
     float v[kE];
     x.get(v);
+    const int step = team() * kVec;
 #pragma unroll
-    for (int i = 0; i < kNV; ++i) {
+    for (int i = 0; i < kNV; ++i, mine += step) {
       float e[kVec];
 #pragma unroll
       for (int j = 0; j < kVec; ++j) e[j] = v[i * kVec + j];
-      if (has(i)) Elems<kVec, T>::store(mine + i * team() * kVec, e);
+      if (has(i)) Elems<kVec, T>::store(mine, e);
     }
   }
   // x where a piece is inside the row, else 0
@@ -149,14 +151,62 @@ struct TeamSum {
 #pragma unroll
         for (int i = 0; i < kN; ++i) b[i * 32 + w] = v[i];
       asm volatile("bar.sync %0, %1;" ::"r"(bar_id), "r"(team_threads) : "memory");
+      // lanes read the warps' values, repeated over a power of two of lanes
+      int top = 1;
+      while (top < nw) top <<= 1;
+      const int at = lane & (top - 1);
 #pragma unroll
       for (int i = 0; i < kN; ++i) {
-        float s = lane < nw ? b[i * 32 + lane] : 0.f;
-#pragma unroll
-        for (int o = 16; o > 0; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
+        float s = at < nw ? b[i * 32 + at] : 0.f;
+        for (int o = top >> 1; o > 0; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
         v[i] = s;
       }
     }
+  }
+};
+
+// A float for each column in shared memory, in the order that a team's threads read without
+// bank conflicts: thread by thread, at most four floats of a piece at a time.
+template <int kVec, int kNV, bool kWarp>
+struct ColBuf {
+  static constexpr int kE = kVec * kNV, kW = kVec < 4 ? kVec : 4, kS = kVec / kW;
+  float* base;
+  __device__ __forceinline__ float* at(const Cols<kVec, kNV, kWarp>& cols, int i, int h) const {
+    return base + ((i * kS + h) * cols.team() + cols.t) * kW;
+  }
+  __device__ __forceinline__ void store(const Cols<kVec, kNV, kWarp>& cols, const Pairs<kE>& x) const {
+    float v[kE];
+    x.get(v);
+#pragma unroll
+    for (int i = 0; i < kNV; ++i)
+#pragma unroll
+      for (int h = 0; h < kS; ++h) {
+        const float* f = v + i * kVec + h * kW;
+        float* to = at(cols, i, h);
+        if constexpr (kW == 4) *reinterpret_cast<float4*>(to) = make_float4(f[0], f[1], f[2], f[3]);
+        else if constexpr (kW == 2) *reinterpret_cast<float2*>(to) = make_float2(f[0], f[1]);
+        else to[0] = f[0];
+      }
+  }
+  __device__ __forceinline__ void load(const Cols<kVec, kNV, kWarp>& cols, Pairs<kE>& x) const {
+    float v[kE];
+#pragma unroll
+    for (int i = 0; i < kNV; ++i)
+#pragma unroll
+      for (int h = 0; h < kS; ++h) {
+        float* f = v + i * kVec + h * kW;
+        const float* from = at(cols, i, h);
+        if constexpr (kW == 4) {
+          const float4 q = *reinterpret_cast<const float4*>(from);
+          f[0] = q.x, f[1] = q.y, f[2] = q.z, f[3] = q.w;
+        } else if constexpr (kW == 2) {
+          const float2 q = *reinterpret_cast<const float2*>(from);
+          f[0] = q.x, f[1] = q.y;
+        } else {
+          f[0] = from[0];
+        }
+      }
+    x.set(v);
   }
 };
 
@@ -185,7 +235,10 @@ __device__ __forceinline__ float2 statistics(Pairs<kVec * kNV>& v, int kind, con
   return make_float2(mean, 1.f / sqrtf(fmaf(s[0], p.inv_c, p.eps)));
 }
 
-constexpr int kWarpBlock = 128;  // threads of a block whose teams are warps
+constexpr int kWarpBlock = 128;  // threads of a forward block whose teams are warps
+// Threads of a backward block at most: where a thread has more than eight elements of a row
+// (in teams of a warp) it needs 168 registers, else 128 do.
+constexpr int kBackBlock = 512, kBackWarpBlock = 384;
 
 __device__ __forceinline__ uint4 lds16(uint32_t a) {
   uint4 v;
@@ -211,7 +264,7 @@ __device__ __forceinline__ uint16_t lds2(uint32_t a) {
 // Rows on their way to this thread: kNA arrays, kNV pieces of kVec elements of each, `depth`
 // slots.  Rows come in the order of the fetches, `stride` bytes apart.  Pieces of two bytes
 // (an odd row of 16-bit elements) are copied at once instead.
-template <typename T, int kVec, int kNV, int kNA, bool kWarpTeam>
+template <typename T, int kVec, int kNV, int kNA, bool kWarpTeam, int kBlock>
 struct Ring {
   static constexpr int kBytes = kVec * static_cast<int>(sizeof(T));
   static constexpr int kPiece = kBytes > 16 ? 16 : kBytes;
@@ -221,7 +274,7 @@ struct Ring {
   uint32_t base, slot_bytes, cur, nxt;  // shared-memory addresses of this thread's pieces
   int depth;
   __device__ __forceinline__ uint32_t gap() const {  // between a thread's pieces in shared memory
-    return (kWarpTeam ? kWarpBlock : blockDim.x) * kPiece;
+    return (kBlock > 0 ? kBlock : blockDim.x) * kPiece;
   }
   __device__ __forceinline__ void init(uint32_t smem, const Cols<kVec, kNV, kWarpTeam>& cols, int64_t row, int64_t step,
                                        int slots, const void* const (&from)[kNA]) {
@@ -241,27 +294,30 @@ struct Ring {
   }
   // starts bringing the next row (nothing if it is not `there`) into the next slot, as one group
   __device__ __forceinline__ void fetch(const Cols<kVec, kNV, kWarpTeam>& cols, bool there) {
+    const uint32_t g = gap();
+    const int step = cols.team() * kBytes;
 #pragma unroll
     for (int a = 0; a < kNA; ++a) {
       if (src[a] == nullptr) continue;
-      if (there)
+      if (there) {
+        const char* p = src[a];
+        uint32_t dst = nxt + a * kNV * kSplit * g;
 #pragma unroll
-        for (int i = 0; i < kNV; ++i) {
+        for (int i = 0; i < kNV; ++i, p += step, dst += kSplit * g) {
           if (!cols.has(i)) continue;
-          const char* p = src[a] + static_cast<int64_t>(i) * cols.team() * kBytes;
-          const uint32_t dst = nxt + (a * kNV + i) * kSplit * gap();
           if constexpr (kBytes < 4) {
             asm volatile("st.shared.u16 [%0], %1;" ::"r"(dst), "h"(*reinterpret_cast<const uint16_t*>(p)) : "memory");
           } else {
 #pragma unroll
             for (int h = 0; h < kSplit; ++h) {
               if constexpr (kPiece == 16)
-                asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst + h * gap()), "l"(p + 16 * h) : "memory");
+                asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst + h * g), "l"(p + 16 * h) : "memory");
               else
                 asm volatile("cp.async.ca.shared.global [%0], [%1], %2;" ::"r"(dst), "l"(p), "n"(kPiece) : "memory");
             }
           }
         }
+      }
       src[a] += stride;
     }
     asm volatile("cp.async.commit_group;" ::: "memory");
@@ -278,10 +334,11 @@ struct Ring {
   // that is not there
   __device__ __forceinline__ void read(const Cols<kVec, kNV, kWarpTeam>& cols, int a, Pairs<kVec * kNV>& to) const {
     float v[kVec * kNV];
+    const uint32_t g = gap();
+    uint32_t at = cur + a * kNV * kSplit * g;
 #pragma unroll
-    for (int i = 0; i < kNV; ++i) {
+    for (int i = 0; i < kNV; ++i, at += kSplit * g) {
       float e[kVec] = {};
-      const uint32_t at = cur + (a * kNV + i) * kSplit * gap();
       if (src[a] != nullptr && cols.has(i)) {
         if constexpr (kBytes == 2) {
           const uint16_t w = lds2(at);
@@ -300,7 +357,7 @@ struct Ring {
           unpack(w.z, T(), e[4], e[5]);
           unpack(w.w, T(), e[6], e[7]);
         } else {
-          const uint4 w = lds16(at), z = lds16(at + gap());
+          const uint4 w = lds16(at), z = lds16(at + g);
           e[0] = __uint_as_float(w.x), e[1] = __uint_as_float(w.y), e[2] = __uint_as_float(w.z), e[3] = __uint_as_float(w.w);
           e[4] = __uint_as_float(z.x), e[5] = __uint_as_float(z.y), e[6] = __uint_as_float(z.z), e[7] = __uint_as_float(z.w);
         }
@@ -322,7 +379,7 @@ __global__ void __launch_bounds__(kWarpTeam ? 128 : 512, kWarpTeam ? 4 : 1) bsa_
   const Cols<kVec, kNV, kWarpTeam> cols(p.C, team_threads, t);
   const int step = gridDim.x * teams, rows = static_cast<int>(p.rows);  // rows and steps fit 31 bits
   int row = blockIdx.x * teams + team;
-  Ring<T, kVec, kNV, 2, kWarpTeam> ring;
+  Ring<T, kVec, kNV, 2, kWarpTeam, kWarpTeam ? kWarpBlock : 0> ring;
   ring.init(ptx::smem_addr(smem) + teams * 256, cols, row, step, p.depth, {p.x, p.y});
   int64_t ahead = row;  // the next row to fetch
   for (int d = 0; d + 1 < p.depth; ++d, ahead += step) ring.fetch(cols, ahead < rows);
@@ -401,75 +458,94 @@ __global__ void __launch_bounds__(kWarpTeam ? 128 : 512, kWarpTeam ? 4 : 1) bsa_
 }
 
 // kMeans: a layer norm takes part or biases have gradients (the plain means, T and Q are kept).
-template <typename T, int kVec, int kNV, bool kWarpTeam, bool kMeans>
-__global__ void __launch_bounds__(kWarpTeam ? 128 : 512, kWarpTeam ? 2 : 1) bsa_block_norm_back_kernel(const __grid_constant__ NormParams p,
-                                                                                    int team_threads) {
+// kBlock: threads of the block at most.
+template <typename T, int kVec, int kNV, bool kWarpTeam, bool kMeans, int kBlock>
+__global__ void __launch_bounds__(kBlock, 1) bsa_block_norm_back_kernel(const __grid_constant__ NormParams p,
+                                                                        int team_threads) {
   constexpr int kE = kVec * kNV, kP = kE / 2;
   constexpr int kN = kMeans ? 2 : 1;
-  extern __shared__ __align__(16) uint8_t smem[];  // [C] sums, the teams' reduction areas, the ring
-  float* sums = reinterpret_cast<float*>(smem);
+  extern __shared__ __align__(16) uint8_t smem[];  // three column buffers, the reduction areas, the ring
   const int teams = blockDim.x / team_threads, team = threadIdx.x / team_threads, t = threadIdx.x % team_threads;
-  const int cpad = (p.C + 3) / 4 * 4;
-  TeamSum<kN, kWarpTeam> sum{sums + cpad + team * (2 * kN * 32), team_threads, 1 + team};
   const Cols<kVec, kNV, kWarpTeam> cols(p.C, team_threads, t);
+  float* buf = reinterpret_cast<float*>(smem);
+  const int width = kE * cols.team();
+  // the teams' sums; pre weight; branch_scale gate post_weight of the gate row at hand
+  const ColBuf<kVec, kNV, kWarpTeam> sums{buf}, wpre{buf + width}, coef{buf + 2 * width};
+  TeamSum<kN, kWarpTeam> sum{buf + 3 * width + team * (2 * kN * 32), team_threads, 1 + team};
   // rows fit 31 bits
   const int r0 = static_cast<int>(blockIdx.x * p.rows_per_block);
   const int r1 = static_cast<int>(min(blockIdx.x * p.rows_per_block + p.rows_per_block, p.rows));
   const bool f32 = p.params_f32 != 0;
   const bool pre_layer = p.pre == BSA_NORM_LAYER, post_layer = p.post == BSA_NORM_LAYER;
 
-  Pairs<kE> accP{}, accS{}, wpre, coef;
-  Pairs<kMeans ? kE : 2> accQ{}, accT{};
-  {
-    float w[kE];
-    cols.template param<T>(p.pre_w, 0, f32, 1.f, w);
-    wpre.set(w);
-  }
-  // adds the teams' x in shared memory and writes it to C floats at `to`
-  auto flush = [&](const Pairs<kE>& x, float* to) {
-    float v[kE];
-    x.get(v);
-    for (int k = 0; k < teams; ++k) {
-      if (team == k) {
-#pragma unroll
-        for (int i = 0; i < kNV; ++i) {
-          const int c = cols.at(i);
-          if (c < p.C)
-#pragma unroll
-            for (int j = 0; j < kVec; ++j) sums[c + j] = k == 0 ? v[i * kVec + j] : sums[c + j] + v[i * kVec + j];
-        }
-      }
-      __syncthreads();
-    }
-    for (int c = threadIdx.x; c < p.C; c += blockDim.x) to[c] = sums[c];
-    __syncthreads();
-  };
   // The block's rows go round its teams; a team's rows are one sequence for the ring, cut
   // where the gate row changes.
   int64_t row = r0 + team, ahead = row;
-  Ring<T, kVec, kNV, 4, kWarpTeam> ring;
-  ring.init(ptx::smem_addr(smem) + (cpad + teams * 2 * kN * 32) * static_cast<uint32_t>(sizeof(float)), cols, row,
+  Ring<T, kVec, kNV, 4, kWarpTeam, 0> ring;
+  ring.init(ptx::smem_addr(smem) + (3 * width + teams * 2 * kN * 32) * static_cast<uint32_t>(sizeof(float)), cols, row,
             teams, p.depth, {p.dstream, p.y, p.dnormed == nullptr ? nullptr : p.x, p.dnormed});
   for (int d = 0; d + 1 < p.depth; ++d, ahead += teams) ring.fetch(cols, ahead < r1);
   T* dx = static_cast<T*>(p.dx) + row * p.C + cols.at(0);
   T* dy = static_cast<T*>(p.dy) + row * p.C + cols.at(0);
   const float4* saved = reinterpret_cast<const float4*>(p.saved);
   const int stride = teams * p.C;
+  float4 st_next = make_float4(0.f, 0.f, 0.f, 0.f);
+  if (row < r1) st_next = __ldg(saved + row);
+
+  Pairs<kE> accP{}, accS{};
+  Pairs<kMeans ? kE : 2> accQ{}, accT{};
+  if (team == 0) {
+    float w[kE];
+    Pairs<kE> x;
+    cols.template param<T>(p.pre_w, 0, f32, 1.f, w);
+    x.set(w);
+    wpre.store(cols, x);
+  }
+  // adds the teams' x in shared memory, in their order; the last writes the columns at `to`
+  auto flush = [&](Pairs<kE> x, float* to) {
+    for (int k = 0; k < teams; ++k) {
+      if (team == k) {
+        if (k > 0) {
+          Pairs<kE> before;
+          sums.load(cols, before);
+#pragma unroll
+          for (int e = 0; e < kP; ++e) x.v[e] = ptx::fadd2(before.v[e], x.v[e]);
+        }
+        if (k + 1 < teams) {
+          sums.store(cols, x);
+        } else {
+          float v[kE];
+          x.get(v);
+#pragma unroll
+          for (int i = 0; i < kNV; ++i)
+#pragma unroll
+            for (int j = 0; j < kVec; ++j)
+              if (cols.has(i)) to[cols.at(i) + j] = v[i * kVec + j];
+        }
+      }
+      __syncthreads();
+    }
+  };
   for (int64_t s0 = r0; s0 < r1;) {
     const int64_t gate_row = s0 / p.per_gate;
     const int64_t s1 = min(static_cast<int64_t>(r1), (gate_row + 1) * p.per_gate);
-    {
+    __syncthreads();  // all teams are done with the last gate row's
+    if (team == 0) {
       float w[kE], g[kE];
+      Pairs<kE> x;
       cols.template param<T>(p.post_w, 0, f32, 1.f, w);
       cols.template param<T>(p.gate, gate_row, f32, 1.f, g);
 #pragma unroll
       for (int e = 0; e < kE; ++e) w[e] *= p.alpha * g[e];
-      coef.set(w);
+      x.set(w);
+      coef.store(cols, x);
     }
+    __syncthreads();
     for (; row < s1; row += teams, dx += stride, dy += stride) {
       ring.fetch(cols, ahead < r1);
       ahead += teams;
-      const float4 st = __ldg(saved + row);
+      const float4 st = st_next;
+      if (row + teams < r1) st_next = __ldg(saved + row + teams);
       ring.wait();
       Pairs<kE> D;
       ring.read(cols, 0, D);
@@ -479,13 +555,15 @@ __global__ void __launch_bounds__(kWarpTeam ? 128 : 512, kWarpTeam ? 2 : 1) bsa_
         ring.read(cols, 3, a);
         const uint64_t r2 = twice(st.w);
         uint64_t m0 = 0ull, m1 = 0ull;
+        Pairs<kE> w;
+        wpre.load(cols, w);
 #pragma unroll
         for (int e = 0; e < kP; ++e) {
           if constexpr (kMeans) xh.v[e] = ptx::fadd2(xh.v[e], cols.inside(e, -st.z));
           xh.v[e] = ptx::fmul2(xh.v[e], r2);
           accP.v[e] = ptx::ffma2(a.v[e], xh.v[e], accP.v[e]);
           if constexpr (kMeans) accQ.v[e] = ptx::fadd2(accQ.v[e], a.v[e]);
-          a.v[e] = ptx::fmul2(a.v[e], wpre.v[e]);
+          a.v[e] = ptx::fmul2(a.v[e], w.v[e]);
           m0 = ptx::ffma2(a.v[e], xh.v[e], m0);
           if constexpr (kMeans) m1 = ptx::fadd2(m1, a.v[e]);
         }
@@ -509,8 +587,9 @@ __global__ void __launch_bounds__(kWarpTeam ? 128 : 512, kWarpTeam ? 2 : 1) bsa_
         cols.store(dx, o);
       }
       if (p.y != nullptr) {
-        Pairs<kE> yh;
+        Pairs<kE> yh, w;
         ring.read(cols, 1, yh);
+        coef.load(cols, w);
         const uint64_t r2 = twice(p.post != BSA_NORM_NONE ? st.y : 1.f);
         uint64_t m0 = 0ull, m1 = 0ull;
 #pragma unroll
@@ -519,7 +598,7 @@ __global__ void __launch_bounds__(kWarpTeam ? 128 : 512, kWarpTeam ? 2 : 1) bsa_
           yh.v[e] = ptx::fmul2(yh.v[e], r2);
           accS.v[e] = ptx::ffma2(D.v[e], yh.v[e], accS.v[e]);
           if constexpr (kMeans) accT.v[e] = ptx::fadd2(accT.v[e], D.v[e]);
-          D.v[e] = ptx::fmul2(D.v[e], coef.v[e]);
+          D.v[e] = ptx::fmul2(D.v[e], w.v[e]);
           m0 = ptx::ffma2(D.v[e], yh.v[e], m0);
           if constexpr (kMeans) m1 = ptx::fadd2(m1, D.v[e]);
         }
@@ -581,13 +660,36 @@ __device__ __forceinline__ void param_put(void* p, int64_t i, int type, float v)
   else static_cast<__half*>(p)[i] = from_f32<__half>(v);
 }
 
+// Sums of slots first, first + step, .. < n of one column (two quantities C apart each): eight
+// slots are on their way at once.
+__device__ __forceinline__ void sum_slots(const float* from, int64_t n, int first, int step, int C, int means, float& a,
+                                          float& b) {
+  const int64_t stride = static_cast<int64_t>(1 + means) * C;
+  for (int64_t k = first; k < n; k += 8 * step) {
+    float x[8], y[8];
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      const bool there = k + i * step < n;
+      const float* q = from + (k + i * step) * stride;
+      x[i] = there ? __ldg(q) : 0.f;
+      y[i] = there && means ? __ldg(q + C) : 0.f;
+    }
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      a += x[i];
+      b += y[i];
+    }
+  }
+}
+
 // Adds the slots: 32 columns a block, 32 lanes (warps) a column.
 __global__ void __launch_bounds__(1024) bsa_block_norm_sum_kernel(const SumParams p) {
   __shared__ float buf[4][32][33];
   const int lane = threadIdx.x, ty = threadIdx.y;
   const int c = blockIdx.x * 32 + lane;
   const bool in = c < p.C;
-  float dw = 0.f, db = 0.f;
+  float dw = 0.f, db = 0.f, P = 0.f, Q = 0.f;
+  if (p.has_pre && in) sum_slots(p.part_pre + c, p.blocks, ty, 32, p.C, p.means, P, Q);
   if (p.has_y) {
     // lane group `bb` of the 32 / lanes_per_gate takes gate rows bb, bb + groups, ...; its
     // lanes share the slots of one
@@ -599,13 +701,7 @@ __global__ void __launch_bounds__(1024) bsa_block_norm_sum_kernel(const SumParam
       const int64_t lo = g * p.per_gate / p.rows_per_block;
       const int64_t hi = p.rows == 0 ? -1 : min((min((g + 1) * p.per_gate, p.rows) - 1) / p.rows_per_block, p.blocks - 1);
       float S = 0.f, T = 0.f;
-      if (in)
-#pragma unroll 8
-        for (int64_t k = lo + sub; k <= hi; k += per) {
-          const float* q = p.part + (k + g) * (1 + p.means) * p.C + c;
-          S += q[0];
-          if (p.means) T += q[p.C];
-        }
+      if (in) sum_slots(p.part + (g + lo) * (1 + p.means) * p.C + c, hi - lo + 1, sub, per, p.C, p.means, S, T);
       if (per > 1) {
         // groups * per = 32 and one pass: every lane comes here exactly once
         buf[0][ty][lane] = S;
@@ -631,14 +727,6 @@ __global__ void __launch_bounds__(1024) bsa_block_norm_sum_kernel(const SumParam
     }
     __syncthreads();
   }
-  float P = 0.f, Q = 0.f;
-  if (p.has_pre && in)
-#pragma unroll 8
-    for (int64_t k = ty; k < p.blocks; k += 32) {
-      const float* q = p.part_pre + k * (1 + p.means) * p.C + c;
-      P += q[0];
-      if (p.means) Q += q[p.C];
-    }
   buf[0][ty][lane] = dw;
   buf[1][ty][lane] = db;
   buf[2][ty][lane] = P;
@@ -663,34 +751,46 @@ struct Team {
   bool warp;             // a warp a row, without barriers
 };
 
-// arrays: how many the ring brings; sums: [C] floats and kN areas a team (backward).
+constexpr size_t kSmemMost = 220 * 1024;
+
 Team team_of(int C, size_t esize, bool aligned, bool backward, bool means) {
   Team t{};
   t.vec = aligned && C % 8 == 0 ? 8 : aligned && C % 2 == 0 ? 2 : 1;
   const int n = C / t.vec;
   // A warp takes a row while a lane's share fits its registers (the backward keeps two sums
-  // a column, four with plain means), else the fewest pieces a thread that 512 threads allow.
+  // a column, four with plain means), else the block with few pieces a thread.
   const int most = t.vec < 8 ? 0 : backward && means ? 2 : 3;
   if (n <= 32 * most) {
     t.nv = (n + 31) / 32;
     t.threads = 32;
-    t.teams = 4;
     t.warp = true;
   } else {
     t.nv = t.vec == 8 ? (n <= 512 ? 1 : 2) : t.vec == 2 ? (n <= 2048 ? 4 : 8) : (n <= 4096 ? 8 : 16);
     t.threads = ((n + t.nv - 1) / t.nv + 31) / 32 * 32;
-    t.teams = std::max(1, 256 / t.threads);
   }
-  const int block = t.threads * t.teams, nq = means ? 2 : 1;
-  const size_t fixed = backward ? ((C + 3) / 4 * 4 + t.teams * 2 * nq * 32) * sizeof(float) : t.teams * 256;
-  const size_t slot = static_cast<size_t>(block) * (backward ? 4 : 2) * t.nv * t.vec * esize;
-  // blocks on an SM that the registers allow: about 128 a thread, 255 for the backward's warps
-  const int by_regs = std::max(1, (backward && t.warp ? 256 : 512) / block);
-  t.depth = 3;
-  t.per_sm = by_regs;
-  while (t.depth > 1 && (fixed + t.depth * slot + 1024) * t.per_sm > 220 * 1024) --t.depth;
-  while (t.per_sm > 1 && (fixed + t.depth * slot + 1024) * t.per_sm > 220 * 1024) --t.per_sm;
-  t.smem = fixed + t.depth * slot;
+  const auto slot = [&] { return static_cast<size_t>(t.threads * t.teams) * (backward ? 4 : 2) * t.nv * t.vec * esize; };
+  if (!backward) {
+    // about 128 registers a thread
+    t.teams = t.warp ? kWarpBlock / 32 : std::max(1, 256 / t.threads);
+    t.per_sm = std::max(1, 512 / (t.threads * t.teams));
+    const size_t fixed = t.teams * 256;
+    t.depth = 3;
+    while (t.depth > 1 && (fixed + t.depth * slot() + 1024) * t.per_sm > kSmemMost) --t.depth;
+    while (t.per_sm > 1 && (fixed + t.depth * slot() + 1024) * t.per_sm > kSmemMost) --t.per_sm;
+    t.smem = fixed + t.depth * slot();
+    return t;
+  }
+  // one block an SM, of as many teams as leave room for two rows on their way in each
+  t.per_sm = 1;
+  const auto fixed = [&] {
+    return (3 * static_cast<size_t>(t.nv * t.vec) * t.threads + t.teams * 2 * (means ? 2 : 1) * 32) * sizeof(float);
+  };
+  t.teams = std::max(1, (t.warp && t.nv > 1 ? kBackWarpBlock : kBackBlock) / t.threads);
+  t.depth = 2;
+  while (t.teams > 1 && fixed() + 2 * slot() > kSmemMost) --t.teams;
+  if (fixed() + 2 * slot() > kSmemMost) t.depth = 1;
+  else if (fixed() + 3 * slot() <= kSmemMost) t.depth = 3;
+  t.smem = fixed() + t.depth * slot();
   return t;
 }
 
@@ -787,20 +887,21 @@ BackPlan back_plan(const NormParams& p, const Team& t, int gate_rows, bool means
 
 template <typename T, bool kMeans>
 bool launch_back(const NormParams& p, const Team& t, const BackPlan& b, cudaStream_t s) {
+  constexpr int kB = kBackBlock, kW = kBackWarpBlock;
   if (t.warp) {
-    if (t.nv == 1) return start(bsa_block_norm_back_kernel<T, 8, 1, true, kMeans>, p, t, b.blocks, s);
+    if (t.nv == 1) return start(bsa_block_norm_back_kernel<T, 8, 1, true, kMeans, kB>, p, t, b.blocks, s);
     if constexpr (!kMeans)
-      if (t.nv == 3) return start(bsa_block_norm_back_kernel<T, 8, 3, true, kMeans>, p, t, b.blocks, s);
-    return start(bsa_block_norm_back_kernel<T, 8, 2, true, kMeans>, p, t, b.blocks, s);
+      if (t.nv == 3) return start(bsa_block_norm_back_kernel<T, 8, 3, true, kMeans, kW>, p, t, b.blocks, s);
+    return start(bsa_block_norm_back_kernel<T, 8, 2, true, kMeans, kW>, p, t, b.blocks, s);
   }
   if (t.vec == 8)
-    return t.nv == 1 ? start(bsa_block_norm_back_kernel<T, 8, 1, false, kMeans>, p, t, b.blocks, s)
-                     : start(bsa_block_norm_back_kernel<T, 8, 2, false, kMeans>, p, t, b.blocks, s);
+    return t.nv == 1 ? start(bsa_block_norm_back_kernel<T, 8, 1, false, kMeans, kB>, p, t, b.blocks, s)
+                     : start(bsa_block_norm_back_kernel<T, 8, 2, false, kMeans, kB>, p, t, b.blocks, s);
   if (t.vec == 2)
-    return t.nv == 4 ? start(bsa_block_norm_back_kernel<T, 2, 4, false, kMeans>, p, t, b.blocks, s)
-                     : start(bsa_block_norm_back_kernel<T, 2, 8, false, kMeans>, p, t, b.blocks, s);
-  return t.nv == 8 ? start(bsa_block_norm_back_kernel<T, 1, 8, false, kMeans>, p, t, b.blocks, s)
-                   : start(bsa_block_norm_back_kernel<T, 1, 16, false, kMeans>, p, t, b.blocks, s);
+    return t.nv == 4 ? start(bsa_block_norm_back_kernel<T, 2, 4, false, kMeans, kB>, p, t, b.blocks, s)
+                     : start(bsa_block_norm_back_kernel<T, 2, 8, false, kMeans, kB>, p, t, b.blocks, s);
+  return t.nv == 8 ? start(bsa_block_norm_back_kernel<T, 1, 8, false, kMeans, kB>, p, t, b.blocks, s)
+                   : start(bsa_block_norm_back_kernel<T, 1, 16, false, kMeans, kB>, p, t, b.blocks, s);
 }
 
 bool takes_means(const bsa_block_norm_args& a) { return a.post == BSA_NORM_LAYER || a.pre == BSA_NORM_LAYER; }
