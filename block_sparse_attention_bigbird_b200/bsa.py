@@ -864,7 +864,7 @@ def bsa_fp8_matmul(a, a_scale, b, b_scale, bias=None, out_dtype=None, out=None, 
     def call(ptr):
         o = torch.empty((M, N), dtype=out_dtype, device=a.device) if out is None else out
         ws = workspace
-        if ws is None and M > 32:
+        if ws is None and M > 8:
             n = bsa_fp8_matmul_workspace_bytes(M, N, K)
             ws = torch.empty(n, dtype=torch.uint8, device=a.device) if n else None
         _check(lib.bsa_fp8_matmul(a.data_ptr(), at, a.stride(0), a_scale.data_ptr(), ar, b.data_ptr(), bt, b.stride(0),

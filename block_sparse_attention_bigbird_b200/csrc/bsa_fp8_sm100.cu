@@ -6,7 +6,7 @@
 // in the tensor cores and the sum over blocks is done in fp32 by threads, each block's
 // partial read from TMEM and added with its scale by one fma an element.
 //
-// bsa_fp8_mma_kernel, for more than 32 rows.  Persistent, one CTA per SM, 384 threads.  A
+// bsa_fp8_mma_kernel, for more than 8 rows.  Persistent, one CTA per SM, 384 threads.  A
 // unit of work is a tile of 128 rows by kBN columns, over all of K or one of `splits` ranges
 // of blocks.
 //   warp 0     TMA producer: per block of K (128 bytes: one 128-byte swizzle atom) the A box
@@ -27,13 +27,12 @@
 // uniform registers after every wait; two of them hide the waits.  No register may spill: with
 // the shared memory taken, L1 is too small to hold them.
 //
-// bsa_fp8_rows_kernel, for up to 32 rows (tokens).  There the time is that of reading b
-// once.  A block of threads takes 16 rows of b, its warps an equal share of K's blocks each;
-// the codes go straight from global memory to registers (16 bytes a thread and row), are
-// widened to fp16, which holds every e4m3 and e5m2 value, and multiplied by
-// mma.sync m16n8k16 with b as the 16-row side and the tokens as the 8 columns.  The products
-// of a block of 128 are summed in fp32 before their scale; the warps' sums meet in shared
-// memory in a fixed order.
+// bsa_fp8_rows_kernel, for up to 8 rows (tokens).  There the time is that of reading b once.
+// A block of threads takes 16 rows of b at a time, its warps an equal share of K's blocks each;
+// every warp brings its part of b with cp.async, kRowsAhead blocks of K ahead and over the end
+// of one 16-row tile into the next, so that the loads in flight do not depend on registers.  Codes are widened to fp16, which holds every e4m3 and e5m2 value, and multiplied
+// by mma.sync m16n8k16 with b as the 16-row side and the tokens as the 8 columns.  The products of a block of 128 are summed in fp32 before their
+// scale; the warps' sums meet in shared memory in a fixed order.
 //
 // Every wait is bounded; on expiry the CTA records BSA_ERR_DEVICE_TIMEOUT, drains its copies
 // and MMAs, frees TMEM and returns.
@@ -146,14 +145,6 @@ __device__ __forceinline__ bool elected() {
   return p != 0;
 }
 
-// 16 TMEM columns of this thread's lane (32x32b).
-__device__ __forceinline__ void tmem_ld16(uint32_t taddr, uint32_t (&r)[16]) {
-  asm volatile(
-      "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15}, [%16];"
-      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]),
-        "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
-      : "r"(taddr));
-}
 // 16 lanes of 32 TMEM columns (16x256b, four times): of columns 8 i + 2 (lane % 4), + 1 the
 // words 4 i, + 1 in row lane / 4 and 4 i + 2, + 3 in row lane / 4 + 8.
 __device__ __forceinline__ void tmem_ld_frag(uint32_t taddr, uint32_t (&r)[16]) {
@@ -421,19 +412,28 @@ __device__ void promoter(const MmaParams& p, uint32_t smem, uint8_t* smem_gen, u
         return;
       }
       __syncwarp();
+      // a lane writes the same four bytes of each row: an fp32 column or two bf16 ones
       uint8_t* out = static_cast<uint8_t*>(p.out) + t.split * p.split_stride * esize;
-      for (int b = 0; b < boxes; ++b)
-        for (int r = 0; r < 32 && row0 + r < p.M; ++r) {
-          const uint8_t* from = smem_gen + stg + b * 4096u + r * 128;
-          for (int e = lane; e < cols; e += 32) {
-            const int col = c0 + b * cols + e, at = e * esize;
-            if (col >= p.N) continue;
-            const uint8_t* x = from + (((at >> 4) ^ (r & 7)) << 4) + (at & 15);
-            uint8_t* to = out + (static_cast<int64_t>(row0 + r) * p.N + col) * esize;
-            if (p.out_f32) *reinterpret_cast<uint32_t*>(to) = *reinterpret_cast<const uint32_t*>(x);
-            else *reinterpret_cast<uint16_t*>(to) = *reinterpret_cast<const uint16_t*>(x);
+      const int col = c0 + (p.out_f32 ? lane : 2 * lane);
+      const bool words = p.out_f32 || ((p.N & 1) == 0 && (reinterpret_cast<uintptr_t>(p.out) & 3u) == 0);
+      for (int b = 0; b < boxes; ++b) {
+        const int c = col + b * cols;
+        if (c >= p.N) break;
+        uint8_t* to = out + (static_cast<int64_t>(row0) * p.N + c) * esize;
+        const int64_t pitch = static_cast<int64_t>(p.N) * esize;
+#pragma unroll 8
+        for (int r = 0; r < 32; ++r, to += pitch) {
+          const uint32_t w = *reinterpret_cast<const uint32_t*>(smem_gen + stg + b * 4096u + r * 128 +
+                                                                (((lane >> 2) ^ (r & 7)) << 4) + (lane & 3) * 4);
+          if (row0 + r >= p.M) continue;
+          if (words) {
+            *reinterpret_cast<uint32_t*>(to) = w;
+          } else {
+            reinterpret_cast<uint16_t*>(to)[0] = static_cast<uint16_t>(w);
+            if (c + 1 < p.N) reinterpret_cast<uint16_t*>(to)[1] = static_cast<uint16_t>(w >> 16);
           }
         }
+      }
       __syncwarp();
     };
     uint8_t* mine = smem_gen + stg + lane * 128;
@@ -665,8 +665,9 @@ struct RowsParams {
   int bias_f32, out_f32;
 };
 
-constexpr int kRowsMost = 32;      // rows of a that the kernel takes
-constexpr int kRowsWarpsMost = 8;  // warps of a block at most
+constexpr int kRowsMost = 8;        // rows of a that the kernel takes
+constexpr int kRowsWarpsMost = 16;  // warps of a block at most
+constexpr int kRowsAhead = 4;       // blocks of K on their way to a warp, the one in use included
 
 template <bool kE5>
 __device__ __forceinline__ uint32_t widen(uint32_t two) {  // two codes in the low 16 bits -> two fp16
@@ -685,101 +686,203 @@ __device__ __forceinline__ void mma_f16(float (&d)[4], uint32_t a0, uint32_t a1,
 }
 
 // 16 codes of a row at column k (a multiple of 16); zeros past the row's end, which is not
-// read past.
+// read past.  kTail: K may end inside the 16.
+template <bool kTail>
 __device__ __forceinline__ uint4 codes16(const uint8_t* row, int k, int K) {
-  if (k + 16 <= K) return __ldg(reinterpret_cast<const uint4*>(row + k));
+  if (k + (kTail ? 16 : 1) <= K) return __ldg(reinterpret_cast<const uint4*>(row + k));
   uint32_t x[4] = {};
+  if constexpr (kTail) {
+#pragma unroll 1
+    for (int i = 0; i < 15; ++i)
+      if (k + i < K) {
+        const uint32_t c = static_cast<uint32_t>(row[k + i]) << (8 * (i & 3));
 #pragma unroll
-  for (int i = 0; i < 15; ++i)
-    if (k + i < K) x[i >> 2] |= static_cast<uint32_t>(row[k + i]) << (8 * (i & 3));
+        for (int w = 0; w < 4; ++w) x[w] |= w == i >> 2 ? c : 0u;
+      }
+  }
   return make_uint4(x[0], x[1], x[2], x[3]);
 }
 
-// kG groups of eight tokens.  Thread (g, t) of a warp (lane / 4, lane % 4) holds, of each 64
-// codes of K, the 16 at 16 t of b's rows g and g + 8 and of tokens g, g + 8, ..: any order of
-// K's products gives the same sum, so four codes of these serve as the thread's k-slots of one
-// m16n8k16 product.
-template <int kG, bool kAE5, bool kBE5>
-__global__ void __launch_bounds__(kRowsWarpsMost * 32) bsa_fp8_rows_kernel(const __grid_constant__ RowsParams p) {
-  __shared__ float part[kRowsWarpsMost][kG][32][4];
+// Thread (g, t) of a warp (lane / 4, lane % 4) holds, of each 64 codes of K, the 16 at 16 t of
+// b's rows g and g + 8 and of token g: any order of K's products gives the same sum, so four
+// codes of these serve as the thread's k-slots of one m16n8k16 product.
+// kHeld: a warp's blocks of K (1 to 4), whose tokens stay widened in registers from tile to
+// tile; 0: more, their tokens are read again for every tile.
+template <bool kAE5, bool kBE5, bool kTail, int kHeld>
+__global__ void __launch_bounds__(kRowsWarpsMost * 32, 1) bsa_fp8_rows_kernel(const __grid_constant__ RowsParams p) {
+  __shared__ float part[2][kRowsWarpsMost][32][4];
+  // b's codes of the blocks to come, each warp's own: 16 rows of 128 bytes a slot, fetched as
+  // whole lines (8 lanes a row); 16-byte chunk c of row r lies at chunk c ^ 4 (r % 2), which
+  // spreads what 8 lanes read of two rows over all banks
+  extern __shared__ __align__(16) uint8_t ring[];
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
-  const int warps = blockDim.x >> 5;
-  const int n0 = blockIdx.x * 16 + g, n1 = n0 + 8;
-  const uint8_t* b0 = p.b + static_cast<int64_t>(min(n0, p.N - 1)) * p.ldb;
-  const uint8_t* b1 = p.b + static_cast<int64_t>(min(n1, p.N - 1)) * p.ldb;
-  const float* sb0 = p.sb + static_cast<int64_t>(min(n0, p.N - 1) >> p.b_shift) * p.kb;
-  const float* sb1 = p.sb + static_cast<int64_t>(min(n1, p.N - 1) >> p.b_shift) * p.kb;
-  const int per = (p.kb + warps - 1) / warps;
-  const int k0 = warp * per, k1 = min(k0 + per, p.kb);
-  float acc[kG][4] = {};
-  for (int kb = k0; kb < k1; ++kb) {
-    uint4 w0[2], w1[2];
+  const int warps = blockDim.x >> 5, tiles = (p.N + 15) / 16;
+  const int per = kHeld > 0 ? kHeld : (p.kb + warps - 1) / warps;
+  const int k0 = min(warp * per, p.kb), k1 = min(k0 + per, p.kb);
+  const uint32_t mine = ptx::smem_addr(ring) + warp * (kRowsAhead * 2048u);
+
+  // ---- fetching: lane / 8 + 4 j is its row, lane % 8 its 16 bytes
+  const int64_t four = 4 * p.ldb, tile_step = static_cast<int64_t>(gridDim.x) * 16 * p.ldb;
+  int fk = k0, fr = blockIdx.x * 16 + (lane >> 3);
+  const uint8_t* from = p.b + static_cast<int64_t>(fr) * p.ldb + (lane & 7) * 16;
+  uint32_t fdst = mine + (lane >> 3) * 128u + (((lane & 7) ^ ((lane >> 3 & 1) << 2)) << 4);
+  uint32_t fslot = 0;
+  auto fetch = [&] {
+    if (fr - (lane >> 3) < p.N && k0 < k1) {
+      const int k = fk * kKB + (lane & 7) * 16;
+      const uint8_t* at = from + fk * kKB;
 #pragma unroll
-    for (int h = 0; h < 2; ++h) {
-      w0[h] = codes16(b0, kb * kKB + h * 64 + t * 16, p.K);
-      w1[h] = codes16(b1, kb * kKB + h * 64 + t * 16, p.K);
-    }
-    const float s0 = __ldg(sb0 + kb), s1 = __ldg(sb1 + kb);
-    float d[kG][4] = {};
-#pragma unroll
-    for (int h = 0; h < 2; ++h) {
-      uint4 x[kG];
-#pragma unroll
-      for (int q = 0; q < kG; ++q) {
-        const int m = q * 8 + g;
-        x[q] = m < p.M ? codes16(p.a + static_cast<int64_t>(m) * p.lda, kb * kKB + h * 64 + t * 16, p.K)
-                       : make_uint4(0, 0, 0, 0);
-      }
-      const uint32_t r0[4] = {w0[h].x, w0[h].y, w0[h].z, w0[h].w}, r1[4] = {w1[h].x, w1[h].y, w1[h].z, w1[h].w};
-#pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        const uint32_t a0 = widen<kBE5>(r0[i]), a2 = widen<kBE5>(r0[i] >> 16);
-        const uint32_t a1 = widen<kBE5>(r1[i]), a3 = widen<kBE5>(r1[i] >> 16);
-#pragma unroll
-        for (int q = 0; q < kG; ++q) {
-          const uint32_t xi = i == 0 ? x[q].x : i == 1 ? x[q].y : i == 2 ? x[q].z : x[q].w;
-          mma_f16(d[q], a0, a1, a2, a3, widen<kAE5>(xi), widen<kAE5>(xi >> 16));
+      for (int j = 0; j < 4; ++j, at += four) {
+        const bool row = fr + 4 * j < p.N;
+        const uint32_t dst = fdst + j * 512u;
+        if (kTail && k + 16 > p.K) {  // the row's last codes, or none
+          const uint4 w = row ? codes16<kTail>(at - k, k, p.K) : make_uint4(0, 0, 0, 0);
+          asm volatile("st.shared.v4.u32 [%0], {%1, %2, %3, %4};" ::"r"(dst), "r"(w.x), "r"(w.y), "r"(w.z), "r"(w.w) : "memory");
+        } else {  // outside the matrix nothing is read and zeros are stored
+          const bool in = row && k < p.K;
+          asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(in ? at : p.b), "r"(in ? 16 : 0)
+                       : "memory");
         }
       }
+      if (++fk == k1) {
+        fk = k0;
+        fr += gridDim.x * 16;
+        from += tile_step;
+      }
+      const bool wrap = ++fslot == kRowsAhead;
+      fdst += wrap ? -(kRowsAhead - 1) * 2048u : 2048u;
+      fslot = wrap ? 0 : fslot;
+    }
+    asm volatile("cp.async.commit_group;" ::: "memory");
+  };
+  for (int i = 0; i + 1 < kRowsAhead; ++i) fetch();
+
+  // ---- the tokens
+  const uint8_t* a = p.a + static_cast<int64_t>(min(g, p.M - 1)) * p.lda;
+  const float* sa0 = p.sa + static_cast<int64_t>(min(2 * t, p.M - 1) >> p.a_shift) * p.kb;
+  const float* sa1 = p.sa + static_cast<int64_t>(min(2 * t + 1, p.M - 1) >> p.a_shift) * p.kb;
+  struct Tokens {  // a block's: four codes of each of two 64s widened, and two tokens' scales
+    uint32_t x[2][8];
+    float m0, m1;
+  };
+  auto tokens = [&](int kb) {
+    Tokens c;
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+      const uint4 w = g < p.M ? codes16<kTail>(a, kb * kKB + h * 64 + t * 16, p.K) : make_uint4(0, 0, 0, 0);
+      const uint32_t v[4] = {w.x, w.y, w.z, w.w};
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        c.x[h][2 * i] = widen<kAE5>(v[i]);
+        c.x[h][2 * i + 1] = widen<kAE5>(v[i] >> 16);
+      }
+    }
+    c.m0 = __ldg(sa0 + kb);
+    c.m1 = __ldg(sa1 + kb);
+    return c;
+  };
+  Tokens held[kHeld > 0 ? kHeld : 1];
+#pragma unroll
+  for (int i = 0; i < kHeld; ++i)
+    if (k0 + i < k1) held[i] = tokens(k0 + i);
+
+  uint32_t rd = mine + g * 128u, slot = 0;
+  const uint32_t c0 = (t ^ ((g & 1) << 2)) << 4, c1 = ((4 + t) ^ ((g & 1) << 2)) << 4;
+  // adds the block at hand, of tokens c and of the scales s0 and s1 of b's rows g and g + 8
+  auto use = [&](const Tokens& c, float s0, float s1, float (&acc)[4]) {
+    asm volatile("cp.async.wait_group %0;" ::"n"(kRowsAhead - 1) : "memory");
+    __syncwarp();
+    float d[4] = {};
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+      uint32_t r[2][4];
+#pragma unroll
+      for (int e = 0; e < 2; ++e)
+        asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];"
+                     : "=r"(r[e][0]), "=r"(r[e][1]), "=r"(r[e][2]), "=r"(r[e][3])
+                     : "r"(rd + e * 1024u + (h ? c1 : c0)));
+#pragma unroll
+      for (int i = 0; i < 4; ++i)
+        mma_f16(d, widen<kBE5>(r[0][i]), widen<kBE5>(r[1][i]), widen<kBE5>(r[0][i] >> 16), widen<kBE5>(r[1][i] >> 16),
+                c.x[h][2 * i], c.x[h][2 * i + 1]);
+    }
+    acc[0] = fmaf(d[0], s0 * c.m0, acc[0]);
+    acc[1] = fmaf(d[1], s0 * c.m1, acc[1]);
+    acc[2] = fmaf(d[2], s1 * c.m0, acc[2]);
+    acc[3] = fmaf(d[3], s1 * c.m1, acc[3]);
+    const bool wrap = ++slot == kRowsAhead;
+    rd += wrap ? -(kRowsAhead - 1) * 2048u : 2048u;
+    slot = wrap ? 0 : slot;
+    __syncwarp();  // the slot may be fetched into again
+  };
+  int turn = 0;
+  for (int tile = blockIdx.x; tile < tiles; tile += gridDim.x, turn ^= 1) {
+    float acc[4] = {};
+    const float* sb0 = p.sb + static_cast<int64_t>(min(tile * 16 + g, p.N - 1) >> p.b_shift) * p.kb;
+    const float* sb1 = p.b_shift ? sb0 : p.sb + static_cast<int64_t>(min(tile * 16 + g + 8, p.N - 1)) * p.kb;
+    if constexpr (kHeld > 0) {
+      float s0[kHeld], s1[kHeld];
+#pragma unroll
+      for (int i = 0; i < kHeld; ++i) {
+        const bool there = k0 + i < k1;
+        s0[i] = there ? __ldg(sb0 + k0 + i) : 0.f;
+        s1[i] = p.b_shift ? s0[i] : there ? __ldg(sb1 + k0 + i) : 0.f;
+      }
+#pragma unroll
+      for (int i = 0; i < kHeld; ++i)
+        if (k0 + i < k1) {
+          fetch();
+          use(held[i], s0[i], s1[i], acc);
+        }
+    } else {
+      for (int kb = k0; kb < k1; ++kb) {
+        fetch();
+        const float s0 = __ldg(sb0 + kb), s1 = __ldg(sb1 + kb);
+        use(tokens(kb), s0, s1, acc);
+      }
     }
 #pragma unroll
-    for (int q = 0; q < kG; ++q) {
-      const int m = q * 8 + 2 * t;
-      const float m0 = __ldg(p.sa + static_cast<int64_t>(min(m, p.M - 1) >> p.a_shift) * p.kb + kb);
-      const float m1 = __ldg(p.sa + static_cast<int64_t>(min(m + 1, p.M - 1) >> p.a_shift) * p.kb + kb);
-      acc[q][0] = fmaf(d[q][0], s0 * m0, acc[q][0]);
-      acc[q][1] = fmaf(d[q][1], s0 * m1, acc[q][1]);
-      acc[q][2] = fmaf(d[q][2], s1 * m0, acc[q][2]);
-      acc[q][3] = fmaf(d[q][3], s1 * m1, acc[q][3]);
+    for (int i = 0; i < 4; ++i) part[turn][warp][lane][i] = acc[i];
+    __syncthreads();  // the other half of part is read before the next one
+    // output (m, n): 16 neighbouring threads write 16 neighbouring columns of one token
+    for (int o = threadIdx.x; o < 8 * 16; o += blockDim.x) {
+      const int c = o & 15, m = o >> 4, n = tile * 16 + c;
+      if (m >= p.M || n >= p.N) continue;
+      const int ln = (c & 7) * 4 + (m >> 1), i = (c >> 3) * 2 + (m & 1);
+      float v = 0.f;
+      for (int w = 0; w < warps; ++w) v += part[turn][w][ln][i];
+      if (p.bias != nullptr)
+        v += p.bias_f32 ? static_cast<const float*>(p.bias)[n]
+                        : __bfloat162float(static_cast<const __nv_bfloat16*>(p.bias)[n]);
+      const int64_t at = static_cast<int64_t>(m) * p.N + n;
+      if (p.out_f32) static_cast<float*>(p.out)[at] = v;
+      else static_cast<__nv_bfloat16*>(p.out)[at] = __float2bfloat16_rn(v);
     }
-  }
-#pragma unroll
-  for (int q = 0; q < kG; ++q)
-#pragma unroll
-    for (int i = 0; i < 4; ++i) part[warp][q][lane][i] = acc[q][i];
-  __syncthreads();
-  // output (m, n): 16 neighbouring threads write 16 neighbouring columns of one token
-  for (int o = threadIdx.x; o < kG * 8 * 16; o += blockDim.x) {
-    const int c = o & 15, m = o >> 4, n = blockIdx.x * 16 + c;
-    if (m >= p.M || n >= p.N) continue;
-    const int q = m >> 3, ln = (c & 7) * 4 + ((m & 7) >> 1), i = (c >> 3) * 2 + (m & 1);
-    float v = 0.f;
-    for (int w = 0; w < warps; ++w) v += part[w][q][ln][i];
-    if (p.bias != nullptr)
-      v += p.bias_f32 ? static_cast<const float*>(p.bias)[n]
-                      : __bfloat162float(static_cast<const __nv_bfloat16*>(p.bias)[n]);
-    const int64_t at = static_cast<int64_t>(m) * p.N + n;
-    if (p.out_f32) static_cast<float*>(p.out)[at] = v;
-    else static_cast<__nv_bfloat16*>(p.out)[at] = __float2bfloat16_rn(v);
   }
 }
 
-template <int kG>
-void launch_rows(const RowsParams& p, bool ae5, bool be5, int grid, int threads, cudaStream_t s) {
-  if (ae5) be5 ? bsa_fp8_rows_kernel<kG, true, true><<<grid, threads, 0, s>>>(p)
-               : bsa_fp8_rows_kernel<kG, true, false><<<grid, threads, 0, s>>>(p);
-  else be5 ? bsa_fp8_rows_kernel<kG, false, true><<<grid, threads, 0, s>>>(p)
-           : bsa_fp8_rows_kernel<kG, false, false><<<grid, threads, 0, s>>>(p);
+template <bool kAE5, bool kBE5, bool kTail, int kHeld>
+int start_rows(const RowsParams& p, int grid, int threads, cudaStream_t s) {
+  auto* kernel = bsa_fp8_rows_kernel<kAE5, kBE5, kTail, kHeld>;
+  const int smem = kRowsAhead * 2048 * (threads / 32);
+  if (smem > 32 * 1024 &&
+      cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem) != cudaSuccess)
+    return BSA_ERR_CUDA;
+  kernel<<<grid, threads, smem, s>>>(p);
+  return cudaGetLastError() == cudaSuccess ? BSA_OK : BSA_ERR_CUDA;
+}
+
+// A K that is no multiple of 16 is rare and takes the form that holds nothing.
+template <bool kAE5, bool kBE5>
+int launch_rows(const RowsParams& p, int grid, int threads, cudaStream_t s) {
+  if (p.K % 16 != 0) return start_rows<kAE5, kBE5, true, 0>(p, grid, threads, s);
+  switch ((p.kb + threads / 32 - 1) / (threads / 32)) {
+    case 1: return start_rows<kAE5, kBE5, false, 1>(p, grid, threads, s);
+    case 2: return start_rows<kAE5, kBE5, false, 2>(p, grid, threads, s);
+    case 3: return start_rows<kAE5, kBE5, false, 3>(p, grid, threads, s);
+    case 4: return start_rows<kAE5, kBE5, false, 4>(p, grid, threads, s);
+    default: return start_rows<kAE5, kBE5, false, 0>(p, grid, threads, s);
+  }
 }
 
 // ------------------------------------------------------------ host
@@ -866,6 +969,7 @@ MmaPlan mma_plan(int64_t M, int64_t N, int64_t kb, int sms) {
   for (const int bn : {256, 128}) {
     const int64_t tiles = ((M + kMB - 1) / kMB) * ((N + bn - 1) / bn);
     for (int64_t want = 1; want <= 32 && want <= kb; ++want) {
+      if (want > 1 && tiles * want > 4 * sms) break;  // more units than that only cost partials
       const int64_t per = (kb + want - 1) / want, splits = (kb + per - 1) / per;
       if (splits != want) continue;
       const int64_t waves = (tiles * splits + sms - 1) / sms;
@@ -954,12 +1058,12 @@ int bsa_fp8_matmul(const void* a, int a_type, int64_t lda, const float* a_scale,
     p.M = M, p.N = N, p.K = K, p.kb = kb;
     p.a_shift = a_rows == 128 ? 7 : 0, p.b_shift = b_rows == 128 ? 7 : 0;
     p.bias_f32 = bias_f32, p.out_f32 = out_f32;
-    const int grid = (N + 15) / 16, threads = 32 * std::min(kb, kRowsWarpsMost);
+    // one block of up to 16 warps an SM, more of fewer warps where K is short
+    const int warps = std::min(kb, kRowsWarpsMost), threads = 32 * warps;
+    const int grid = std::min((N + 15) / 16, sms * (kRowsWarpsMost / warps));
     const bool ae5 = a_type == BSA_E5M2, be5 = b_type == BSA_E5M2;
-    if (M <= 8) launch_rows<1>(p, ae5, be5, grid, threads, s);
-    else if (M <= 16) launch_rows<2>(p, ae5, be5, grid, threads, s);
-    else launch_rows<4>(p, ae5, be5, grid, threads, s);
-    return cudaGetLastError() == cudaSuccess ? BSA_OK : BSA_ERR_CUDA;
+    if (ae5) return be5 ? launch_rows<true, true>(p, grid, threads, s) : launch_rows<true, false>(p, grid, threads, s);
+    return be5 ? launch_rows<false, true>(p, grid, threads, s) : launch_rows<false, false>(p, grid, threads, s);
   }
   const MmaPlan plan = mma_plan(M, N, kb, sms);
   if (plan.bytes > 0 && (workspace == nullptr || reinterpret_cast<uintptr_t>(workspace) % 256 != 0 ||
