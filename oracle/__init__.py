@@ -2,8 +2,9 @@
 
 Plain, slow, obviously-correct fp64 reference: an independent layout builder
 (``oracle.layout``), masked-dense attention (``oracle.attention``), its
-gradients (``oracle.backward``) and the layer's two projections
-(``oracle.projection``).  Only
+gradients (``oracle.backward``), the layer's two projections
+(``oracle.projection``) and the operators around the attention (``oracle.rope``,
+``oracle.block_norm``, ``oracle.fp8``).  Only
 ``tests/``, ``__graft_entry__.smoke()`` and ``bench.py``'s CPU-baseline leg may
 import it; the CUDA library never does, and this package imports nothing from
 the library.  Every function cites the page passage it follows.
@@ -13,4 +14,4 @@ against a closed form, a library routine, a published known-answer vector or
 brute force (see ``tests/test_oracle_*.py``).
 """
 
-from . import attention, backward, layout, projection  # noqa: F401
+from . import attention, backward, block_norm, fp8, layout, projection, rope  # noqa: F401
