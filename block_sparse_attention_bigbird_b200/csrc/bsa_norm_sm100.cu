@@ -239,6 +239,8 @@ constexpr int kWarpBlock = 128;  // threads of a forward block whose teams are w
 // Threads of a backward block at most: where a thread has more than eight elements of a row
 // (in teams of a warp) it needs 168 registers, else 128 do.
 constexpr int kBackBlock = 512, kBackWarpBlock = 384;
+// Teams of a block that meet at a barrier of their own: ids 1 to 15 (0 is the block's).
+constexpr int kNamedBarriers = 15;
 
 __device__ __forceinline__ uint4 lds16(uint32_t a) {
   uint4 v;
@@ -786,6 +788,7 @@ Team team_of(int C, size_t esize, bool aligned, bool backward, bool means) {
     return (3 * static_cast<size_t>(t.nv * t.vec) * t.threads + t.teams * 2 * (means ? 2 : 1) * 32) * sizeof(float);
   };
   t.teams = std::max(1, (t.warp && t.nv > 1 ? kBackWarpBlock : kBackBlock) / t.threads);
+  if (!t.warp) t.teams = std::min(t.teams, kNamedBarriers);
   t.depth = 2;
   while (t.teams > 1 && fixed() + 2 * slot() > kSmemMost) --t.teams;
   if (fixed() + 2 * slot() > kSmemMost) t.depth = 1;

@@ -187,6 +187,9 @@ CASES = [  # B, L, C, post, pre, gate, bias, type, parameter type
     (2, 19, 320, None, "rms", 1, False, torch.bfloat16, torch.float32),
     (2, 19, 320, None, None, 2, False, torch.bfloat16, torch.bfloat16),
     (3, 600, 768, "rms", "rms", 0, False, torch.bfloat16, torch.float32),
+    (3, 2866, 59, "rms", "rms", 1, False, torch.bfloat16, torch.float32),     # every team of every block has rows
+    (2, 4000, 42, "layer", "layer", 2, True, torch.float32, torch.float32),
+    (1, 5000, 48, "rms", "layer", 1, True, torch.bfloat16, torch.bfloat16),
 ]
 
 
