@@ -511,25 +511,19 @@ def _raw_stream(index: int) -> int:
     return _current_raw(index)
 
 
-def _on(device, stream, call):
-    """call(stream pointer) with the tensors' device current, and ``stream``, where one is
-    given, the stream that call's allocations belong to."""
+def _on(index: int, stream, call):
+    """call(stream pointer) with the tensors' device ``index`` current, and ``stream``, where one
+    is given, the stream that call's allocations belong to."""
     import torch
-    if stream is None and device.index == torch.cuda.current_device():
-        return call(_raw_stream(device.index))
-    with torch.cuda.device(device):
+    if stream is None and index == torch.cuda.current_device():
+        return call(_raw_stream(index))
+    with torch.cuda.device(index):
         if stream is None:
-            return call(_raw_stream(device.index))
+            return call(_raw_stream(index))
         if isinstance(stream, int):
-            stream = torch.cuda.ExternalStream(stream, device=device)
+            stream = torch.cuda.ExternalStream(stream, device=index)
         with torch.cuda.stream(stream):
             return call(stream.cuda_stream)
-
-
-def _check_same(device, **tensors):
-    for name, t in tensors.items():
-        if t is not None and t.device != device:
-            raise ValueError(f"{name} is on {t.device}, not on {device}")
 
 
 def _ptr(t):
@@ -598,10 +592,6 @@ def bsa_rope_table(rope: Rope):
 _pack3, _pack12 = struct.Struct("3q").pack, struct.Struct("12q").pack  # host int64 arrays
 
 
-def _columns_lie(t, d: int) -> bool:
-    return d == 1 or t.stride(3) == 1
-
-
 def bsa_rope_apply(q, k, positions, rope: Rope, inverse: bool = False, q_out=None, k_out=None, stream=None):
     """q [B, H, L, d] and k [B, Hk, L, d] (or None) with their pairs turned by their positions.
 
@@ -610,86 +600,111 @@ def bsa_rope_apply(q, k, positions, rope: Rope, inverse: bool = False, q_out=Non
     [axes, B, L].  ``inverse`` turns back (the gradient).  Results are new contiguous tensors,
     or q_out and k_out, which may be q and k themselves; other overlaps are not allowed.
     """
-    device, dtype = q.device, q.dtype
+    dev, dtype = q.get_device(), q.dtype
     ty, pt = _type_of(dtype), _type_of(positions.dtype)
-    if q.dim() != 4 or ty not in (BF16, FP16, FP32) or device.type != "cuda" or not _columns_lie(q, q.shape[3]):
-        raise ValueError("q must be a bf16, fp16 or fp32 CUDA tensor [B, H, L, d] with contiguous columns")
+    if q.dim() != 4 or ty is None or ty > FP32 or dev < 0:
+        raise ValueError("q must be a bf16, fp16 or fp32 CUDA tensor [B, H, L, d]")
     B, H, L, d = q.shape
-    Hk = 0
+    sb, sh, sl, sc = q.stride()
+    if sc != 1 and d != 1:
+        raise ValueError("q must have contiguous columns")
+    Hk, ks = 0, None
     if k is not None:
-        if k.dim() != 4 or k.dtype is not dtype or k.shape[0] != B or k.shape[2] != L or k.shape[3] != d or \
-                not _columns_lie(k, d) or k.device != device:
-            raise ValueError("k must be like q, [B, Hk, L, d]")
+        ks = k.stride()
+        if k.dim() != 4 or k.dtype is not dtype or k.get_device() != dev or k.shape[0] != B or k.shape[2] != L or \
+                k.shape[3] != d or (ks[3] != 1 and d != 1):
+            raise ValueError("k must be like q, [B, Hk, L, d] with contiguous columns")
         Hk = k.shape[1]
-    pd = positions.dim()
-    if pt not in (INT32, INT64, FP32) or pd not in (2, 3) or positions.shape[0] < rope.n_axes or \
-            positions.shape[-1] != L or (pd == 3 and positions.shape[1] != B) or positions.device != device:
+    ps, n = positions.stride(), positions.shape
+    if pt not in (INT32, INT64, FP32) or len(n) not in (2, 3) or n[0] < rope.n_axes or n[-1] != L or \
+            (len(n) == 3 and n[1] != B) or positions.get_device() != dev:
         raise ValueError(f"positions must be int32, int64 or fp32 [axes, L] or [axes, B, L] on q's device with at "
                          f"least {rope.n_axes} axes")
-    for name, t, src in (("q_out", q_out, q), ("k_out", k_out, k)):
-        if t is not None and (src is None or t.dtype is not dtype or t.shape != src.shape or t.device != device or
-                              not _columns_lie(t, d) or any(n > 1 and s == 0 for n, s in zip(t.shape, t.stride()))):
-            raise ValueError(f"{name} must have its input's type and shape, contiguous columns and no shared rows")
+    if q_out is not None or k_out is not None:
+        for name, t, src in (("q_out", q_out, q), ("k_out", k_out, k)):
+            if t is not None and (src is None or t.dtype is not dtype or t.shape != src.shape or
+                                  t.get_device() != dev or (t.stride(3) != 1 and d != 1) or
+                                  any(m > 1 and s == 0 for m, s in zip(t.shape, t.stride()))):
+                raise ValueError(f"{name} must have its input's type and shape, contiguous columns and no shared rows")
 
     def call(ptr):
-        qo = q.new_empty((B, H, L, d)) if q_out is None else q_out
-        a, b, c, _ = q.stride()
-        e, f, g, _ = qo.stride()
-        ko, kp, kop, ks = k_out, None, None, (0, 0, 0, 0, 0, 0)
-        if k is not None:
-            if ko is None:
+        if q_out is None:  # new and contiguous
+            qo = q.new_empty((B, H, L, d))
+            e, f, g = H * L * d, L * d, d
+        else:
+            qo = q_out
+            e, f, g, _ = qo.stride()
+        ko = kp = kop = None
+        r, s, t, u, v, w = 0, 0, 0, 0, 0, 0
+        if ks is not None:
+            r, s, t, _ = ks
+            if k_out is None:
                 ko = k.new_empty((B, Hk, L, d))
-            ks = k.stride()[:3] + ko.stride()[:3]
+                u, v, w = Hk * L * d, L * d, d
+            else:
+                ko = k_out
+                u, v, w, _ = ko.stride()
             kp, kop = k.data_ptr(), ko.data_ptr()
-        ps = positions.stride()
-        _check(lib.bsa_rope_apply(q.data_ptr(), qo.data_ptr(), H, kp, kop, Hk, B, L, d, ty,
-                                  _pack12(a, b, c, e, f, g, *ks), positions.data_ptr(), pt,
-                                  _pack3(ps[0], ps[1] if pd == 3 else 0, ps[-1]), rope._h, inverse, ptr),
-               "bsa_rope_apply")
+        code = lib.bsa_rope_apply(q.data_ptr(), qo.data_ptr(), H, kp, kop, Hk, B, L, d, ty,
+                                  _pack12(sb, sh, sl, e, f, g, r, s, t, u, v, w), positions.data_ptr(), pt,
+                                  _pack3(ps[0], ps[1] if len(n) == 3 else 0, ps[-1]), rope._h, inverse, ptr)
+        if code:
+            _check(code, "bsa_rope_apply")
         return qo, ko
-    return _on(device, stream, call)
+    return _on(dev, stream, call)
 
 
 # ---------------------------------------------------------------- norms and residual of a block
+def _vector_of(name, t, pt, C, dev):
+    """Refuses a parameter that is not a vector [C] of type pt on device dev; its address."""
+    if t.dtype is not pt or t.dim() != 1 or t.numel() != C or t.get_device() != dev or not t.is_contiguous():
+        raise ValueError(f"{name} must be a contiguous [C] on x's device, of one type with the other parameters")
+    return t.data_ptr()
+
+
 def _norm_args(x, y, post, post_weight, post_bias, gate, branch_scale, stream_scale, pre, pre_weight, pre_bias, eps):
-    ty, device, shape = _type_of(x.dtype), x.device, x.shape
-    if ty not in (BF16, FP16, FP32) or device.type != "cuda" or not x.is_contiguous() or not shape or shape[-1] < 1:
+    """(the C structure, rows, device index)"""
+    dtype, dev, shape, n = x.dtype, x.get_device(), x.shape, x.dim()
+    ty = _type_of(dtype)
+    if ty is None or ty > FP32 or dev < 0 or not x.is_contiguous() or n < 1 or shape[-1] < 1:
         raise ValueError("x must be a contiguous bf16, fp16 or fp32 CUDA tensor [.., C]")
     C = shape[-1]
-    B = shape[0] if len(shape) > 1 else 1
+    B = shape[0] if n > 1 else 1
     if post not in NORMS or pre not in NORMS:
         raise ValueError('post and pre must be "rms", "layer" or None')
-    if y is not None and (y.shape != shape or y.dtype is not x.dtype or not y.is_contiguous() or y.device != device):
+    if y is None:
+        if post is not None or gate is not None or pre is None or branch_scale != 1.0 or stream_scale != 1.0:
+            raise ValueError("without y there is the pre norm alone")
+    elif y.dtype is not dtype or y.shape != shape or y.get_device() != dev or not y.is_contiguous():
         raise ValueError("y must be like x")
-    if y is None and (post is not None or gate is not None or pre is None or branch_scale != 1.0 or
-                      stream_scale != 1.0):
-        raise ValueError("without y there is the pre norm alone")
-    pt, gate_rows = None, 1
-    for name, t in (("post_weight", post_weight), ("post_bias", post_bias), ("gate", gate),
-                    ("pre_weight", pre_weight), ("pre_bias", pre_bias)):
-        if t is None:
-            continue
-        if pt is None:
-            pt = t.dtype
-        if t.dtype is not pt or not t.is_contiguous() or t.device != device:
-            raise ValueError("parameters and gate must be contiguous, on x's device and of one type")
-        if t.dim() != 1 and name == "gate" and t.dim() == 2 and t.shape[0] in (1, B):
-            gate_rows = t.shape[0]
-        elif t.dim() != 1:
-            raise ValueError(f"{name} must be [C]" + (" or [B, C]" if name == "gate" else ""))
-        if t.shape[-1] != C:
-            raise ValueError(f"{name} must have C columns")
-    pt = ty if pt is None else _type_of(pt)
-    if pt != ty and pt != FP32:
-        raise ValueError("parameters and gate must be all of x's type or all fp32")
     if (post is None and (post_weight is not None or post_bias is not None)) or \
             (pre is None and (pre_weight is not None or pre_bias is not None)):
         raise ValueError("a weight or bias needs its norm")
+    pt = dtype
+    for t in (post_weight, pre_weight, gate, post_bias, pre_bias):
+        if t is not None:
+            pt = t.dtype
+            break
+    pty = ty if pt is dtype else _type_of(pt)
+    if pty != ty and pty != FP32:
+        raise ValueError("parameters and gate must be all of x's type or all fp32")
+    g, gate_rows = None, 1
+    if gate is not None:
+        if gate.dim() == 2 and gate.shape[0] in (1, B) and gate.shape[1] == C:
+            if gate.dtype is not pt or gate.get_device() != dev or not gate.is_contiguous():
+                raise ValueError("gate must be contiguous, on x's device and of one type with the parameters")
+            g, gate_rows = gate.data_ptr(), gate.shape[0]
+        else:
+            g = _vector_of("gate (or [B, C])", gate, pt, C, dev)
     rows = x.numel() // C
-    a = BlockNormArgs(B, rows // B if B else 0, C, ty, pt, NORMS[post], NORMS[pre],
-                      _ptr(post_weight), _ptr(post_bias), _ptr(gate), _ptr(pre_weight), _ptr(pre_bias), gate_rows,
-                      branch_scale, stream_scale, eps)
-    return a, rows
+    a = BlockNormArgs(
+        B, rows // B if B else 0, C, ty, pty, NORMS[post], NORMS[pre],
+        None if post_weight is None else _vector_of("post_weight", post_weight, pt, C, dev),
+        None if post_bias is None else _vector_of("post_bias", post_bias, pt, C, dev), g,
+        None if pre_weight is None else _vector_of("pre_weight", pre_weight, pt, C, dev),
+        None if pre_bias is None else _vector_of("pre_bias", pre_bias, pt, C, dev), gate_rows,
+        branch_scale, stream_scale, eps)
+    return a, rows, dev
 
 
 def bsa_block_norm(x, y=None, post: Optional[str] = None, post_weight=None, post_bias=None, gate=None,
@@ -709,23 +724,27 @@ def bsa_block_norm(x, y=None, post: Optional[str] = None, post_weight=None, post
     out and normed may be given; they may be x or y.
     """
     import torch
-    a, rows = _norm_args(x, y, post, post_weight, post_bias, gate, branch_scale, stream_scale, pre, pre_weight,
-                         pre_bias, eps)
-    for name, t in (("out", out), ("normed", normed)):
-        if t is not None and (t.shape != x.shape or t.dtype != x.dtype or not t.is_contiguous() or
-                              t.device != x.device):
-            raise ValueError(f"{name} must be like x")
-    if (out is not None and y is None) or (normed is not None and pre is None):
-        raise ValueError("an output was given that the call does not have")
+    a, rows, dev = _norm_args(x, y, post, post_weight, post_bias, gate, branch_scale, stream_scale, pre, pre_weight,
+                              pre_bias, eps)
+    if out is not None or normed is not None:
+        for name, t in (("out", out), ("normed", normed)):
+            if t is not None and (t.shape != x.shape or t.dtype != x.dtype or not t.is_contiguous() or
+                                  t.device != x.device):
+                raise ValueError(f"{name} must be like x")
+        if (out is not None and y is None) or (normed is not None and pre is None):
+            raise ValueError("an output was given that the call does not have")
 
     def call(ptr):
         o = torch.empty_like(x) if y is not None and out is None else out
         n = torch.empty_like(x) if pre is not None and normed is None else normed
         st = torch.empty((rows, 4), dtype=torch.float32, device=x.device) if save_stats else None
-        _check(lib.bsa_block_norm(ctypes.byref(a), x.data_ptr(), _ptr(y), _ptr(o), _ptr(n), _ptr(st), ptr),
-               "bsa_block_norm")
+        code = lib.bsa_block_norm(ctypes.byref(a), x.data_ptr(), None if y is None else y.data_ptr(),
+                                  None if o is None else o.data_ptr(), None if n is None else n.data_ptr(), _ptr(st),
+                                  ptr)
+        if code:
+            _check(code, "bsa_block_norm")
         return (x if y is None else o), n, st
-    return _on(x.device, stream, call)
+    return _on(dev, stream, call)
 
 
 def bsa_block_norm_backward(dstream, dnormed, x, y, stats, post: Optional[str] = None, post_weight=None,
@@ -740,8 +759,8 @@ def bsa_block_norm_backward(dstream, dnormed, x, y, stats, post: Optional[str] =
     False leaves the parameters' and the gate's gradients out.
     """
     import torch
-    a, rows = _norm_args(x, y, post, post_weight, post_bias, gate, branch_scale, stream_scale, pre, pre_weight,
-                         pre_bias, 0.0)
+    a, rows, dev = _norm_args(x, y, post, post_weight, post_bias, gate, branch_scale, stream_scale, pre, pre_weight,
+                              pre_bias, 0.0)
     for name, t in (("dstream", dstream), ("dnormed", dnormed)):
         if t is not None and (t.shape != x.shape or t.dtype != x.dtype or not t.is_contiguous() or
                               t.device != x.device):
@@ -769,7 +788,7 @@ def bsa_block_norm_backward(dstream, dnormed, x, y, stats, post: Optional[str] =
                                            _ptr(g["pre_bias"]), _ptr(ws), 0 if ws is None else ws.numel(), ptr),
                "bsa_block_norm_backward")
         return g
-    return _on(x.device, stream, call)
+    return _on(dev, stream, call)
 
 
 # ---------------------------------------------------------------- 8-bit floating point
@@ -784,42 +803,56 @@ def bsa_fp8_quantize(x, square: bool = False, rows: bool = True, cols: bool = Fa
     """
     import torch
     dtype = torch.float8_e4m3fn if dtype is None else dtype
-    ty, ct = _type_of(x.dtype), _type_of(dtype)
-    if ty not in (BF16, FP16, FP32) or not x.is_cuda or not x.is_contiguous() or x.dim() < 1 or x.shape[-1] < 1:
+    ty, ct, dev = _type_of(x.dtype), _type_of(dtype), x.get_device()
+    if ty is None or ty > FP32 or dev < 0 or not x.is_contiguous() or x.dim() < 1 or x.shape[-1] < 1:
         raise ValueError("x must be a contiguous bf16, fp16 or fp32 CUDA tensor [.., C]")
-    if ct not in (E4M3, E5M2):
+    if ct != E4M3 and ct != E5M2:
         raise ValueError("dtype must be torch.float8_e4m3fn or torch.float8_e5m2")
     if not rows and not cols:
         raise ValueError("ask for rows, cols or both")
     C = x.shape[-1]
     R = x.numel() // C
 
-    def form(n, m):  # codes [n, m] in padded rows, and their scales
+    def form(n, m):  # codes [n, m] in padded rows, their pitch, and their scales
         ld = (m + 15) // 16 * 16
-        codes = torch.empty((n, ld), dtype=dtype, device=x.device)
-        scale = torch.empty(((n + 127) // 128 if square else n, (m + 127) // 128), dtype=torch.float32,
-                            device=x.device)
-        return (codes if ld == m else codes[:, :m]), scale
+        codes = x.new_empty((n, ld), dtype=dtype)
+        scale = x.new_empty(((n + 127) // 128 if square else n, (m + 127) // 128), dtype=torch.float32)
+        return (codes if ld == m else codes[:, :m]), scale, ld
 
     def call(ptr):
-        got = (form(R, C) if rows else (None, None)) + (form(C, R) if cols else (None, None))
-        ld = (0 if got[0] is None else (C + 15) // 16 * 16, 0 if got[2] is None else (R + 15) // 16 * 16)
-        _check(lib.bsa_fp8_quantize(x.data_ptr(), ty, R, C, int(square), ct, _ptr(got[0]), ld[0], _ptr(got[1]),
-                                    _ptr(got[2]), ld[1], _ptr(got[3]), ptr), "bsa_fp8_quantize")
-        return tuple(t for t in got if t is not None)
-    return _on(x.device, stream, call)
+        codes, scale, ld = form(R, C) if rows else (None, None, 0)
+        codes_t, scale_t, ld_t = form(C, R) if cols else (None, None, 0)
+        code = lib.bsa_fp8_quantize(x.data_ptr(), ty, R, C, square, ct, _ptr(codes), ld, _ptr(scale), _ptr(codes_t),
+                                    ld_t, _ptr(scale_t), ptr)
+        if code:
+            _check(code, "bsa_fp8_quantize")
+        return (codes, scale, codes_t, scale_t) if rows and cols else (codes, scale) if rows else (codes_t, scale_t)
+    return _on(dev, stream, call)
 
 
-def _scale_rows(name, scale, rows, kb):
+def _codes_pitch(name, t, ty, dev) -> int:
+    """Refuses what is no matrix of 8-bit codes; the distance of its rows."""
+    if (ty != E4M3 and ty != E5M2) or t.dim() != 2 or t.get_device() != dev or dev < 0:
+        raise ValueError(f"{name} must be an 8-bit CUDA matrix")
+    ld, one = t.stride()
+    n = t.shape[1]
+    if n < 1 or (one != 1 and n > 1) or ld % 16 or ld < n or t.data_ptr() % 16:
+        raise ValueError(f"{name} must have contiguous columns and rows starting at multiples of 16 bytes")
+    return ld
+
+
+def _scale_rows(name, scale, rows, kb, dev) -> int:
     """How many rows share a scale: 1 or 128."""
-    import torch
-    if scale.dtype != torch.float32 or scale.dim() != 2 or not scale.is_contiguous() or scale.shape[1] != kb:
-        raise ValueError(f"{name} must be contiguous fp32 with one column for each 128 of K")
-    if scale.shape[0] == rows:
-        return 1
-    if scale.shape[0] == (rows + 127) // 128:
-        return 128
-    raise ValueError(f"{name} must have a row for each row, or for each 128 rows, of its matrix")
+    if _type_of(scale.dtype) != FP32 or scale.dim() != 2 or not scale.is_contiguous() or scale.get_device() != dev:
+        raise ValueError(f"{name} must be a contiguous fp32 matrix on the codes' device")
+    n, m = scale.shape
+    if m == kb:
+        if n == rows:
+            return 1
+        if n == (rows + 127) // 128:
+            return 128
+    raise ValueError(f"{name} must have a row for each row, or for each 128 rows, of its matrix, and a column for "
+                     "each 128 of K")
 
 
 def bsa_fp8_matmul_workspace_bytes(M: int, N: int, K: int) -> int:
@@ -838,41 +871,46 @@ def bsa_fp8_matmul(a, a_scale, b, b_scale, bias=None, out_dtype=None, out=None, 
     omitted.
     """
     import torch
-    at, bt = _type_of(a.dtype), _type_of(b.dtype)
-    for name, t, ty in (("a", a, at), ("b", b, bt)):
-        if ty not in (E4M3, E5M2) or not t.is_cuda or t.dim() != 2 or t.shape[1] < 1 or \
-                (t.shape[1] > 1 and t.stride(1) != 1) or t.stride(0) % 16 or t.stride(0) < t.shape[1] or \
-                t.data_ptr() % 16:
-            raise ValueError(f"{name} must be an 8-bit CUDA matrix whose rows start at multiples of 16 bytes")
-    (M, K), N = a.shape, b.shape[0]
-    if b.shape[1] != K:
+    at, bt, dev = _type_of(a.dtype), _type_of(b.dtype), a.get_device()
+    lda, ldb = _codes_pitch("a", a, at, dev), _codes_pitch("b", b, bt, dev)
+    (M, K), (N, Kb) = a.shape, b.shape
+    if Kb != K:
         raise ValueError("a and b must have the same number of columns")
     kb = (K + 127) // 128
-    ar, br = _scale_rows("a_scale", a_scale, M, kb), _scale_rows("b_scale", b_scale, N, kb)
-    if bias is not None and (_type_of(bias.dtype) not in (BF16, FP32) or tuple(bias.shape) != (N,) or
-                             not bias.is_contiguous()):
-        raise ValueError("bias must be a contiguous bf16 or fp32 vector [N]")
+    ar, br = _scale_rows("a_scale", a_scale, M, kb, dev), _scale_rows("b_scale", b_scale, N, kb, dev)
+    bp, bty = None, BF16
+    if bias is not None:
+        bty = _type_of(bias.dtype)
+        if bty not in (BF16, FP32) or bias.dim() != 1 or bias.numel() != N or not bias.is_contiguous() or \
+                bias.get_device() != dev:
+            raise ValueError("bias must be a contiguous bf16 or fp32 vector [N]")
+        bp = bias.data_ptr()
     if out is not None:
-        if out_dtype not in (None, out.dtype) or tuple(out.shape) != (M, N) or not out.is_contiguous():
+        if out_dtype not in (None, out.dtype) or tuple(out.shape) != (M, N) or not out.is_contiguous() or \
+                out.get_device() != dev:
             raise ValueError("out must be a contiguous tensor [M, N] of the result's type")
         out_dtype = out.dtype
     out_dtype = torch.bfloat16 if out_dtype is None else out_dtype
-    if _type_of(out_dtype) not in (BF16, FP32):
+    ot = _type_of(out_dtype)
+    if ot != BF16 and ot != FP32:
         raise ValueError("the result is bf16 or fp32")
-    _check_same(a.device, b=b, a_scale=a_scale, b_scale=b_scale, bias=bias, out=out, workspace=workspace)
+    if workspace is not None and workspace.get_device() != dev:
+        raise ValueError("workspace must be on a's device")
 
     def call(ptr):
-        o = torch.empty((M, N), dtype=out_dtype, device=a.device) if out is None else out
-        ws = workspace
-        if ws is None and M > 8:
+        o = a_scale.new_empty((M, N), dtype=out_dtype) if out is None else out
+        ws, n = workspace, 0
+        if ws is not None:
+            n = ws.numel() * ws.element_size()
+        elif M > 8:  # fewer rows never split K
             n = bsa_fp8_matmul_workspace_bytes(M, N, K)
-            ws = torch.empty(n, dtype=torch.uint8, device=a.device) if n else None
-        _check(lib.bsa_fp8_matmul(a.data_ptr(), at, a.stride(0), a_scale.data_ptr(), ar, b.data_ptr(), bt, b.stride(0),
-                                  b_scale.data_ptr(), br, _ptr(bias), BF16 if bias is None else _type_of(bias.dtype),
-                                  M, N, K, o.data_ptr(), _type_of(out_dtype), _ptr(ws),
-                                  0 if ws is None else ws.numel() * ws.element_size(), ptr), "bsa_fp8_matmul")
+            ws = a_scale.new_empty(n, dtype=torch.uint8) if n else None
+        code = lib.bsa_fp8_matmul(a.data_ptr(), at, lda, a_scale.data_ptr(), ar, b.data_ptr(), bt, ldb,
+                                  b_scale.data_ptr(), br, bp, bty, M, N, K, o.data_ptr(), ot, _ptr(ws), n, ptr)
+        if code:
+            _check(code, "bsa_fp8_matmul")
         return o
-    return _on(a.device, stream, call)
+    return _on(dev, stream, call)
 
 
 def bsa_sync_status(stream=None) -> int:
