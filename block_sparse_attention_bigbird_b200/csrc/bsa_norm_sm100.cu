@@ -644,8 +644,8 @@ struct SumParams {
   const void *post_w, *post_b, *gate;
   void *dpost_w, *dpost_b, *dgate, *dpre_w, *dpre_b;
   int64_t rows, per_gate, rows_per_block, blocks;
-  int C, gate_rows, means, has_y, has_pre, param_type;
-  int lanes_per_gate;  // of the 32 lanes a column has: power of two, 32 / it >= gate rows or 1
+  int C, gate_rows, has_y, has_pre, param_type;
+  int lanes_per_gate;  // of a column's lanes: power of two, lanes / it >= gate rows or 1
   float alpha;
 };
 
@@ -664,17 +664,17 @@ __device__ __forceinline__ void param_put(void* p, int64_t i, int type, float v)
 
 // Sums of slots first, first + step, .. < n of one column (two quantities C apart each): eight
 // slots are on their way at once.
-__device__ __forceinline__ void sum_slots(const float* from, int64_t n, int first, int step, int C, int means, float& a,
-                                          float& b) {
-  const int64_t stride = static_cast<int64_t>(1 + means) * C;
-  for (int64_t k = first; k < n; k += 8 * step) {
+template <bool kMeans>
+__device__ __forceinline__ void sum_slots(const float* from, int n, int first, int step, int C, float& a, float& b) {
+  const int64_t stride = (kMeans ? 2 : 1) * static_cast<int64_t>(C), far = step * stride;
+  from += first * stride;
+  for (int k = first; k < n; k += 8 * step) {
     float x[8], y[8];
 #pragma unroll
-    for (int i = 0; i < 8; ++i) {
+    for (int i = 0; i < 8; ++i, from += far) {
       const bool there = k + i * step < n;
-      const float* q = from + (k + i * step) * stride;
-      x[i] = there ? __ldg(q) : 0.f;
-      y[i] = there && means ? __ldg(q + C) : 0.f;
+      x[i] = there ? __ldg(from) : 0.f;
+      y[i] = kMeans && there ? __ldg(from + C) : 0.f;
     }
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
@@ -684,18 +684,23 @@ __device__ __forceinline__ void sum_slots(const float* from, int64_t n, int firs
   }
 }
 
-// Adds the slots: 32 columns a block, 32 lanes (warps) a column.
+// Adds the slots: 32 columns a block, blockDim.y lanes (warps) a column, the gate's and the post
+// norm's sums in blocks with blockIdx.y = 0 and the pre norm's in those with 1.  Launched as the
+// backward's programmatic dependent: its launch overlaps the backward's end.
+template <bool kMeans>
 __global__ void __launch_bounds__(1024) bsa_block_norm_sum_kernel(const SumParams p) {
-  __shared__ float buf[4][32][33];
-  const int lane = threadIdx.x, ty = threadIdx.y;
+  __shared__ float buf[2][32][33];
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  const int lane = threadIdx.x, ty = threadIdx.y, lanes = blockDim.y;
   const int c = blockIdx.x * 32 + lane;
-  const bool in = c < p.C;
-  float dw = 0.f, db = 0.f, P = 0.f, Q = 0.f;
-  if (p.has_pre && in) sum_slots(p.part_pre + c, p.blocks, ty, 32, p.C, p.means, P, Q);
-  if (p.has_y) {
-    // lane group `bb` of the 32 / lanes_per_gate takes gate rows bb, bb + groups, ...; its
+  const bool in = c < p.C, post = blockIdx.y == 0;
+  float dw = 0.f, db = 0.f;
+  if (!post) {
+    if (p.has_pre && in) sum_slots<kMeans>(p.part_pre + c, static_cast<int>(p.blocks), ty, lanes, p.C, dw, db);
+  } else if (p.has_y) {
+    // lane group `bb` of the lanes / lanes_per_gate takes gate rows bb, bb + groups, ...; its
     // lanes share the slots of one
-    const int per = p.lanes_per_gate, sub = ty % per, bb = ty / per, groups = 32 / per;
+    const int per = p.lanes_per_gate, sub = ty % per, bb = ty / per, groups = lanes / per;
     const float w = in ? param_at(p.post_w, c, p.param_type, 1.f) : 0.f;
     const float b = in ? param_at(p.post_b, c, p.param_type, 0.f) : 0.f;
     for (int64_t g = bb; g < p.gate_rows; g += groups) {
@@ -703,9 +708,10 @@ __global__ void __launch_bounds__(1024) bsa_block_norm_sum_kernel(const SumParam
       const int64_t lo = g * p.per_gate / p.rows_per_block;
       const int64_t hi = p.rows == 0 ? -1 : min((min((g + 1) * p.per_gate, p.rows) - 1) / p.rows_per_block, p.blocks - 1);
       float S = 0.f, T = 0.f;
-      if (in) sum_slots(p.part + (g + lo) * (1 + p.means) * p.C + c, hi - lo + 1, sub, per, p.C, p.means, S, T);
+      if (in)
+        sum_slots<kMeans>(p.part + (g + lo) * (kMeans ? 2 : 1) * p.C + c, static_cast<int>(hi - lo + 1), sub, per, p.C, S, T);
       if (per > 1) {
-        // groups * per = 32 and one pass: every lane comes here exactly once
+        // groups * per = lanes and one pass: every lane comes here at most once
         buf[0][ty][lane] = S;
         buf[1][ty][lane] = T;
       } else {
@@ -731,15 +737,11 @@ __global__ void __launch_bounds__(1024) bsa_block_norm_sum_kernel(const SumParam
   }
   buf[0][ty][lane] = dw;
   buf[1][ty][lane] = db;
-  buf[2][ty][lane] = P;
-  buf[3][ty][lane] = Q;
   __syncthreads();
-  if (ty < 4 && in) {
+  if (ty < 2 && in) {
     float s = 0.f;
-#pragma unroll
-    for (int k = 0; k < 32; ++k) s += buf[ty][k][lane];
-    void* to[4] = {p.dpost_w, p.dpost_b, p.dpre_w, p.dpre_b};
-    param_put(ty == 0 ? to[0] : ty == 1 ? to[1] : ty == 2 ? to[2] : to[3], c, p.param_type, s);
+    for (int k = 0; k < lanes; ++k) s += buf[ty][k][lane];
+    param_put(post ? (ty == 0 ? p.dpost_w : p.dpost_b) : (ty == 0 ? p.dpre_w : p.dpre_b), c, p.param_type, s);
   }
 }
 
@@ -1021,14 +1023,26 @@ int bsa_block_norm_backward(const bsa_block_norm_args* args, const void* dstream
     q.post_w = a.post_weight, q.post_b = a.post_bias, q.gate = a.gate;
     q.dpost_w = dpost_weight, q.dpost_b = dpost_bias, q.dgate = dgate, q.dpre_w = dpre_weight, q.dpre_b = dpre_bias;
     q.rows = p.rows, q.per_gate = p.per_gate, q.rows_per_block = b.rows_per_block, q.blocks = b.blocks;
-    q.C = a.C, q.gate_rows = a.gate_rows, q.means = means;
+    q.C = a.C, q.gate_rows = a.gate_rows;
     q.has_y = p.rows == 0 || y != nullptr;
     q.has_pre = dnormed != nullptr;
     q.param_type = a.param_type, q.alpha = a.branch_scale;
-    int lanes = 1;
-    while (lanes < 32 && 32 / (2 * lanes) >= a.gate_rows) lanes *= 2;
-    q.lanes_per_gate = lanes;
-    bsa_block_norm_sum_kernel<<<(a.C + 31) / 32, dim3(32, 32), 0, s>>>(q);
+    // few lanes start and end sooner; more share many gate rows
+    const int lanes = a.gate_rows <= 8 ? 8 : 32;
+    int per = 1;
+    while (per < lanes && lanes / (2 * per) >= a.gate_rows) per *= 2;
+    q.lanes_per_gate = per;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cudaLaunchConfig_t cfg{};
+    cfg.gridDim = dim3((a.C + 31) / 32, 2);
+    cfg.blockDim = dim3(32, lanes);
+    cfg.stream = s;
+    cfg.attrs = attr;
+    cfg.numAttrs = p.rows > 0 ? 1 : 0;  // the backward comes directly before, unless it had no rows
+    ok = ok && (means ? cudaLaunchKernelEx(&cfg, bsa_block_norm_sum_kernel<true>, q)
+                      : cudaLaunchKernelEx(&cfg, bsa_block_norm_sum_kernel<false>, q)) == cudaSuccess;
   }
   return cudaGetLastError() == cudaSuccess && ok ? BSA_OK : BSA_ERR_CUDA;
 }
