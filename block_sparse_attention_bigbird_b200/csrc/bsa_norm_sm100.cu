@@ -236,9 +236,10 @@ __device__ __forceinline__ float2 statistics(Pairs<kVec * kNV>& v, int kind, con
 }
 
 constexpr int kWarpBlock = 128;  // threads of a forward block whose teams are warps
-// Threads of a backward block at most: where a thread has more than eight elements of a row
-// (in teams of a warp) it needs 168 registers, else 128 do.
-constexpr int kBackBlock = 512, kBackWarpBlock = 384;
+// Threads of a backward block at most: where a thread has more than eight elements of a row it
+// needs 168 registers, else 128 do.  (Rows of more than 4096 columns take 512 threads whatever
+// that costs.)
+constexpr int kBackBlock = 512, kBackWideBlock = 384;
 // Teams of a block that meet at a barrier of their own: ids 1 to 15 (0 is the block's).
 constexpr int kNamedBarriers = 15;
 
@@ -762,14 +763,16 @@ Team team_of(int C, size_t esize, bool aligned, bool backward, bool means) {
   t.vec = aligned && C % 8 == 0 ? 8 : aligned && C % 2 == 0 ? 2 : 1;
   const int n = C / t.vec;
   // A warp takes a row while a lane's share fits its registers (the backward keeps two sums
-  // a column, four with plain means), else the block with few pieces a thread.
+  // a column, four with plain means), else the block, with as many elements a thread as 384
+  // threads have registers for: what a team does once a row, its sums, is then shared by
+  // fewer warps (4113 fp32 rows of 1030, backward: 4, 6 pieces of two took 46, 38 us).
   const int most = t.vec < 8 ? 0 : backward && means ? 2 : 3;
   if (n <= 32 * most) {
     t.nv = (n + 31) / 32;
     t.threads = 32;
     t.warp = true;
   } else {
-    t.nv = t.vec == 8 ? (n <= 512 ? 1 : 2) : t.vec == 2 ? (n <= 2048 ? 4 : 8) : (n <= 4096 ? 8 : 16);
+    t.nv = t.vec == 8 ? (n <= 512 ? 1 : 2) : t.vec == 2 ? (n <= 2048 ? 6 : 8) : (n <= 4096 ? 12 : 16);
     t.threads = ((n + t.nv - 1) / t.nv + 31) / 32 * 32;
   }
   const auto slot = [&] { return static_cast<size_t>(t.threads * t.teams) * (backward ? 4 : 2) * t.nv * t.vec * esize; };
@@ -789,7 +792,7 @@ Team team_of(int C, size_t esize, bool aligned, bool backward, bool means) {
   const auto fixed = [&] {
     return (3 * static_cast<size_t>(t.nv * t.vec) * t.threads + t.teams * 2 * (means ? 2 : 1) * 32) * sizeof(float);
   };
-  t.teams = std::max(1, (t.warp && t.nv > 1 ? kBackWarpBlock : kBackBlock) / t.threads);
+  t.teams = std::max(1, (t.nv * t.vec > 8 ? kBackWideBlock : kBackBlock) / t.threads);
   if (!t.warp) t.teams = std::min(t.teams, kNamedBarriers);
   t.depth = 2;
   while (t.teams > 1 && fixed() + 2 * slot() > kSmemMost) --t.teams;
@@ -860,9 +863,9 @@ bool launch_norm(const NormParams& p, const Team& t, int64_t blocks, cudaStream_
     return t.nv == 1 ? start(bsa_block_norm_kernel<T, 8, 1, false, kBias>, p, t, blocks, s)
                      : start(bsa_block_norm_kernel<T, 8, 2, false, kBias>, p, t, blocks, s);
   if (t.vec == 2)
-    return t.nv == 4 ? start(bsa_block_norm_kernel<T, 2, 4, false, kBias>, p, t, blocks, s)
+    return t.nv == 6 ? start(bsa_block_norm_kernel<T, 2, 6, false, kBias>, p, t, blocks, s)
                      : start(bsa_block_norm_kernel<T, 2, 8, false, kBias>, p, t, blocks, s);
-  return t.nv == 8 ? start(bsa_block_norm_kernel<T, 1, 8, false, kBias>, p, t, blocks, s)
+  return t.nv == 12 ? start(bsa_block_norm_kernel<T, 1, 12, false, kBias>, p, t, blocks, s)
                    : start(bsa_block_norm_kernel<T, 1, 16, false, kBias>, p, t, blocks, s);
 }
 template <typename T>
@@ -892,7 +895,7 @@ BackPlan back_plan(const NormParams& p, const Team& t, int gate_rows, bool means
 
 template <typename T, bool kMeans>
 bool launch_back(const NormParams& p, const Team& t, const BackPlan& b, cudaStream_t s) {
-  constexpr int kB = kBackBlock, kW = kBackWarpBlock;
+  constexpr int kB = kBackBlock, kW = kBackWideBlock;
   if (t.warp) {
     if (t.nv == 1) return start(bsa_block_norm_back_kernel<T, 8, 1, true, kMeans, kB>, p, t, b.blocks, s);
     if constexpr (!kMeans)
@@ -903,9 +906,9 @@ bool launch_back(const NormParams& p, const Team& t, const BackPlan& b, cudaStre
     return t.nv == 1 ? start(bsa_block_norm_back_kernel<T, 8, 1, false, kMeans, kB>, p, t, b.blocks, s)
                      : start(bsa_block_norm_back_kernel<T, 8, 2, false, kMeans, kB>, p, t, b.blocks, s);
   if (t.vec == 2)
-    return t.nv == 4 ? start(bsa_block_norm_back_kernel<T, 2, 4, false, kMeans, kB>, p, t, b.blocks, s)
+    return t.nv == 6 ? start(bsa_block_norm_back_kernel<T, 2, 6, false, kMeans, kW>, p, t, b.blocks, s)
                      : start(bsa_block_norm_back_kernel<T, 2, 8, false, kMeans, kB>, p, t, b.blocks, s);
-  return t.nv == 8 ? start(bsa_block_norm_back_kernel<T, 1, 8, false, kMeans, kB>, p, t, b.blocks, s)
+  return t.nv == 12 ? start(bsa_block_norm_back_kernel<T, 1, 12, false, kMeans, kW>, p, t, b.blocks, s)
                    : start(bsa_block_norm_back_kernel<T, 1, 16, false, kMeans, kB>, p, t, b.blocks, s);
 }
 
