@@ -124,9 +124,9 @@ def block_norm(x: torch.Tensor, y: Optional[torch.Tensor] = None, post: Optional
 
 class _Fp8Linear(torch.autograd.Function):
     @staticmethod
-    def forward(ctx, x, weight, bias, grad_dtype):
+    def forward(ctx, x, weight, bias, grad_dtype, grads):
         rows = x.reshape(-1, x.shape[-1]).contiguous()
-        need_x, need_w = ctx.needs_input_grad[:2]
+        need_x, need_w = (grads and need for need in ctx.needs_input_grad[:2])
         xs = bsa.bsa_fp8_quantize(rows, cols=need_w)
         ws = bsa.bsa_fp8_quantize(weight.contiguous(), square=True, cols=need_x)
         y = bsa.bsa_fp8_matmul(xs[0], xs[1], ws[0], ws[1], bias=bias, out_dtype=x.dtype)
@@ -154,7 +154,7 @@ class _Fp8Linear(torch.autograd.Function):
                 dw = bsa.bsa_fp8_matmul(q[-2], q[-1], xt, xt_scale, out_dtype=wide).to(w_dtype)
         if need_b:
             db = dy.sum(0, dtype=torch.float32).to(b_dtype)
-        return dx, dw, db, None
+        return dx, dw, db, None, None
 
 
 def fp8_linear(x: torch.Tensor, weight: torch.Tensor, bias: Optional[torch.Tensor] = None,
@@ -172,4 +172,5 @@ def fp8_linear(x: torch.Tensor, weight: torch.Tensor, bias: Optional[torch.Tenso
         raise ValueError("x must be bf16 or fp32")
     if weight.dim() != 2 or x.dim() < 1 or x.shape[-1] != weight.shape[1]:
         raise ValueError("x must be [.., K] and weight [N, K]")
-    return _Fp8Linear.apply(x, weight, bias, grad_dtype)
+    # inside a Function gradients are always off, so whether any are wanted is asked here
+    return _Fp8Linear.apply(x, weight, bias, grad_dtype, torch.is_grad_enabled())

@@ -309,6 +309,8 @@ def test_linear_parts_and_no_rows():
     dx, = torch.autograd.grad(fp8_linear(xg, w.detach()).sum(), xg)
     both = torch.autograd.grad(fp8_linear(xg, w).sum(), (xg, w))
     assert torch.equal(both[0], dx) and torch.equal(both[1], dw)
+    with torch.no_grad():
+        assert torch.equal(fp8_linear(xg, w), fp8_linear(xg.detach(), w.detach()))
     for bad in (x.half(), x[:, :60]):
         with pytest.raises(ValueError):
             fp8_linear(bad, w)
