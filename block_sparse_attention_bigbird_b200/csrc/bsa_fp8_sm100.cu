@@ -636,21 +636,50 @@ __global__ void __launch_bounds__(kMThreads, 1) bsa_fp8_mma_kernel(const __grid_
   if (warp == 1) ptx::tmem_dealloc(tmem, kTmem);
 }
 
-// Sums the splits' partial results in order, adds the bias and rounds once.
+// Sums the splits' partial results in order, adds the bias and rounds once; kVec elements a
+// thread (4 where rows of the result are multiples of 4).  Launched as the product's
+// programmatic dependent: its launch overlaps the product's end.
+template <int kVec>
 __global__ void __launch_bounds__(256) bsa_fp8_sum_kernel(const float* part, int splits, int64_t stride, int64_t n,
                                                           int N, const void* bias, int bias_f32, void* out,
                                                           int out_f32) {
-  const int64_t i = static_cast<int64_t>(blockIdx.x) * 256 + threadIdx.x;
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  const int64_t i = (static_cast<int64_t>(blockIdx.x) * 256 + threadIdx.x) * kVec;
   if (i >= n) return;
-  float v = 0.f;
-#pragma unroll 8
-  for (int s = 0; s < splits; ++s) v += part[s * stride + i];
+  float v[kVec] = {};
+  for (int s0 = 0; s0 < splits; s0 += 8) {
+    float x[8][kVec];
+#pragma unroll
+    for (int s = 0; s < 8; ++s) {
+      const float* from = part + (s0 + s) * stride + i;
+      if constexpr (kVec == 4) {
+        const float4 q = s0 + s < splits ? *reinterpret_cast<const float4*>(from) : make_float4(0.f, 0.f, 0.f, 0.f);
+        x[s][0] = q.x, x[s][1] = q.y, x[s][2] = q.z, x[s][3] = q.w;
+      } else {
+        x[s][0] = s0 + s < splits ? *from : 0.f;
+      }
+    }
+#pragma unroll
+    for (int s = 0; s < 8; ++s)
+#pragma unroll
+      for (int e = 0; e < kVec; ++e) v[e] += x[s][e];
+  }
   if (bias != nullptr) {
     const int c = static_cast<int>(i % N);
-    v += bias_f32 ? static_cast<const float*>(bias)[c] : __bfloat162float(static_cast<const __nv_bfloat16*>(bias)[c]);
+#pragma unroll
+    for (int e = 0; e < kVec; ++e)
+      v[e] += bias_f32 ? static_cast<const float*>(bias)[c + e]
+                       : __bfloat162float(static_cast<const __nv_bfloat16*>(bias)[c + e]);
   }
-  if (out_f32) static_cast<float*>(out)[i] = v;
-  else static_cast<__nv_bfloat16*>(out)[i] = __float2bfloat16_rn(v);
+  if constexpr (kVec == 4) {
+    if (out_f32) *reinterpret_cast<float4*>(static_cast<float*>(out) + i) = make_float4(v[0], v[1], v[2], v[3]);
+    else
+      *reinterpret_cast<uint2*>(static_cast<__nv_bfloat16*>(out) + i) =
+          make_uint2(pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3]));
+  } else {
+    if (out_f32) static_cast<float*>(out)[i] = v[0];
+    else static_cast<__nv_bfloat16*>(out)[i] = __float2bfloat16_rn(v[0]);
+  }
 }
 
 // ------------------------------------------------------------ a few rows
@@ -1093,9 +1122,23 @@ int bsa_fp8_matmul(const void* a, int a_type, int64_t lda, const float* a_scale,
   const int grid = static_cast<int>(std::min<int64_t>(units, sms));
   if (plan.bn == 256) launch_mma<256>(p, grid, s);
   else launch_mma<128>(p, grid, s);
-  if (split)
-    bsa_fp8_sum_kernel<<<static_cast<unsigned>((n + 255) / 256), 256, 0, s>>>(
-        static_cast<const float*>(workspace), plan.splits, n, n, N, bias, bias_f32, out, out_f32);
+  if (split) {
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    const bool four = N % 4 == 0 && aligned16(out);
+    cudaLaunchConfig_t cfg{};
+    cfg.gridDim = dim3(static_cast<unsigned>(((four ? n / 4 : n) + 255) / 256));
+    cfg.blockDim = dim3(256);
+    cfg.stream = s;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    const float* part = static_cast<const float*>(workspace);
+    if ((four ? cudaLaunchKernelEx(&cfg, bsa_fp8_sum_kernel<4>, part, plan.splits, n, n, N, bias, bias_f32, out, out_f32)
+              : cudaLaunchKernelEx(&cfg, bsa_fp8_sum_kernel<1>, part, plan.splits, n, n, N, bias, bias_f32, out,
+                                   out_f32)) != cudaSuccess)
+      return BSA_ERR_CUDA;
+  }
   return cudaGetLastError() == cudaSuccess ? BSA_OK : BSA_ERR_CUDA;
 }
 
