@@ -170,7 +170,7 @@ def fp8_linear(x: torch.Tensor, weight: torch.Tensor, bias: Optional[torch.Tenso
     """
     if x.dtype not in (torch.bfloat16, torch.float32):
         raise ValueError("x must be bf16 or fp32")
-    if weight.dim() != 2 or x.dim() < 1 or x.shape[-1] != weight.shape[1]:
-        raise ValueError("x must be [.., K] and weight [N, K]")
+    if weight.dim() != 2 or weight.numel() == 0 or x.dim() < 1 or x.shape[-1] != weight.shape[1]:
+        raise ValueError("x must be [.., K] and weight [N, K], N and K at least 1")
     # inside a Function gradients are always off, so whether any are wanted is asked here
     return _Fp8Linear.apply(x, weight, bias, grad_dtype, torch.is_grad_enabled())

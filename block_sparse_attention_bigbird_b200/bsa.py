@@ -544,6 +544,10 @@ class Rope:
     def handle(self) -> ctypes.c_void_p:
         return self._h
 
+    def __reduce__(self):  # copied and stored by its tables, with the module that holds it
+        axis, freq = bsa_rope_table(self)
+        return bsa_rope_from_table, (axis, freq, self.adjacent)
+
     def __del__(self):
         h = getattr(self, "_h", None)
         if h is not None and h.value and lib is not None:   # lib is None at interpreter exit
@@ -598,7 +602,8 @@ def bsa_rope_apply(q, k, positions, rope: Rope, inverse: bool = False, q_out=Non
     bf16, fp16 or fp32 CUDA tensors of any strides with contiguous columns (views of a packed
     projection too).  positions: int32, int64 or fp32 [axes, L], shared by the batch, or
     [axes, B, L].  ``inverse`` turns back (the gradient).  Results are new contiguous tensors,
-    or q_out and k_out, which may be q and k themselves; other overlaps are not allowed.
+    or q_out and k_out, which may be q and k themselves; other overlaps are not allowed (and
+    refused where two of them start at one address).
     """
     dev, dtype = q.get_device(), q.dtype
     ty, pt = _type_of(dtype), _type_of(positions.dtype)
@@ -721,7 +726,7 @@ def bsa_block_norm(x, y=None, post: Optional[str] = None, post_weight=None, post
     each index of x's first axis.  Parameters and gate are all of x's type or all fp32; None
     stands for 1 (weights, gate) and 0 (biases).  Without y the stream is x itself and only
     the pre norm is taken.  stats (with ``save_stats``): fp32 [rows, 4], for the backward.
-    out and normed may be given; they may be x or y.
+    out and normed may be given; they may be x or y, not each other.
     """
     import torch
     a, rows, dev = _norm_args(x, y, post, post_weight, post_bias, gate, branch_scale, stream_scale, pre, pre_weight,

@@ -99,7 +99,7 @@ struct MmaParams {
   int a_shift, b_rows;  // row of sa = m >> a_shift; b_rows: a scale for each row of b
   int bias_f32, out_f32;
   int idesc_formats;    // A and B format bits of the instruction descriptor
-  int m_tiles, n_tiles, splits, kb_split, units;
+  int n_tiles, splits, kb_split, units;
   int64_t split_stride;  // elements of one split's partial result (splits > 1: out is fp32 partials)
   uint64_t timeout_ns;
 };
@@ -1104,9 +1104,9 @@ int bsa_fp8_matmul(const void* a, int a_type, int64_t lda, const float* a_scale,
   p.M = M, p.N = N, p.kb = kb;
   p.a_shift = a_rows == 128 ? 7 : 0, p.b_rows = b_rows == 1;
   p.idesc_formats = (format_bits(a_type) << 7) | (format_bits(b_type) << 10);
-  p.m_tiles = (M + kMB - 1) / kMB, p.n_tiles = (N + plan.bn - 1) / plan.bn;
+  p.n_tiles = (N + plan.bn - 1) / plan.bn;
   p.splits = plan.splits, p.kb_split = plan.kb_split;
-  const int64_t units = static_cast<int64_t>(p.m_tiles) * p.n_tiles * p.splits;
+  const int64_t units = static_cast<int64_t>((M + kMB - 1) / kMB) * p.n_tiles * p.splits;
   if (units > (1 << 30)) return BSA_ERR_INVALID_ARG;
   p.units = static_cast<int>(units);
   p.timeout_ns = kDefaultTimeoutNs;

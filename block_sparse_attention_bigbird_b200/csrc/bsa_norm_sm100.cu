@@ -937,6 +937,7 @@ int bsa_block_norm(const bsa_block_norm_args* args, const void* x, const void* y
     return BSA_ERR_INVALID_ARG;
   if (y == nullptr && (a.post != BSA_NORM_NONE || a.gate != nullptr || a.pre == BSA_NORM_NONE))
     return BSA_ERR_INVALID_ARG;
+  if (y != nullptr && a.pre != BSA_NORM_NONE && stream_out == normed) return BSA_ERR_INVALID_ARG;
   if (p.rows > 0x7fffffff || misaligned(a.type, {x, y, stream_out, normed}) ||
       (stats != nullptr && !aligned16(stats)))
     return BSA_ERR_INVALID_ARG;
@@ -992,7 +993,7 @@ int bsa_block_norm_backward(const bsa_block_norm_args* args, const void* dstream
       return BSA_ERR_INVALID_ARG;
     if (y == nullptr && (a.post != BSA_NORM_NONE || a.gate != nullptr || a.pre == BSA_NORM_NONE))
       return BSA_ERR_INVALID_ARG;
-    if (dnormed != nullptr && a.pre == BSA_NORM_NONE) return BSA_ERR_INVALID_ARG;
+    if ((dnormed != nullptr && a.pre == BSA_NORM_NONE) || dx == dy) return BSA_ERR_INVALID_ARG;
     if (p.rows > 0x7fffffff || misaligned(a.type, {x, y, dstream, dnormed, dx, dy}) || !aligned16(stats))
       return BSA_ERR_INVALID_ARG;
   }

@@ -257,6 +257,8 @@ int bsa_rope_apply(const void* q, void* q_out, int H, const void* k, void* k_out
   if (B == 0 || L == 0 || H + static_cast<int64_t>(Hk) == 0) return BSA_OK;
   if ((H > 0 && (q == nullptr || q_out == nullptr)) || (Hk > 0 && k_out == nullptr) || positions == nullptr)
     return BSA_ERR_INVALID_ARG;
+  // one result may not be the other's, nor the other's input
+  if (H > 0 && Hk > 0 && (q_out == k_out || q_out == k || k_out == q)) return BSA_ERR_INVALID_ARG;
   RopeParams p;
   const size_t es = type_bytes(type);
   bool vec = d % 8 == 0 && pairs % 8 == 0;

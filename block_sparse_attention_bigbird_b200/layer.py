@@ -194,8 +194,10 @@ class BigBirdBlock(torch.nn.Module):
                 positions: Optional[torch.Tensor] = None, gate: Optional[torch.Tensor] = None,
                 normed: Optional[torch.Tensor] = None, following: Optional["BigBirdBlock"] = None):
         """The stream after the block; with ``following`` (stream, its normed input), to be passed
-        to that block as ``normed``.  x: contiguous [B, L, dim].
+        to that block as ``normed`` (its eps must be this block's).  x: contiguous [B, L, dim].
         """
+        if following is not None and following.eps != self.eps:
+            raise ValueError("one pass takes both norms with one eps: the following block has another")
         if normed is None:
             _, normed = block_norm(x, pre=self.pre, pre_weight=self.pre_weight, pre_bias=self.pre_bias, eps=self.eps)
         y = self.attention(normed, key_mask=key_mask, positions=positions)

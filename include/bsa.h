@@ -440,7 +440,8 @@ void bsa_rope_free(bsa_rope* rope);
  *             [B, Hk, L, d] with the element strides below; columns contiguous.  k may be
  *             NULL (Hk ignored).
  *   q_out, k_out  device, the same shapes; may be q and k themselves with the same strides
- *             (any other overlap gives undefined results).
+ *             (q_out at k, k_out or k_out at q is BSA_ERR_INVALID_ARG, any other overlap gives
+ *             undefined results).
  *   strides   host, 12 int64: (b, h, l) of q, of q_out, of k, of k_out.
  *   positions device, BSA_INT32, BSA_INT64 or BSA_FP32: element
  *             a p_strides[0] + b p_strides[1] + l p_strides[2] is p[a, b, l]
@@ -482,7 +483,8 @@ typedef struct {
 /*
  * bsa_block_norm -- the forward.  x, y: device, `type`, [rows, C] contiguous; y NULL for the
  * norm alone (then post = BSA_NORM_NONE, no gate).  stream_out (NULL without y) and normed
- * (NULL with pre = BSA_NORM_NONE): written, `type`; they may be x or y themselves.
+ * (NULL with pre = BSA_NORM_NONE): written, `type`; they may be x or y themselves,
+ * not each other.
  * stats: device fp32 [rows, 4] or NULL: mean and 1/sqrt(..) of the post norm, then of the
  * pre norm (0 where there is none), for the backward.  The second norm is taken of the
  * stream before its rounding to `type`.  Enqueues one kernel.
@@ -501,10 +503,11 @@ int bsa_block_norm_backward_workspace_bytes(const bsa_block_norm_args* args, siz
  *     dgate = sum branch_scale D z over the rows that share a gate row, and the sums over
  *     rows that make the gradients of weights and biases.
  * x: the forward's stream (its x without y); y, stats: the forward's.  dx, and dy with y,
- * are written, `type`, and may be dstream or dnormed themselves.  dpost_weight, dpost_bias,
+ * are written, `type`, and may be dstream or dnormed themselves (not each other).  dpost_weight, dpost_bias,
  * dgate, dpre_weight, dpre_bias: `param_type`, each NULL or written in full (only of a
- * parameter that args has).  All sums are in fp32 in a fixed order.  workspace: 256-byte aligned, any contents.  Enqueues two
- * kernels.
+ * parameter that args has).  All sums are in fp32 in a fixed order.  workspace: 256-byte
+ * aligned, any contents, not shared by calls that may run at the same time; unused (NULL)
+ * where no sums are asked for.  Enqueues two kernels, one without the sums.
  */
 int bsa_block_norm_backward(const bsa_block_norm_args* args, const void* dstream, const void* dnormed,
                             const void* x, const void* y, const float* stats, void* dx, void* dy,
@@ -548,8 +551,8 @@ int bsa_fp8_matmul_workspace_bytes(int M, int N, int K, size_t* bytes);
  * input's gradient (a: dy in rows form, b: W's columns form) and its weight's (a: dy, b: x,
  * both in columns form).  Each block's products are summed by the tensor cores, the blocks
  * in fp32 with their scales, in a fixed order.  M or N of 0 is an empty call; K >= 1.
- * workspace: as sized above, 256-byte aligned, any contents (NULL when 0).  Enqueues one
- * kernel, two where K is split.  A device-side timeout is reported by bsa_sync_status.
+ * workspace: as sized above, 256-byte aligned, any contents (NULL when 0), not shared by calls
+ * that may run at the same time.  Enqueues one kernel, two where K is split.  A device-side timeout is reported by bsa_sync_status.
  */
 int bsa_fp8_matmul(const void* a, int a_type, int64_t lda, const float* a_scale, int a_rows, const void* b,
                    int b_type, int64_t ldb, const float* b_scale, int b_rows, const void* bias, int bias_type,

@@ -8,6 +8,8 @@ its gradients against those of the same steps in torch fp32 with the kernels' ro
 noise: a wrong path is off by the gradient's own size, the bound is a fraction of it.
 """
 
+import copy
+
 import numpy as np
 import pytest
 import torch
@@ -31,6 +33,16 @@ def test_refusals():
         LY.BigBirdSelfAttention(128, 2, fp8=True)(torch.zeros(1, 64, 128))
     with pytest.raises(ValueError):
         LY.BigBirdBlock(128, 2, pre=None)
+    one, other = LY.BigBirdBlock(128, 2), LY.BigBirdBlock(128, 2, eps=1e-5)
+    with pytest.raises(ValueError, match="eps"):
+        one(torch.zeros(1, 64, 128), following=other)
+
+
+def test_a_block_with_rotary_positions_is_copied():
+    m = LY.BigBirdBlock(128, 2, rope=(8, 12, 12))
+    again = copy.deepcopy(m)
+    assert again.attention.rope is not m.attention.rope and again.attention.rope.n_pairs == 32
+    assert all((s == t).all() for s, t in zip(m.state_dict().values(), again.state_dict().values()))
 
 
 def test_rotary_in_the_layer_over_fakes(monkeypatch):
@@ -176,3 +188,35 @@ def test_block_against_dense_fp32(kw, bound):
     want = torch.autograd.grad(ref, [xf] + leaves[1:], dout.float())
     for a, b in zip((out, *grads), (ref, *want)):
         assert (a.float() - b.float()).norm() <= bound * b.float().norm(), a.shape
+
+
+@gpu
+@needs_cuda
+def test_a_captured_step_replays_with_new_inputs():
+    m, _ = _blocks(fp8=True)
+    B, L = 2, 192
+    g = torch.Generator(device="cuda").manual_seed(4)
+    x = torch.randn(B, L, 256, generator=g, device="cuda").bfloat16().requires_grad_()
+    pos = torch.randint(0, 300, (3, B, L), generator=g, device="cuda")
+    dout = torch.randn(B, L, 256, generator=g, device="cuda").bfloat16()
+    leaves = [x] + list(m.parameters())
+
+    def step():
+        out = m(x, positions=pos)
+        return [t.detach() for t in (out, *torch.autograd.grad(out, leaves, dout))]
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        step()  # layouts are built and uploaded on first use
+    torch.cuda.current_stream().wait_stream(side)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        got = step()
+    for seed in (5, 6):
+        with torch.no_grad():
+            x.copy_(torch.randn(x.shape, generator=g.manual_seed(seed), device="cuda"))
+        pos.random_(0, 1000, generator=g)
+        graph.replay()
+        torch.cuda.synchronize()
+        assert all(torch.equal(a, b) for a, b in zip(got, step()))
+    assert bsa.bsa_sync_status() == 0

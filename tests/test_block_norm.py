@@ -41,13 +41,13 @@ def _args(**kw):
 
 def test_forward_refuses_before_device_work():
     f, p = bsa.lib.bsa_block_norm, 1 << 20
-    call = lambda x=p, y=p, out=p, normed=p, stats=None, **kw: f(  # noqa: E731
+    call = lambda x=p, y=p, out=p, normed=2 * p, stats=None, **kw: f(  # noqa: E731
         ctypes.byref(_args(**kw)), x, y, out, normed, stats, None)
     assert f(None, p, p, p, p, None, None) == bsa.BSA_ERR_INVALID_ARG
     for kw in (dict(B=-1), dict(rows_per_batch=-1), dict(C=0), dict(post=3), dict(pre=-1), dict(gate_rows=3),
                dict(eps=-1.0), dict(eps=float("nan")), dict(branch_scale=float("nan")), dict(post=0), dict(pre=0),
                dict(x=None), dict(out=None), dict(normed=None), dict(y=None), dict(x=p + 1), dict(stats=p + 4),
-               dict(gate=p + 2), dict(y=None, post=0, post_weight=None, gate=None, pre=0, pre_weight=None)):
+               dict(gate=p + 2), dict(normed=p), dict(y=None, post=0, post_weight=None, gate=None, pre=0, pre_weight=None)):
         assert call(**kw) == bsa.BSA_ERR_INVALID_ARG, kw
     for kw in (dict(C=8193), dict(type=bsa.E4M3), dict(type=bsa.BF16, param_type=bsa.FP16)):
         assert call(**kw) == bsa.BSA_ERR_UNSUPPORTED, kw
@@ -59,11 +59,11 @@ def test_backward_refuses_before_device_work():
     order = ("dstream", "dnormed", "x", "y", "stats", "dx", "dy", "dpw", "dpb", "dg", "dw", "db", "ws")
 
     def call(**kw):
-        a = {n: p for n in order} | {"dpb": None, "db": None}
+        a = {n: p for n in order} | {"dy": 2 * p, "dpb": None, "db": None}
         a.update({k: v for k, v in kw.items() if k in order})
         return f(ctypes.byref(_args(**{k: v for k, v in kw.items() if k not in order})), *[a[n] for n in order], 1 << 30, None)
     for kw in (dict(x=None), dict(dx=None), dict(stats=None), dict(dy=None), dict(y=None), dict(dpb=p), dict(db=p),
-               dict(gate=None), dict(pre=0, pre_weight=None), dict(x=p + 1), dict(dg=p + 1)):
+               dict(gate=None), dict(pre=0, pre_weight=None), dict(x=p + 1), dict(dg=p + 1), dict(dy=p)):
         assert call(**kw) == bsa.BSA_ERR_INVALID_ARG, kw
 
 

@@ -311,6 +311,6 @@ def test_linear_parts_and_no_rows():
     assert torch.equal(both[0], dx) and torch.equal(both[1], dw)
     with torch.no_grad():
         assert torch.equal(fp8_linear(xg, w), fp8_linear(xg.detach(), w.detach()))
-    for bad in (x.half(), x[:, :60]):
+    for bad in ((x.half(), w), (x[:, :60], w), (x, w[:0]), (x[:, :0], w[:, :0])):
         with pytest.raises(ValueError):
-            fp8_linear(bad, w)
+            fp8_linear(*bad)

@@ -13,7 +13,9 @@ last place (2^-23).  So each of sin and cos errs by less than 2^-21.5, and an el
 the result's type adds half a step, relative 2^-8 (bf16), 2^-11 (fp16) or 2^-24 (fp32).
 """
 
+import copy
 import ctypes
+import pickle
 
 import numpy as np
 import pytest
@@ -58,19 +60,27 @@ def test_from_table_refuses(axis, freq):
 
 def test_apply_refuses_before_device_work():
     rope = bsa.bsa_rope_build([4, 4])
-    a = 1 << 20
+    a, b = 1 << 20, 1 << 21
     strides, ps = (ctypes.c_int64 * 12)(*[16] * 12), (ctypes.c_int64 * 3)(1, 1, 1)
 
-    def call(q=a, qo=a, H=2, k=a, ko=a, Hk=1, B=1, L=4, d=16, ty=bsa.BF16, st=strides, pos=a, pt=bsa.INT64, pst=ps,
+    def call(q=a, qo=a, H=2, k=b, ko=b, Hk=1, B=1, L=4, d=16, ty=bsa.BF16, st=strides, pos=a, pt=bsa.INT64, pst=ps,
              r=rope.handle):
         return bsa.lib.bsa_rope_apply(q, qo, H, k, ko, Hk, B, L, d, ty, st, pos, pt, pst, r, 0, None)
     for kw in (dict(q=None), dict(qo=None), dict(ko=None), dict(pos=None), dict(r=None), dict(st=None), dict(pst=None),
-               dict(B=-1), dict(L=-1), dict(H=-1), dict(Hk=-1), dict(d=0), dict(d=15), dict(q=a + 1), dict(ko=a + 1)):
+               dict(B=-1), dict(L=-1), dict(H=-1), dict(Hk=-1), dict(d=0), dict(d=15), dict(q=a + 1), dict(ko=b + 1), dict(qo=b), dict(ko=a), dict(k=3 << 20, qo=b)):
         assert call(**kw) == bsa.BSA_ERR_INVALID_ARG, kw
     for kw in (dict(ty=bsa.E4M3), dict(ty=9), dict(pt=bsa.BF16), dict(d=258)):
         assert call(**kw) == bsa.BSA_ERR_UNSUPPORTED, kw
     for kw in (dict(B=0), dict(L=0), dict(H=0, k=None)):
         assert call(**kw) == bsa.BSA_OK, kw  # empty calls
+
+
+def test_a_code_is_copied_and_stored_by_its_tables():
+    for rope in (bsa.bsa_rope_build([8, 12, 12], 1e6, per_axis=True), bsa.bsa_rope_from_table([2, 0], [0.5, -3.0], True)):
+        for again in (copy.deepcopy(rope), pickle.loads(pickle.dumps(rope))):
+            assert (again.n_pairs, again.n_axes, again.adjacent) == (rope.n_pairs, rope.n_axes, rope.adjacent)
+            assert again.handle.value != rope.handle.value
+            assert all((s == t).all() for s, t in zip(bsa.bsa_rope_table(again), bsa.bsa_rope_table(rope)))
 
 
 def test_binding_refuses_cpu_tensors():
