@@ -98,6 +98,7 @@ struct MmaParams {
   int M, N, kb;         // kb: blocks of K
   int a_shift, b_rows;  // row of sa = m >> a_shift; b_rows: a scale for each row of b
   int bias_f32, out_f32;
+  int wide;             // a batch's scales of a row lie in 16 aligned bytes
   int idesc_formats;    // A and B format bits of the instruction descriptor
   int n_tiles, splits, kb_split, units;
   int64_t split_stride;  // elements of one split's partial result (splits > 1: out is fp32 partials)
@@ -247,6 +248,19 @@ __device__ void mma_issuer(const MmaParams& p, uint32_t smem, uint32_t bars, uin
   wait_force(bar_at(bars, C::kFinal), 0u, abort_flag, p.timeout_ns);
 }
 
+// The scales of a row's n <= kBatch blocks from `from` on, 0 after them.  A load of a column of
+// rows touches a line for each lane, whatever it takes of it.
+static_assert(kBatch == 4, "a float4 of scales");
+__device__ __forceinline__ void batch_of(const float* from, int n, bool wide, float (&v)[kBatch]) {
+  if (wide) {
+    const float4 q = __ldg(reinterpret_cast<const float4*>(from));
+    v[0] = q.x, v[1] = q.y, v[2] = q.z, v[3] = q.w;
+  } else {
+#pragma unroll
+    for (int e = 0; e < kBatch; ++e) v[e] = e < n ? __ldg(from + e) : 0.f;
+  }
+}
+
 // Brings the scales of kBatch blocks at a time: with a scale for 128 rows of b the products
 // with the 128 scales of a for both halves of the columns, else a's and then b's own.
 template <int kBN, bool kBRows>
@@ -259,19 +273,17 @@ __device__ void scale_loader(const MmaParams& p, uint8_t* smem_gen, uint32_t bar
     for (int k = t.k0; k < t.k1; k += kBatch, ++bt) {
       const int n = min(kBatch, t.k1 - k);
       float* dst = reinterpret_cast<float*>(smem_gen + C::kScale) + (bt & 1u) * (kBatch * C::kScales);
-      float a[kBatch][kMB / 32], b[kBatch][kBRows ? 1 : kNB];
+      float a[kMB / 32][kBatch], b[kBRows ? 1 : kNB][kBatch];
 #pragma unroll
       for (int i = 0; i < kMB / 32; ++i) {
         const float* from = p.sa + static_cast<int64_t>(min(t.m0 + 32 * i + lane, p.M - 1) >> p.a_shift) * p.kb + k;
-#pragma unroll
-        for (int e = 0; e < kBatch; ++e) a[e][i] = e < n ? __ldg(from + e) : 0.f;
+        batch_of(from, n, p.wide, a[i]);
       }
       if constexpr (!kBRows) {
 #pragma unroll
         for (int h = 0; h < 2; ++h) {
           const float* from = p.sb + static_cast<int64_t>(min(t.n0 + h * kHalf, p.N - 1) >> 7) * p.kb + k;
-#pragma unroll
-          for (int e = 0; e < kBatch; ++e) b[e][h] = e < n ? __ldg(from + e) : 0.f;
+          batch_of(from, n, p.wide, b[h]);
         }
       }
       // b's own scales come 128 rows at a time, the first of them before the wait for the slot
@@ -280,8 +292,7 @@ __device__ void scale_loader(const MmaParams& p, uint8_t* smem_gen, uint32_t bar
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
           const float* from = p.sb + static_cast<int64_t>(min(t.n0 + 32 * (i0 + i) + lane, p.N - 1)) * p.kb + k;
-#pragma unroll
-          for (int e = 0; e < kBatch; ++e) v[i][e] = e < n ? __ldg(from + e) : 0.f;
+          batch_of(from, n, p.wide, v[i]);
         }
       };
       if constexpr (kBRows) load_b(0);
@@ -317,10 +328,10 @@ __device__ void scale_loader(const MmaParams& p, uint8_t* smem_gen, uint32_t bar
         for (int i = 0; i < kMB / 32; ++i) {
           float* to = dst + e * C::kScales + 32 * i + lane;
           if constexpr (kBRows) {
-            to[0] = a[e][i];
+            to[0] = a[i][e];
           } else {
-            to[0] = a[e][i] * b[e][0];
-            to[kMB] = a[e][i] * b[e][1];
+            to[0] = a[i][e] * b[0][e];
+            to[kMB] = a[i][e] * b[1][e];
           }
         }
       __syncwarp();
@@ -999,7 +1010,9 @@ MmaPlan mma_plan(int64_t M, int64_t N, int64_t kb, int sms) {
     const int64_t tiles = ((M + kMB - 1) / kMB) * ((N + bn - 1) / bn);
     for (int64_t want = 1; want <= 32 && want <= kb; ++want) {
       if (want > 1 && tiles * want > 4 * sms) break;  // more units than that only cost partials
-      const int64_t per = (kb + want - 1) / want, splits = (kb + per - 1) / per;
+      int64_t per = (kb + want - 1) / want;
+      if (want > 1) per = (per + kBatch - 1) / kBatch * kBatch;  // whole batches of scales
+      const int64_t splits = (kb + per - 1) / per;
       if (splits != want) continue;
       const int64_t waves = (tiles * splits + sms - 1) / sms;
       double cost = static_cast<double>(waves) * (static_cast<double>(per) * (bn == 256 ? 560 : 330) + 2500.0);
@@ -1109,6 +1122,7 @@ int bsa_fp8_matmul(const void* a, int a_type, int64_t lda, const float* a_scale,
   const int64_t units = static_cast<int64_t>((M + kMB - 1) / kMB) * p.n_tiles * p.splits;
   if (units > (1 << 30)) return BSA_ERR_INVALID_ARG;
   p.units = static_cast<int>(units);
+  p.wide = kb % kBatch == 0 && aligned16(a_scale) && aligned16(b_scale);
   p.timeout_ns = kDefaultTimeoutNs;
   const bool split = plan.splits > 1;
   const int64_t n = static_cast<int64_t>(M) * N;
