@@ -286,16 +286,12 @@ __device__ void scale_loader(const MmaParams& p, uint8_t* smem_gen, uint32_t bar
           batch_of(from, n, p.wide, b[h]);
         }
       }
-      // b's own scales come 128 rows at a time, the first of them before the wait for the slot
-      float v[kBRows ? 4 : 1][kBatch];
-      auto load_b = [&](int i0) {
+      float v[kBRows ? kNB : 1][kBatch];  // b's own scales
+      if constexpr (kBRows) {
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          const float* from = p.sb + static_cast<int64_t>(min(t.n0 + 32 * (i0 + i) + lane, p.N - 1)) * p.kb + k;
-          batch_of(from, n, p.wide, v[i]);
-        }
-      };
-      if constexpr (kBRows) load_b(0);
+        for (int i = 0; i < kNB; ++i)
+          batch_of(p.sb + static_cast<int64_t>(min(t.n0 + 32 * i + lane, p.N - 1)) * p.kb + k, n, p.wide, v[i]);
+      }
       float bias[kBRows ? 1 : kBN / 32];
       const bool first = !kBRows && k == t.k0 && p.bias != nullptr;
       if (first)
@@ -314,13 +310,9 @@ __device__ void scale_loader(const MmaParams& p, uint8_t* smem_gen, uint32_t bar
           reinterpret_cast<float*>(smem_gen + C::kBias)[(un & 3u) * kBN + 32 * i + lane] = bias[i];
       if constexpr (kBRows) {
 #pragma unroll
-        for (int i0 = 0; i0 < kNB; i0 += 4) {
-          if (i0 > 0) load_b(i0);
+        for (int i = 0; i < kNB; ++i)
 #pragma unroll
-          for (int i = 0; i < 4; ++i)
-#pragma unroll
-            for (int e = 0; e < kBatch; ++e) dst[e * C::kScales + kMB + 32 * (i0 + i) + lane] = v[i][e];
-        }
+          for (int e = 0; e < kBatch; ++e) dst[e * C::kScales + kMB + 32 * i + lane] = v[i][e];
       }
 #pragma unroll
       for (int e = 0; e < kBatch; ++e)
