@@ -71,7 +71,9 @@ struct MmaCfg {
   static constexpr uint32_t kABytes = kMB * kKB, kBBytes = kBN * kKB, kStageBytes = kABytes + kBBytes;
   static constexpr uint32_t kStg = kStages * kStageBytes;
   // a block's scales: of 128 rows of a and kBN rows of b, or their products for two halves
-  static constexpr int kScales = kBRows ? kMB + kBN : 2 * kMB;
+  // (kBRows: 128 of a, then of each half of b's rows n the four n % 4, a bank's width apart)
+  static constexpr int kColGap = kBN / 8 + 4;
+  static constexpr int kScales = kBRows ? kMB + 8 * kColGap : 2 * kMB;
   static constexpr uint32_t kScale = kStg + kPromoteWarps * kStgBytes;  // [2][kBatch][kScales] fp32
   // The bias of a unit's columns, brought with its first batch.  Batches run at most two ahead,
   // so at most two units ahead of the one whose bias is read.
@@ -146,11 +148,11 @@ __device__ __forceinline__ bool elected() {
   return p != 0;
 }
 
-// 16 lanes of 32 TMEM columns (16x256b, four times): of columns 8 i + 2 (lane % 4), + 1 the
-// words 4 i, + 1 in row lane / 4 and 4 i + 2, + 3 in row lane / 4 + 8.
+// 16 lanes of 32 TMEM columns (16x128b, eight times): of column 4 i + lane % 4 the words 2 i in
+// row lane / 4 and 2 i + 1 in row lane / 4 + 8.
 __device__ __forceinline__ void tmem_ld_frag(uint32_t taddr, uint32_t (&r)[16]) {
   asm volatile(
-      "tcgen05.ld.sync.aligned.16x256b.x4.b32 {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15}, [%16];"
+      "tcgen05.ld.sync.aligned.16x128b.x8.b32 {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15}, [%16];"
       : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]),
         "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
       : "r"(taddr));
@@ -312,7 +314,10 @@ __device__ void scale_loader(const MmaParams& p, uint8_t* smem_gen, uint32_t bar
 #pragma unroll
         for (int i = 0; i < kNB; ++i)
 #pragma unroll
-          for (int e = 0; e < kBatch; ++e) dst[e * C::kScales + kMB + 32 * i + lane] = v[i][e];
+          for (int e = 0; e < kBatch; ++e) {
+            const int c = 32 * i + lane, half = c / kHalf, in = c % kHalf;
+            dst[e * C::kScales + kMB + (4 * half + in % 4) * C::kColGap + in / 4] = v[i][e];
+          }
       }
 #pragma unroll
       for (int e = 0; e < kBatch; ++e)
@@ -477,7 +482,23 @@ __device__ void promoter(const MmaParams& p, uint32_t smem, uint8_t* smem_gen, u
   give_up();
 }
 
-// The same with a scale for each row of b: of every eight columns a thread has two, of rows
+// Four lanes (lane % 4) hold one row's columns 4 m + lane % 4 in v[m]; after it lane % 4 = m holds
+// the columns 4 m .. 4 m + 3.
+__device__ __forceinline__ void turn4(float (&v)[4], int lane) {
+  const bool odd = lane & 1, upper = lane & 2;
+#pragma unroll
+  for (int p = 0; p < 4; p += 2) {
+    const float got = __shfl_xor_sync(0xffffffffu, odd ? v[p] : v[p + 1], 1);
+    (odd ? v[p] : v[p + 1]) = got;
+  }
+#pragma unroll
+  for (int p = 0; p < 2; ++p) {
+    const float got = __shfl_xor_sync(0xffffffffu, upper ? v[p] : v[p + 2], 2);
+    (upper ? v[p] : v[p + 2]) = got;
+  }
+}
+
+// The same with a scale for each row of b: of every four columns a thread has one, of rows
 // lane / 4, + 8, + 16 and + 24 of its warp's 32.
 template <int kBN>
 __device__ void promoter_rows(const MmaParams& p, uint8_t* smem_gen, uint32_t bars, uint32_t tmem, int warp, int lane,
@@ -492,22 +513,22 @@ __device__ void promoter_rows(const MmaParams& p, uint8_t* smem_gen, uint32_t ba
   for (int u = blockIdx.x; u < p.units; u += gridDim.x) {
     const Unit t = unit_of<kBN>(p, u);
     const int n = t.k1 - t.k0;
-    // [32-column group][8-column group][upper or lower 16 rows][row, row + 8]
-    uint64_t acc[kGroups][4][2][2];
+    // [32-column group][4-column group][upper or lower 16 rows], each of rows row, row + 8
+    uint64_t acc[kGroups][8][2];
 #pragma unroll
-    for (int i = 0; i < kGroups * 16; ++i) (&acc[0][0][0][0])[i] = 0ull;
+    for (int i = 0; i < kGroups * 16; ++i) (&acc[0][0][0])[i] = 0ull;
     for (int k = 0; k < n; ++k, ++it) {
       const uint32_t as = it % C::kAcc;
       if (k % kBatch == 0 && !ready(bar_at(bars, C::kScFull + (bt & 1u)), (bt >> 1) & 1u, abort_flag, p.timeout_ns))
         return;
       const float* sc = scales + ((bt & 1u) * kBatch + k % kBatch) * C::kScales;
-      uint64_t sa2[4];
+      uint64_t sa2[2];
 #pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        const float s = sc[quad * 32 + 8 * i + (lane >> 2)];
-        sa2[i] = ptx::pack2(s, s);
+      for (int h = 0; h < 2; ++h) {
+        const float* at = sc + quad * 32 + 16 * h + (lane >> 2);
+        sa2[h] = ptx::pack2(at[0], at[8]);
       }
-      const float2* sb = reinterpret_cast<const float2*>(sc + kMB + half * kCols) + (lane & 3);
+      const float4* sb = reinterpret_cast<const float4*>(sc + kMB + (4 * half + (lane & 3)) * C::kColGap);
       if (!ready(bar_at(bars, C::kAccFull + as), (it / C::kAcc) & 1u, abort_flag, p.timeout_ns)) return;
       ptx::tc_fence_after();
 #pragma unroll
@@ -515,9 +536,8 @@ __device__ void promoter_rows(const MmaParams& p, uint8_t* smem_gen, uint32_t ba
         uint32_t r[2][16];
         tmem_ld_frag(taddr + as * kBN + 32u * g, r[0]);
         tmem_ld_frag(taddr + as * kBN + 32u * g + (16u << 16), r[1]);
-        float2 b[4];
-#pragma unroll
-        for (int c = 0; c < 4; ++c) b[c] = sb[(32 * g + 8 * c) / 2];
+        const float4 b0 = sb[2 * g], b1 = sb[2 * g + 1];
+        const float b[8] = {b0.x, b0.y, b0.z, b0.w, b1.x, b1.y, b1.z, b1.w};
         ptx::tmem_wait_ld();
         reg_fence16(r[0]);
         reg_fence16(r[1]);
@@ -527,15 +547,13 @@ __device__ void promoter_rows(const MmaParams& p, uint8_t* smem_gen, uint32_t ba
           if (lane == 0) ptx::mbar_arrive(bar_at(bars, C::kAccEmpty + as));
         }
 #pragma unroll
-        for (int c = 0; c < 4; ++c) {
-          const uint64_t b2 = ptx::pack2(b[c].x, b[c].y);
+        for (int i = 0; i < 8; ++i) {
+          const uint64_t b2 = ptx::pack2(b[i], b[i]);
 #pragma unroll
-          for (int h = 0; h < 2; ++h)
-#pragma unroll
-            for (int e = 0; e < 2; ++e) {
-              const uint64_t x = ptx::pack2(__uint_as_float(r[h][4 * c + 2 * e]), __uint_as_float(r[h][4 * c + 2 * e + 1]));
-              acc[g][c][h][e] = ptx::ffma2(ptx::fmul2(x, b2), sa2[2 * h + e], acc[g][c][h][e]);
-            }
+          for (int h = 0; h < 2; ++h) {
+            const uint64_t x = ptx::pack2(__uint_as_float(r[h][2 * i]), __uint_as_float(r[h][2 * i + 1]));
+            acc[g][i][h] = ptx::ffma2(ptx::fmul2(x, sa2[h]), b2, acc[g][i][h]);
+          }
         }
       }
       if (k % kBatch == kBatch - 1 || k + 1 == n) {
@@ -544,51 +562,51 @@ __device__ void promoter_rows(const MmaParams& p, uint8_t* smem_gen, uint32_t ba
         ++bt;
       }
     }
-    // four lanes write eight neighbouring columns of a row
+    // four lanes turn their columns so that each has four neighbours: together 16 of a row
     const int esize = p.out_f32 ? 4 : 2;
     uint8_t* out = static_cast<uint8_t*>(p.out) + t.split * p.split_stride * esize;
-    const bool pairs = (p.N & 1) == 0 && (reinterpret_cast<uintptr_t>(p.out) & 7u) == 0;
+    const bool fours = (p.N & 3) == 0 && (reinterpret_cast<uintptr_t>(p.out) & 15u) == 0;
 #pragma unroll
     for (int g = 0; g < kGroups; ++g)
 #pragma unroll
-      for (int c = 0; c < 4; ++c) {
-        const int col = t.n0 + half * kCols + 32 * g + 8 * c + 2 * (lane & 3);
-        float b0 = 0.f, b1 = 0.f;
-        if (p.bias != nullptr) {
-          if (col < p.N)
-            b0 = p.bias_f32 ? __ldg(static_cast<const float*>(p.bias) + col)
-                            : __bfloat162float(static_cast<const __nv_bfloat16*>(p.bias)[col]);
-          if (col + 1 < p.N)
-            b1 = p.bias_f32 ? __ldg(static_cast<const float*>(p.bias) + col + 1)
-                            : __bfloat162float(static_cast<const __nv_bfloat16*>(p.bias)[col + 1]);
-        }
+      for (int q = 0; q < 2; ++q) {
+        const int col = t.n0 + half * kCols + 32 * g + 16 * q + 4 * (lane & 3);
+        float bias[4] = {};
+        if (p.bias != nullptr)
 #pragma unroll
-        for (int h = 0; h < 2; ++h)
+          for (int i = 0; i < 4; ++i)
+            if (col + i < p.N)
+              bias[i] = p.bias_f32 ? __ldg(static_cast<const float*>(p.bias) + col + i)
+                                   : __bfloat162float(static_cast<const __nv_bfloat16*>(p.bias)[col + i]);
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+          float v[2][4];
+#pragma unroll
+          for (int i = 0; i < 4; ++i) ptx::unpack2(acc[g][4 * q + i][h], v[0][i], v[1][i]);
 #pragma unroll
           for (int e = 0; e < 2; ++e) {
+            turn4(v[e], lane);
             const int row = t.m0 + quad * 32 + 16 * h + 8 * e + (lane >> 2);
             if (row >= p.M || col >= p.N) continue;
-            float v0, v1;
-            ptx::unpack2(acc[g][c][h][e], v0, v1);
-            v0 += b0;
-            v1 += b1;
+#pragma unroll
+            for (int i = 0; i < 4; ++i) v[e][i] += bias[i];
             const int64_t at = static_cast<int64_t>(row) * p.N + col;
             if (p.out_f32) {
               float* to = reinterpret_cast<float*>(out) + at;
-              if (pairs) *reinterpret_cast<float2*>(to) = make_float2(v0, v1);
-              else {
-                to[0] = v0;
-                if (col + 1 < p.N) to[1] = v1;
-              }
+              if (fours) *reinterpret_cast<float4*>(to) = make_float4(v[e][0], v[e][1], v[e][2], v[e][3]);
+              else
+                for (int i = 0; i < 4; ++i)
+                  if (col + i < p.N) to[i] = v[e][i];
             } else {
               __nv_bfloat16* to = reinterpret_cast<__nv_bfloat16*>(out) + at;
-              if (pairs) *reinterpret_cast<uint32_t*>(to) = pack_bf16x2(v0, v1);
-              else {
-                to[0] = __float2bfloat16_rn(v0);
-                if (col + 1 < p.N) to[1] = __float2bfloat16_rn(v1);
-              }
+              if (fours)
+                *reinterpret_cast<uint2*>(to) = make_uint2(pack_bf16x2(v[e][0], v[e][1]), pack_bf16x2(v[e][2], v[e][3]));
+              else
+                for (int i = 0; i < 4; ++i)
+                  if (col + i < p.N) to[i] = __float2bfloat16_rn(v[e][i]);
             }
           }
+        }
       }
   }
 }
