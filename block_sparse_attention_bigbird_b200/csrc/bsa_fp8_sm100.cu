@@ -17,22 +17,36 @@
 //   warps 4-11 keep the tile's sums in registers, read each accumulator with tcgen05.ld as its
 //              MMAs complete, hand it back and add it with its scales; at a tile's end they
 //              add the bias and write.  With a scale for 128 rows of b a thread owns a row of
-//              half the columns and its scale is one number a block; with a scale for each
-//              row of b (kBRows) the accumulator is read in the 16x256b form, in which a
-//              thread holds two neighbouring columns of every eight and four rows: 32 column
-//              scales to read a block instead of 128.
-// At kBN = 256 a block's MMAs take 512 cycles of the tensor pipe.  Everything else has to stay
-// below that.  An issuer whose loop is uniform over the warp and elects a lane for the MMAs
-// alone takes half the time of a single thread's loop, whose descriptors have to be moved to
-// uniform registers after every wait; two of them hide the waits.  No register may spill: with
-// the shared memory taken, L1 is too small to hold them.
+//              half the columns and its scale is one number a block (the 32x32b form).  With a
+//              scale for each row of b (kBRows) that form would need 128 column scales a thread
+//              and block; in the 16x128b form a thread has one column of every four and four
+//              rows, so 32 column scales and four row scales.
+// Cycles a block of a 128 x 256 tile, measured: its MMAs 512; the eight warps' reads of TMEM 160
+// (16x128b 277, 16x256b 521), their additions 340 (kBRows 540: two operations a pair), waits and
+// hand-overs about 350.  Reads and additions hardly overlap, as the two warps of a scheduler wait
+// for the same accumulator, so the adding warps are what bounds long products: about 1000 cycles,
+// kBRows 1300.  65536 x 2304 x 768 takes 141 us (1.65 PFLOP/s; without its loads 128, without
+// writing 124), 8192^3 524 us (2.10 PFLOP/s, at the power limit), 2304 x 768 x 65536 with
+// kBRows 159 us (1.46 PFLOP/s).
+// What follows from it.  An issuer whose loop is uniform over the warp and elects a lane for the
+// MMAs alone takes half the time of a single thread's loop, whose descriptors have to be moved to
+// uniform registers after every wait (513 cycles a block, 711 to 851); two of them hide the waits.
+// No register may spill: with the shared memory taken, L1 is too small to hold them.  Both halves
+// of the columns run the same code (a copy for each took 147 us instead of 141).  Halves with
+// MMAs of N = 128 and accumulators of their own took 155 us: at that width shared memory cannot
+// feed the tensor cores.
 //
 // bsa_fp8_rows_kernel, for up to 8 rows (tokens).  There the time is that of reading b once.
 // A block of threads takes 16 rows of b at a time, its warps an equal share of K's blocks each;
 // every warp brings its part of b with cp.async, kRowsAhead blocks of K ahead and over the end
-// of one 16-row tile into the next, so that the loads in flight do not depend on registers.  Codes are widened to fp16, which holds every e4m3 and e5m2 value, and multiplied
-// by mma.sync m16n8k16 with b as the 16-row side and the tokens as the 8 columns.  The products of a block of 128 are summed in fp32 before their
-// scale; the warps' sums meet in shared memory in a fixed order.
+// of one 16-row tile into the next, so that the loads in flight do not depend on registers.
+// Codes are widened to fp16, which holds every e4m3 and e5m2 value, and multiplied by mma.sync
+// m16n8k16 with b as the 16-row side and the tokens as the 8 columns (a tcgen05 tile of 128 rows
+// would be 15/16 empty).  The products of a block of 128 are summed in fp32 before their scale;
+// the warps' sums meet in shared memory in a fixed order.
+// 4 x 8192 x 8192 (67 MB of b) takes 16.9 us in a graph, a loop that only reads b 11 us.  Where
+// the kernels meet, 8 and 9 rows of N = K = 8192 take 17.2 and 19.4 us, of 2304 x 768 2.6 and 4.9:
+// eight tokens are what one mma.sync has columns for.
 //
 // Every wait is bounded; on expiry the CTA records BSA_ERR_DEVICE_TIMEOUT, drains its copies
 // and MMAs, frees TMEM and returns.
@@ -1008,7 +1022,11 @@ int fp8_device_sms() {
 
 // Tile width and split of K for a product on `sms` SMs: the pair with the least estimate of
 //     waves of units x (blocks of K a unit x block time + a unit's start and end) + bytes of
-// the splits' partial results, in cycles.
+// the splits' partial results.  The constants are of one scale, fitted to a sweep of widths and
+// splits.  In a graph, chosen and next best: 2304 x 768 x 65536 256 columns by 5 splits 158 us,
+// 256 by 8 164, 128 by 4 168; 65536 x 2304 x 768 256 139 us, 128 155; 777 x 2050 x 1104 128
+// 8.4 us, 256 12.7; 300 x 1000 x 20000 128 by 6 16.3 us, 256 by 10 19.1; 512 x 512 x 8192
+// 128 by 4 11.0 us, though 128 by 10 takes 9.9.
 struct MmaPlan {
   int bn, splits, kb_split;
   size_t bytes;

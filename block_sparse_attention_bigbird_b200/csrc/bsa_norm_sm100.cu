@@ -30,7 +30,16 @@
 // (block + gate row), which no two (block, gate row) pairs share.  A second kernel adds the
 // slots in a fixed order.
 //
-// What bounds both: the bytes of the activations; parameters stay in L1 and L2.
+// What bounds both: the bytes of the activations; parameters stay in L1 and L2.  Measured with
+// 65536 bf16 rows of 768, rms norms on both sides and fp32 parameters: forward (403 MB) 66 us
+// alone, 73 in a row (5.5 TB/s, where a copy has 6.55); backward (604 MB) 101 us and 9 for
+// the sum of the slots, 120 in a row (5.0 TB/s).  What is left is the row's chain: pieces
+// landed, sum over the warp, division and root, second sum; four warps a scheduler (three in
+// the backward, whose sums take the registers) hide most of it, issue slots are 51 % and 46 %
+// busy.  4113 fp32 rows of 1030, backward: 33 us and 8 for the sum, 39 in a row; its rows have
+// no 16-byte starts, so that a thread's pieces are of two elements and a row takes a block's
+// worth of barriers.  Without the ring (loads straight to registers) the three took 102, 285
+// and 136 us.
 #include <cuda_runtime.h>
 
 #include <algorithm>

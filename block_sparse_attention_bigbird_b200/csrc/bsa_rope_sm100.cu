@@ -15,6 +15,12 @@
 // pairs' two halves as two 16-byte vectors.  The heads are cut into groups (blockIdx.y) of
 // at least twelve while the card is filled more than once, so that the last wave is short;
 // with one token a call a thread takes one head.
+//
+// Measured: B = 4, L = 16384, 12 + 12 heads of 64 in bf16 (403 MB read and written) 66 us
+// alone, 70 in a row (5.8 TB/s, where a copy has 6.55); 80 registers, six blocks an SM.  Six
+// blocks of batches of 4 heads took 70.0 us; 5 of 4, 7 of 4 and 8 of 3 (which hold fewer loads
+// or spill) 72.3, 74.2 and 73.4.  8 tokens of 16 + 4 heads of 128: 16 us with the call from
+// Python, whose host side is all but a few of them.
 #include <cuda_runtime.h>
 
 #include <algorithm>
