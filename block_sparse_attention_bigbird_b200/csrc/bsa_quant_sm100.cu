@@ -20,8 +20,7 @@
 // elements nearly as much the integer and conversion work (about 7 instructions an element and
 // form; issue slots 59 % busy, DRAM 50 %).  Measured: both forms of 65536 x 768 bf16 (201 MB)
 // 39 us alone, 42 in a row (4.8 TB/s, where a copy has 6.55); both square forms of 4096 x 4096
-// fp32 (101 MB) 20 and 22 us.  Three blocks an SM (two for fp32) are what the kept patch leaves
-// room for.  Persistent blocks that fetch the next tile with cp.async took 43 and 29 us: the
+// fp32 (101 MB) 19 and 21 us.  Persistent blocks that fetch the next tile with cp.async took 43 and 29 us: the
 // second copy through shared memory costs what the overlap gives.  Comparing and dividing
 // element by element in fp32 took 113 us.
 #include <cuda_runtime.h>
@@ -116,9 +115,16 @@ __device__ __forceinline__ uint2 codes8(const float (&v)[8]) {
                     codes2<kE5>(v[4], v[5]) | codes2<kE5>(v[6], v[7]) << 16);
 }
 
+// Blocks an SM, as many as have registers without many spills (us with one block fewer, this many, one
+// more): 16-bit elements, one form of 65536 x 768 (29.1, 27.1, -), both (-, 41.4, 43.6); fp32, columns
+// of 8192 x 2304 (20.8, 19.3, -), both forms of it (-, 25.1, 37.3).
+template <typename T, bool kSquare, int kForm>
+constexpr int kQuantBlocks = sizeof(T) == 2 ? (kForm == 2 ? 3 : 4) : kForm == 2 && !kSquare ? 2 : 3;
+
 // kForm: 0 rows, 1 columns, 2 both
 template <typename T, bool kE5, bool kSquare, int kForm>
-__global__ void __launch_bounds__(256, sizeof(T) == 2 ? 3 : 2) bsa_fp8_quantize_kernel(const __grid_constant__ QuantParams p) {
+__global__ void __launch_bounds__(256, (kQuantBlocks<T, kSquare, kForm>))
+bsa_fp8_quantize_kernel(const __grid_constant__ QuantParams p) {
   constexpr float kTop = kE5 ? 57344.f : 448.f;
   constexpr bool kRows = kForm != 1, kCols = kForm != 0;
   // maxima of the warps' columns (or of the warps), and the columns' top / m
