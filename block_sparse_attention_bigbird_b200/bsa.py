@@ -742,8 +742,8 @@ def bsa_block_norm(x, y=None, post: Optional[str] = None, post_weight=None, post
     def call(ptr):
         o = torch.empty_like(x) if y is not None and out is None else out
         n = torch.empty_like(x) if pre is not None and normed is None else normed
-        st = torch.empty((rows, 4), dtype=torch.float32, device=x.device) if save_stats else None
-        code = lib.bsa_block_norm(ctypes.byref(a), x.data_ptr(), None if y is None else y.data_ptr(),
+        st = x.new_empty((rows, 4), dtype=torch.float32) if save_stats else None
+        code = lib.bsa_block_norm(a, x.data_ptr(), None if y is None else y.data_ptr(),
                                   None if o is None else o.data_ptr(), None if n is None else n.data_ptr(), _ptr(st),
                                   ptr)
         if code:
@@ -766,32 +766,38 @@ def bsa_block_norm_backward(dstream, dnormed, x, y, stats, post: Optional[str] =
     import torch
     a, rows, dev = _norm_args(x, y, post, post_weight, post_bias, gate, branch_scale, stream_scale, pre, pre_weight,
                               pre_bias, 0.0)
+    shape, dtype = x.shape, x.dtype
     for name, t in (("dstream", dstream), ("dnormed", dnormed)):
-        if t is not None and (t.shape != x.shape or t.dtype != x.dtype or not t.is_contiguous() or
-                              t.device != x.device):
+        if t is not None and (t.shape != shape or t.dtype is not dtype or t.get_device() != dev or
+                              not t.is_contiguous()):
             raise ValueError(f"{name} must be like x")
     if dnormed is not None and pre is None:
         raise ValueError("dnormed without a pre norm")
-    if stats.dtype != torch.float32 or tuple(stats.shape) != (rows, 4) or not stats.is_contiguous() or \
-            stats.device != x.device:
+    if stats.dtype is not torch.float32 or stats.shape != (rows, 4) or stats.get_device() != dev or \
+            not stats.is_contiguous():
         raise ValueError("stats must be the forward's fp32 [rows, 4]")
 
     def call(ptr):
         g = {"x": torch.empty_like(x), "y": None if y is None else torch.empty_like(y)}
+        at = []  # addresses of the parameters' gradients
         for name, t in (("post_weight", post_weight), ("post_bias", post_bias), ("gate", gate),
                         ("pre_weight", pre_weight), ("pre_bias", pre_bias)):
-            g[name] = torch.empty_like(t) if params and t is not None else None
-        ws = None
-        if params:
-            n = ctypes.c_size_t()
-            _check(lib.bsa_block_norm_backward_workspace_bytes(ctypes.byref(a), ctypes.byref(n)),
-                   "bsa_block_norm_backward_workspace_bytes")
-            ws = torch.empty(max(n.value, 1), dtype=torch.uint8, device=x.device)
-        _check(lib.bsa_block_norm_backward(ctypes.byref(a), _ptr(dstream), _ptr(dnormed), x.data_ptr(), _ptr(y),
-                                           stats.data_ptr(), g["x"].data_ptr(), _ptr(g["y"]), _ptr(g["post_weight"]),
-                                           _ptr(g["post_bias"]), _ptr(g["gate"]), _ptr(g["pre_weight"]),
-                                           _ptr(g["pre_bias"]), _ptr(ws), 0 if ws is None else ws.numel(), ptr),
-               "bsa_block_norm_backward")
+            if params and t is not None:
+                g[name] = t = torch.empty_like(t)
+                at.append(t.data_ptr())
+            else:
+                g[name] = None
+                at.append(None)
+        ws, n = None, ctypes.c_size_t()
+        if params and at != [None] * 5:
+            code = lib.bsa_block_norm_backward_workspace_bytes(a, n)
+            if code:
+                _check(code, "bsa_block_norm_backward_workspace_bytes")
+            ws = x.new_empty(n.value, dtype=torch.uint8)
+        code = lib.bsa_block_norm_backward(a, _ptr(dstream), _ptr(dnormed), x.data_ptr(), _ptr(y), stats.data_ptr(),
+                                           g["x"].data_ptr(), _ptr(g["y"]), *at, _ptr(ws), n.value, ptr)
+        if code:
+            _check(code, "bsa_block_norm_backward")
         return g
     return _on(dev, stream, call)
 
@@ -822,7 +828,7 @@ def bsa_fp8_quantize(x, square: bool = False, rows: bool = True, cols: bool = Fa
         ld = (m + 15) // 16 * 16
         codes = x.new_empty((n, ld), dtype=dtype)
         scale = x.new_empty(((n + 127) // 128 if square else n, (m + 127) // 128), dtype=torch.float32)
-        return (codes if ld == m else codes[:, :m]), scale, ld
+        return (codes if ld == m else codes.narrow(1, 0, m)), scale, ld
 
     def call(ptr):
         codes, scale, ld = form(R, C) if rows else (None, None, 0)
