@@ -503,12 +503,14 @@ __device__ __forceinline__ void turn4(float (&v)[4], int lane) {
 #pragma unroll
   for (int p = 0; p < 4; p += 2) {
     const float got = __shfl_xor_sync(0xffffffffu, odd ? v[p] : v[p + 1], 1);
-    (odd ? v[p] : v[p + 1]) = got;
+    v[p] = odd ? got : v[p];
+    v[p + 1] = odd ? v[p + 1] : got;
   }
 #pragma unroll
   for (int p = 0; p < 2; ++p) {
     const float got = __shfl_xor_sync(0xffffffffu, upper ? v[p] : v[p + 2], 2);
-    (upper ? v[p] : v[p + 2]) = got;
+    v[p] = upper ? got : v[p];
+    v[p + 2] = upper ? v[p + 2] : got;
   }
 }
 
