@@ -766,6 +766,7 @@ struct Team {
 };
 
 constexpr size_t kSmemMost = 220 * 1024;
+constexpr int kSmemBlock = 227 * 1024;  // what a block can have, and no layout of team_of is above
 
 Team team_of(int C, size_t esize, bool aligned, bool backward, bool means) {
   Team t{};
@@ -851,14 +852,17 @@ void fill(NormParams& p, const bsa_block_norm_args& a) {
   p.inv_c = 1.f / static_cast<float>(a.C);
 }
 
+// The limit of a kernel's dynamic shared memory belongs to the process, and one kernel serves many
+// sizes: it is only ever set to the block's most, so that a call from another thread never finds
+// it below its own size.  False where the launch was refused: what reads the kernel's results is
+// not launched then.
 template <typename F>
 bool start(F* kernel, const NormParams& p, const Team& t, int64_t blocks, cudaStream_t s) {
-  // past 48 KB the size has to be allowed first; the call is cheap and needs no state here
   if (t.smem > 48 * 1024 &&
-      cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(t.smem)) != cudaSuccess)
+      cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmemBlock) != cudaSuccess)
     return false;
   kernel<<<static_cast<unsigned>(blocks), t.threads * t.teams, t.smem, s>>>(p, t.threads);
-  return true;
+  return cudaPeekAtLastError() == cudaSuccess;
 }
 
 template <typename T, bool kBias>
