@@ -931,8 +931,10 @@ template <bool kAE5, bool kBE5, bool kTail, int kHeld>
 int start_rows(const RowsParams& p, int grid, int threads, cudaStream_t s) {
   auto* kernel = bsa_fp8_rows_kernel<kAE5, kBE5, kTail, kHeld>;
   const int smem = kRowsAhead * 2048 * (threads / 32);
-  if (smem > 32 * 1024 &&
-      cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem) != cudaSuccess)
+  // The limit belongs to the process, and one kernel serves several counts of warps: it is only
+  // ever set to the most, so that a call from another thread never finds it below its own size.
+  if (smem > 32 * 1024 && cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                               kRowsAhead * 2048 * kRowsWarpsMost) != cudaSuccess)
     return BSA_ERR_CUDA;
   kernel<<<grid, threads, smem, s>>>(p);
   return cudaGetLastError() == cudaSuccess ? BSA_OK : BSA_ERR_CUDA;

@@ -49,6 +49,23 @@ def _same(got, want):
     assert all(all(torch.equal(a, b) for a, b in zip(g, w)) for g, w in zip(got, want))
 
 
+def _product(K):  # a few tokens
+    g = torch.Generator(device="cuda").manual_seed(K)
+    a, w = (torch.randn(n, K, generator=g, device="cuda") for n in (4, 256))
+    a, b = bsa.bsa_fp8_quantize(a), bsa.bsa_fp8_quantize(w, square=True)
+    return lambda: [bsa.bsa_fp8_matmul(*a, *b)]
+
+
+@gpu
+@needs_cuda
+@pytest.mark.parametrize("Ks", [(1024, 2048), (1000, 2000)])  # a warp for each block of 128 of K, up to 16
+def test_products_of_a_few_rows(Ks):
+    calls = [_product(K) for K in Ks * 2]
+    want = [c() for c in calls]
+    _same(_at_once(calls, 8000), want)
+    assert bsa.bsa_sync_status() == 0
+
+
 def _norm(C, back):
     g = torch.Generator(device="cuda").manual_seed(C)
     x, y, ds, dn = torch.randn(4, 16, C, generator=g, device="cuda").unbind(0)
