@@ -1020,6 +1020,7 @@ int bsa_block_norm_backward(const bsa_block_norm_args* args, const void* dstream
   if (sums && (workspace == nullptr || reinterpret_cast<uintptr_t>(workspace) % 256 != 0 || workspace_bytes < b.bytes))
     return BSA_ERR_WORKSPACE;
   p.x = x, p.y = y, p.dstream = dstream, p.dnormed = dnormed, p.saved = stats, p.dx = dx, p.dy = dy;
+  if (y == nullptr) p.beta = 1.f;  // the stream is x itself
   p.part = sums ? static_cast<float*>(workspace) : nullptr;
   p.part_pre = sums ? p.part + b.slots * (means ? 2 : 1) * a.C : nullptr;
   p.rows_per_block = b.rows_per_block;

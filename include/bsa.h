@@ -465,7 +465,8 @@ int bsa_rope_apply(const void* q, void* q_out, int H, const void* k, void* k_out
  *     stream  = stream_scale x + branch_scale gate z
  *     normed  = N_pre(stream) pre_weight + pre_bias
  * the residual after a block with the norm after it and its gate, and the norm before the
- * next block.  Without y the stream is x itself and only the second norm is taken.
+ * next block.  Without y the stream is x itself, whatever the scales hold, and only the second
+ * norm is taken.
  *   rows = B * rows_per_batch rows; gate is [C] (gate_rows = 1) or [B, C] (gate_rows = B),
  *   row i taking row i / rows_per_batch of it.  1 <= C <= 8192.
  *   Parameters and gate are device arrays of `param_type` (`type` or BSA_FP32); weights and

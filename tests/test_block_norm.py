@@ -350,3 +350,22 @@ def test_autograd(post, pre):
         st = bsa.bsa_block_norm(x, pre=pre, pre_weight=a["pre_weight"], eps=EPS, save_stats=True)[2]
         want = bsa.bsa_block_norm_backward(None, dn, x, None, st, pre=pre, pre_weight=a["pre_weight"])["x"] + ds
         assert torch.equal(gx, want)
+
+
+@gpu
+@needs_cuda
+def test_the_norm_alone_has_no_scales():
+    # without y the stream is x itself, whatever the C structure's scales hold (a zeroed one, too)
+    a, x, _, _, dn = _make(2, 7, 768, None, "rms", 0, False, torch.bfloat16, torch.float32, 8, y=False)
+    _, n, st = bsa.bsa_block_norm(x, eps=EPS, save_stats=True, **a)
+    want = bsa.bsa_block_norm_backward(None, dn, x, None, st, **a)
+    for alpha, beta in ((0.0, 0.0), (3.0, -0.5)):
+        args = _args(rows_per_batch=7, C=768, post=0, post_weight=None, gate=None, pre_weight=a["pre_weight"].data_ptr(),
+                     branch_scale=alpha, stream_scale=beta)
+        got, dx = torch.empty_like(x), torch.empty_like(x)
+        stream = torch.cuda.current_stream().cuda_stream
+        assert bsa.lib.bsa_block_norm(ctypes.byref(args), x.data_ptr(), None, None, got.data_ptr(), None, stream) == bsa.BSA_OK
+        assert bsa.lib.bsa_block_norm_backward(ctypes.byref(args), None, dn.data_ptr(), x.data_ptr(), None, st.data_ptr(),
+                                               dx.data_ptr(), None, None, None, None, None, None, None, 0,
+                                               stream) == bsa.BSA_OK
+        assert torch.equal(dx, want["x"]) and torch.equal(got, n)
