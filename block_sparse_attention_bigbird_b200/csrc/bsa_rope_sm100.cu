@@ -173,6 +173,7 @@ void launch_rope(const RopeParams& p, bool vec, bool adj, dim3 grid, cudaStream_
 // 64: groups of 24, 12, 8, 6 and 4 took 76, 73, 74, 80 and 82 us).
 constexpr int64_t kRopeFill = 148 * 2048;
 constexpr int64_t kRopeGroup = 12;
+constexpr int64_t kGridRows = 65535;  // the most blocks along y
 
 }  // namespace
 }  // namespace bsa
@@ -307,9 +308,10 @@ int bsa_rope_apply(const void* q, void* q_out, int H, const void* k, void* k_out
   const int64_t threads = static_cast<int64_t>(B) * L * p.units;
   const int64_t blocks = (threads + kRopeThreads - 1) / kRopeThreads;
   const int64_t heads = H + static_cast<int64_t>(Hk);
-  if (blocks > 0x7fffffff || heads > 65535) return BSA_ERR_INVALID_ARG;
+  if (blocks > 0x7fffffff || heads > (1 << 30)) return BSA_ERR_INVALID_ARG;
   const int64_t once = kRopeFill / threads, often = std::min(8 * kRopeFill / threads, (heads + kRopeGroup - 1) / kRopeGroup);
-  const int64_t groups = std::min<int64_t>(heads, std::max<int64_t>({1, once, often}));
+  // one group a row of the grid
+  const int64_t groups = std::min<int64_t>({heads, kGridRows, std::max<int64_t>({1, once, often})});
   p.group = static_cast<int>((heads + groups - 1) / groups);
   const dim3 grid(static_cast<unsigned>(blocks), static_cast<unsigned>((heads + p.group - 1) / p.group));
   cudaStream_t s = static_cast<cudaStream_t>(stream);

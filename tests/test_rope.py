@@ -254,3 +254,15 @@ def test_gradients():
     down, _ = bsa.bsa_rope_apply(q.detach() - e, None, pos, rope)
     diff = ((up - down) / 2 * dq).sum().item()
     assert abs(diff - torch.autograd.grad((rotary(q, None, pos, rope)[0] * dq).sum(), q)[0][1, 2, 3, 5].item()) < 1e-5
+
+
+@gpu
+@needs_cuda
+def test_more_heads_than_a_grid_has_rows():
+    rope = bsa.bsa_rope_build([2, 2], adjacent=True)
+    g = torch.Generator(device="cuda").manual_seed(13)
+    for L in (1, 3):
+        q, k = (torch.randn(1, h, L, 8, generator=g, device="cuda") for h in (66_000, 5_001))
+        pos = torch.randint(0, 999, (2, 1, L), generator=g, device="cuda")
+        for x, y in zip((q, k), bsa.bsa_rope_apply(q, k, pos, rope)):
+            _check(y, x, pos, rope)
