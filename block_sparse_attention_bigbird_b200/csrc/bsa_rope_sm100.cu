@@ -12,9 +12,9 @@
 // What bounds it: q and k are read and written once; the arithmetic is 3 operations an
 // element.  The sines are the costly part (about 60 instructions a pair), so a thread keeps
 // the angles of eight pairs of one token and walks over heads with them.  It reads the
-// pairs' two halves as two 16-byte vectors.  The heads are cut into groups (blockIdx.y) of
-// at least twelve while the card is filled more than once, so that the last wave is short;
-// with one token a call a thread takes one head.
+// pairs' two halves as two 16-byte vectors.  The heads are cut into equal groups (blockIdx.y),
+// of at most twelve unless the tokens alone fill the card several times (kRopeFill), so that
+// the last wave is short; with one token a call a thread takes one head.
 //
 // Measured: B = 4, L = 16384, 12 + 12 heads of 64 in bf16 (403 MB read and written) 66 us
 // alone, 70 in a row (5.8 TB/s, where a copy has 6.55); 80 registers, six blocks an SM.  Six
@@ -168,10 +168,11 @@ void launch_rope(const RopeParams& p, bool vec, bool adj, dim3 grid, cudaStream_
   }
 }
 
-// Threads that fill the card (148 SMs x 2048) once, up to where heads are cut singly; up to
-// eight times they are cut into groups of twelve or more (B = 4, L = 16384, 12 + 12 heads of
-// 64: groups of 24, 12, 8, 6 and 4 took 76, 73, 74, 80 and 82 us).
-constexpr int64_t kRopeFill = 148 * 2048;
+// Threads that fill an SM.  Where a call's fill the card less than once, its heads are cut into as
+// many groups as fill it once; else into equal groups of at most twelve, but not into more than
+// fill it eight times (B = 4, L = 16384, 12 + 12 heads of 64: groups of 24, 12, 8, 6 and 4 took
+// 76, 73, 74, 80 and 82 us).
+constexpr int64_t kRopeFill = 2048;
 constexpr int64_t kRopeGroup = 12;
 constexpr int64_t kGridRows = 65535;  // the most blocks along y
 
@@ -309,7 +310,8 @@ int bsa_rope_apply(const void* q, void* q_out, int H, const void* k, void* k_out
   const int64_t blocks = (threads + kRopeThreads - 1) / kRopeThreads;
   const int64_t heads = H + static_cast<int64_t>(Hk);
   if (blocks > 0x7fffffff || heads > (1 << 30)) return BSA_ERR_INVALID_ARG;
-  const int64_t once = kRopeFill / threads, often = std::min(8 * kRopeFill / threads, (heads + kRopeGroup - 1) / kRopeGroup);
+  const int64_t fill = sms * kRopeFill;
+  const int64_t once = fill / threads, often = std::min(8 * fill / threads, (heads + kRopeGroup - 1) / kRopeGroup);
   // one group a row of the grid
   const int64_t groups = std::min<int64_t>({heads, kGridRows, std::max<int64_t>({1, once, often})});
   p.group = static_cast<int>((heads + groups - 1) / groups);
