@@ -266,3 +266,23 @@ def test_more_heads_than_a_grid_has_rows():
         pos = torch.randint(0, 999, (2, 1, L), generator=g, device="cuda")
         for x, y in zip((q, k), bsa.bsa_rope_apply(q, k, pos, rope)):
             _check(y, x, pos, rope)
+
+
+@gpu
+@needs_cuda
+def test_a_replayed_graph_reads_all_of_its_inputs_again():
+    rope = bsa.bsa_rope_build([8, 12, 12])
+    g = torch.Generator(device="cuda").manual_seed(12)
+    q = torch.randn(2, 6, 50, 64, generator=g, device="cuda")
+    k = torch.randn(2, 50, 3, 64, generator=g, device="cuda").transpose(1, 2)
+    pos = torch.randint(0, 999, (3, 2, 50), generator=g, device="cuda")
+    bsa.bsa_rope_apply(q, k, pos, rope)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        got = bsa.bsa_rope_apply(q, k, pos, rope)
+    for change in (lambda: q.mul_(2), lambda: k.add_(1), lambda: pos.add_(17), lambda: (q.neg_(), k.mul_(3), pos.mul_(2))):
+        change()
+        graph.replay()
+        want = bsa.bsa_rope_apply(q, k, pos, rope)
+        assert all(torch.equal(a, b) for a, b in zip(got, want))
+        _check(got[1], k, pos, rope)
