@@ -265,6 +265,7 @@ int bsa_rope_apply(const void* q, void* q_out, int H, const void* k, void* k_out
   if (B == 0 || L == 0 || H + static_cast<int64_t>(Hk) == 0) return BSA_OK;
   if ((H > 0 && (q == nullptr || q_out == nullptr)) || (Hk > 0 && k_out == nullptr) || positions == nullptr)
     return BSA_ERR_INVALID_ARG;
+  if (reinterpret_cast<uintptr_t>(positions) % (position_type == BSA_INT64 ? 8 : 4) != 0) return BSA_ERR_INVALID_ARG;
   // one result may not be the other's, nor the other's input
   if (H > 0 && Hk > 0 && (q_out == k_out || q_out == k || k_out == q)) return BSA_ERR_INVALID_ARG;
   RopeParams p;

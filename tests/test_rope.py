@@ -75,6 +75,15 @@ def test_apply_refuses_before_device_work():
         assert call(**kw) == bsa.BSA_OK, kw  # empty calls
 
 
+def test_apply_refuses_positions_between_elements():
+    rope = bsa.bsa_rope_build([4, 4])
+    a, b = 1 << 20, 1 << 21
+    strides, ps = (ctypes.c_int64 * 12)(*[16] * 12), (ctypes.c_int64 * 3)(1, 1, 1)
+    for ty, off in ((bsa.INT64, 4), (bsa.INT64, 1), (bsa.INT32, 2), (bsa.FP32, 2)):
+        code = bsa.lib.bsa_rope_apply(a, a, 2, b, b, 1, 1, 4, 16, bsa.BF16, strides, a + off, ty, ps, rope.handle, 0, None)
+        assert code == bsa.BSA_ERR_INVALID_ARG, (ty, off)
+
+
 def test_a_code_is_copied_and_stored_by_its_tables():
     for rope in (bsa.bsa_rope_build([8, 12, 12], 1e6, per_axis=True), bsa.bsa_rope_from_table([2, 0], [0.5, -3.0], True)):
         for again in (copy.deepcopy(rope), pickle.loads(pickle.dumps(rope))):
