@@ -293,7 +293,10 @@ extern "C" int bsa_fp8_quantize(const void* x, int type, int R, int C, int squar
   if (x == nullptr || (codes == nullptr && codes_t == nullptr) || (codes != nullptr && scale == nullptr) ||
       (codes_t != nullptr && scale_t == nullptr))
     return BSA_ERR_INVALID_ARG;
-  if (reinterpret_cast<uintptr_t>(x) % type_bytes(type) != 0) return BSA_ERR_INVALID_ARG;
+  if (reinterpret_cast<uintptr_t>(x) % type_bytes(type) != 0 ||
+      (codes != nullptr && reinterpret_cast<uintptr_t>(scale) % 4 != 0) ||
+      (codes_t != nullptr && reinterpret_cast<uintptr_t>(scale_t) % 4 != 0))
+    return BSA_ERR_INVALID_ARG;
   const int64_t r16 = (static_cast<int64_t>(R) + 15) / 16 * 16, c16 = (static_cast<int64_t>(C) + 15) / 16 * 16;
   if (codes != nullptr && (!aligned16(codes) || ld % 16 != 0 || ld < c16)) return BSA_ERR_INVALID_ARG;
   if (codes_t != nullptr && (!aligned16(codes_t) || ld_t % 16 != 0 || ld_t < r16)) return BSA_ERR_INVALID_ARG;

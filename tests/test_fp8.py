@@ -44,6 +44,13 @@ def test_quantize_refuses_before_device_work():
     assert call(R=0) == bsa.BSA_OK and call(C=0) == bsa.BSA_OK
 
 
+def test_quantize_refuses_scales_between_elements():
+    p = 1 << 20
+    for scale, scale_t in ((p + 2, p), (p, p + 1)):
+        code = bsa.lib.bsa_fp8_quantize(p, bsa.BF16, 4, 20, 0, bsa.E4M3, p, 32, scale, p, 16, scale_t, None)
+        assert code == bsa.BSA_ERR_INVALID_ARG, (scale, scale_t)
+
+
 def test_matmul_refuses_before_device_work():
     p = 1 << 20
 
