@@ -32,6 +32,7 @@ SPLIT_THRESHOLD = 48  # BSA_SPLIT_THRESHOLD in include/bsa.h: longer tile unions
 BF16, FP16, FP32, E4M3, E5M2, INT32, INT64 = range(7)
 NORMS = {None: 0, "rms": 1, "layer": 2}  # BSA_NORM_*
 NORM_COLUMNS_MOST = 8192
+INT_MOST = 2 ** 31 - 1  # ctypes cuts what is above to 32 bits without a word
 
 
 class BlockNormArgs(ctypes.Structure):
@@ -530,6 +531,9 @@ def _ptr(t):
     return None if t is None else t.data_ptr()
 
 
+_TOO_LARGE = "a size needs more than 31 bits"
+
+
 # ---------------------------------------------------------------- rotary positions
 class Rope:
     """Owner of a bsa_rope*; freed with the object."""
@@ -621,6 +625,8 @@ def bsa_rope_apply(q, k, positions, rope: Rope, inverse: bool = False, q_out=Non
             raise ValueError("k must be like q, [B, Hk, L, d] with contiguous columns")
         Hk = k.shape[1]
     ps, n = positions.stride(), positions.shape
+    if max(B, H, Hk, L, d) > INT_MOST:
+        raise ValueError(_TOO_LARGE)
     if pt not in (INT32, INT64, FP32) or len(n) not in (2, 3) or n[0] < rope.n_axes or n[-1] != L or \
             (len(n) == 3 and n[1] != B) or positions.get_device() != dev:
         raise ValueError(f"positions must be int32, int64 or fp32 [axes, L] or [axes, B, L] on q's device with at "
@@ -702,6 +708,8 @@ def _norm_args(x, y, post, post_weight, post_bias, gate, branch_scale, stream_sc
         else:
             g = _vector_of("gate (or [B, C])", gate, pt, C, dev)
     rows = x.numel() // C
+    if rows > INT_MOST or C > INT_MOST:
+        raise ValueError(_TOO_LARGE)
     a = BlockNormArgs(
         B, rows // B if B else 0, C, ty, pty, NORMS[post], NORMS[pre],
         None if post_weight is None else _vector_of("post_weight", post_weight, pt, C, dev),
@@ -823,6 +831,8 @@ def bsa_fp8_quantize(x, square: bool = False, rows: bool = True, cols: bool = Fa
         raise ValueError("ask for rows, cols or both")
     C = x.shape[-1]
     R = x.numel() // C
+    if R > INT_MOST or C > INT_MOST:
+        raise ValueError(_TOO_LARGE)
 
     def form(n, m):  # codes [n, m] in padded rows, their pitch, and their scales
         ld = (m + 15) // 16 * 16
@@ -867,6 +877,8 @@ def _scale_rows(name, scale, rows, kb, dev) -> int:
 
 
 def bsa_fp8_matmul_workspace_bytes(M: int, N: int, K: int) -> int:
+    if max(M, N, K) > INT_MOST:
+        raise ValueError(_TOO_LARGE)
     n = ctypes.c_size_t()
     _check(lib.bsa_fp8_matmul_workspace_bytes(M, N, K, ctypes.byref(n)), "bsa_fp8_matmul_workspace_bytes")
     return n.value
@@ -887,6 +899,8 @@ def bsa_fp8_matmul(a, a_scale, b, b_scale, bias=None, out_dtype=None, out=None, 
     (M, K), (N, Kb) = a.shape, b.shape
     if Kb != K:
         raise ValueError("a and b must have the same number of columns")
+    if max(M, N, K) > INT_MOST:
+        raise ValueError(_TOO_LARGE)
     kb = (K + 127) // 128
     ar, br = _scale_rows("a_scale", a_scale, M, kb, dev), _scale_rows("b_scale", b_scale, N, kb, dev)
     bp, bty = None, BF16

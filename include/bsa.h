@@ -448,7 +448,7 @@ void bsa_rope_free(bsa_rope* rope);
  *             (p_strides host, 3 int64; 0 shares positions between batch elements).
  *   d         2 n <= d <= 256.
  * The angle is formed in 64 bits, so that far positions keep their phase.  B, H or L of 0
- * is an empty call.  Enqueues one kernel on `stream`.
+ * is an empty call; H + Hk <= 2^30.  Enqueues one kernel on `stream`.
  */
 int bsa_rope_apply(const void* q, void* q_out, int H, const void* k, void* k_out, int Hk, int B, int L, int d,
                    int type, const int64_t* strides, const void* positions, int position_type,
@@ -467,7 +467,7 @@ int bsa_rope_apply(const void* q, void* q_out, int H, const void* k, void* k_out
  * the residual after a block with the norm after it and its gate, and the norm before the
  * next block.  Without y the stream is x itself, whatever the scales hold, and only the second
  * norm is taken.
- *   rows = B * rows_per_batch rows; gate is [C] (gate_rows = 1) or [B, C] (gate_rows = B),
+ *   rows = B * rows_per_batch rows, below 2^31; gate is [C] (gate_rows = 1) or [B, C] (gate_rows = B),
  *   row i taking row i / rows_per_batch of it.  1 <= C <= 8192.
  *   Parameters and gate are device arrays of `param_type` (`type` or BSA_FP32); weights and
  *   biases may be NULL (1 and 0), the gate too (1).  Biases need a norm.
@@ -529,7 +529,7 @@ int bsa_block_norm_backward(const bsa_block_norm_args* args, const void* dstream
  *     x transposed, so a block is 128 rows of one column;
  *   square != 0: blocks are 128 x 128: scale [ceil(R/128), ceil(C/128)], scale_t its
  *     transpose, and codes_t the transpose of codes.
- * A form whose codes are NULL is left out (not both).  A row's bytes from its end to the next
+ * R, C <= 2^30.  A form whose codes are NULL is left out (not both).  A row's bytes from its end to the next
  * multiple of 16 are written too (bsa_fp8_matmul does not read them).  One pass over x, one kernel.
  */
 int bsa_fp8_quantize(const void* x, int type, int R, int C, int square, int code_type, void* codes, int64_t ld,
@@ -551,7 +551,8 @@ int bsa_fp8_matmul_workspace_bytes(int M, int N, int K, size_t* bytes);
  * With y = x W^T this is a linear layer (a: x in rows form, b: W in square form), its
  * input's gradient (a: dy in rows form, b: W's columns form) and its weight's (a: dy, b: x,
  * both in columns form).  Each block's products are summed by the tensor cores, the blocks
- * in fp32 with their scales, in a fixed order.  M or N of 0 is an empty call; K >= 1.
+ * in fp32 with their scales, in a fixed order.  M or N of 0 is an empty call; K >= 1; each
+ * at most 2^30.
  * workspace: as sized above, 256-byte aligned, any contents (NULL when 0), not shared by calls
  * that may run at the same time.  Enqueues one kernel, two where K is split.  A device-side timeout is reported by bsa_sync_status.
  */
