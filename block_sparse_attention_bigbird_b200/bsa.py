@@ -514,10 +514,13 @@ def _raw_stream(index: int) -> int:
 
 def _on(index: int, stream, call):
     """call(stream pointer) with the tensors' device ``index`` current, and ``stream``, where one
-    is given, the stream that call's allocations belong to."""
+    is given, the stream that call's allocations belong to.  An integer is taken to be a stream of
+    that device."""
     import torch
     if stream is None and index == torch.cuda.current_device():
         return call(_raw_stream(index))
+    if stream is not None and not isinstance(stream, int) and stream.device_index != index:
+        raise ValueError("stream belongs to another device than the tensors")
     with torch.cuda.device(index):
         if stream is None:
             return call(_raw_stream(index))
