@@ -525,7 +525,8 @@ def _on(index: int, stream, call):
         if stream is None:
             return call(_raw_stream(index))
         if isinstance(stream, int):
-            stream = torch.cuda.ExternalStream(stream, device=index)
+            # torch makes a new stream of the pointer 0
+            stream = torch.cuda.ExternalStream(stream, device=index) if stream else torch.cuda.default_stream(index)
         with torch.cuda.stream(stream):
             return call(stream.cuda_stream)
 
