@@ -173,7 +173,12 @@ class BigBirdBlock(torch.nn.Module):
 
     ``pre`` and ``post`` are "rms", "layer" or (``post``) None; layer norms have biases.  gate: a
     learned gate [dim], or False for none; a call may give its own, [dim] or [B, dim].  The other
-    arguments are BigBirdSelfAttention's.  Parameters are all of the stream's type or all fp32.
+    arguments are BigBirdSelfAttention's.
+
+    The stream x is bf16.  The parameters of the norm before the attention are of one type, x's or
+    fp32, and so are those of the norm after it, the gate and the following block's first norm.
+    The projections' parameters are bf16, or of any type that fp8_linear takes with ``fp8`` (under
+    autocast, of any that it casts).
     """
 
     def __init__(self, dim: int, num_heads: int, pre: str = "rms", post: Optional[str] = "rms", gate: bool = True,
@@ -190,6 +195,23 @@ class BigBirdBlock(torch.nn.Module):
         self.post_bias = zero() if post == "layer" else None
         self.gate = one() if gate else None
 
+    def _check_types(self, x, gate, normed, following):
+        """Refuses parameters that one of the steps below would, before the first runs."""
+        layer = self.attention
+        linear = [m for m in (layer.qkv, layer.proj) if type(m) is torch.nn.Linear]
+        if layer.fused and any(m.weight.dtype != torch.bfloat16 for m in linear):
+            raise ValueError("the fused projections take bf16 parameters")
+        if not (layer.fused or layer.fp8 or torch.is_autocast_enabled(x.device.type)) and \
+                any(m.weight.dtype != x.dtype for m in linear):
+            raise ValueError("without fp8 or autocast the projections' parameters must be of the stream's type")
+        after = [self.post_weight, self.post_bias, gate]
+        if following is not None:
+            after += [following.pre_weight, following.pre_bias]
+        for params in ([self.pre_weight, self.pre_bias] if normed is None else [], after):
+            types = {p.dtype for p in params if p is not None}
+            if len(types) > 1 or not types <= {x.dtype, torch.float32}:
+                raise ValueError("the norm parameters and gate of one pass must be all of the stream's type or all fp32")
+
     def forward(self, x: torch.Tensor, key_mask: Optional[torch.Tensor] = None,
                 positions: Optional[torch.Tensor] = None, gate: Optional[torch.Tensor] = None,
                 normed: Optional[torch.Tensor] = None, following: Optional["BigBirdBlock"] = None):
@@ -198,13 +220,15 @@ class BigBirdBlock(torch.nn.Module):
         """
         if following is not None and following.eps != self.eps:
             raise ValueError("one pass takes both norms with one eps: the following block has another")
+        gate = self.gate if gate is None else gate
+        self._check_types(x, gate, normed, following)
         if normed is None:
             _, normed = block_norm(x, pre=self.pre, pre_weight=self.pre_weight, pre_bias=self.pre_bias, eps=self.eps)
         y = self.attention(normed, key_mask=key_mask, positions=positions)
         nxt = {"pre": None} if following is None else {"pre": following.pre, "pre_weight": following.pre_weight,
                                                       "pre_bias": following.pre_bias}
         stream, after = block_norm(x, y.contiguous(), post=self.post, post_weight=self.post_weight,
-                                   post_bias=self.post_bias, gate=self.gate if gate is None else gate,
+                                   post_bias=self.post_bias, gate=gate,
                                    branch_scale=self.branch_scale, stream_scale=self.stream_scale, eps=self.eps,
                                    **nxt)
         return stream if following is None else (stream, after)

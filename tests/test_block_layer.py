@@ -38,6 +38,42 @@ def test_refusals():
         one(torch.zeros(1, 64, 128), following=other)
 
 
+def test_the_block_refuses_types_that_do_not_go_together():
+    x = torch.zeros(1, 64, 128, dtype=torch.bfloat16)
+    block = LY.BigBirdBlock(128, 2, post="layer")  # all fp32, for a bf16 stream
+    with pytest.raises(ValueError, match="projections"):
+        block(x)
+    with pytest.raises(ValueError, match="fused"):
+        LY.BigBirdBlock(128, 2, fused=True)(x)
+    block.attention.to(torch.bfloat16)
+    for module, kw in ((block, dict(gate=torch.zeros(128, dtype=torch.bfloat16))),
+                       (block, dict(following=LY.BigBirdBlock(128, 2).to(torch.bfloat16))),
+                       (LY.BigBirdBlock(128, 2, fp8=True).half(), {})):
+        with pytest.raises(ValueError, match="norm parameters and gate"):
+            module(x, **kw)
+    block.post_bias.data = block.post_bias.data.double()
+    with pytest.raises(ValueError, match="norm parameters and gate"):
+        block(x)
+
+
+def test_the_block_takes_the_types_that_do(monkeypatch):
+    # over a norm and an attention that do nothing: which calls get past the types
+    monkeypatch.setattr(LY, "block_norm", lambda x, y=None, **_: (x, x))
+    x = torch.zeros(1, 64, 128, dtype=torch.bfloat16)
+    for kw, attention, rest in ((dict(fp8=True), torch.float32, torch.float32), (dict(fp8=True), torch.bfloat16, torch.float32),
+                                (dict(fused=True), torch.bfloat16, torch.float32), ({}, torch.bfloat16, torch.bfloat16),
+                                ({}, torch.bfloat16, torch.float32)):
+        block = LY.BigBirdBlock(128, 2, **kw).to(rest)
+        block.attention.to(attention)
+        block.attention.forward = lambda t, **_: t
+        assert block(x, following=block)[0] is x
+    block = LY.BigBirdBlock(128, 2)  # autocast casts the projections' weights
+    block.attention.forward = lambda t, **_: t
+    with torch.autocast("cpu", torch.bfloat16):
+        assert block(x) is x
+    assert block(x.float()).dtype == torch.float32
+
+
 def test_a_block_with_rotary_positions_is_copied():
     m = LY.BigBirdBlock(128, 2, rope=(8, 12, 12))
     again = copy.deepcopy(m)
