@@ -72,7 +72,10 @@ class _Rotary(torch.autograd.Function):
 
 
 def rotary(q: torch.Tensor, k: Optional[torch.Tensor], positions: torch.Tensor, rope: "bsa.Rope"):
-    """(q, k) with rotary positions (see bsa.bsa_rope_apply), differentiable in q and k."""
+    """(q, k) with rotary positions (see bsa.bsa_rope_apply), differentiable in q and k.  Positions
+    have no gradient: those that want one are refused."""
+    if positions.requires_grad and torch.is_grad_enabled():
+        raise ValueError("positions have no gradient: detach them")
     got = _Rotary.apply(q, k, positions, rope)
     return got if k is not None else (got, None)
 

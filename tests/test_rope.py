@@ -98,6 +98,15 @@ def test_binding_refuses_cpu_tensors():
         bsa.bsa_rope_apply(q, None, torch.zeros(1, 4, dtype=torch.int64), bsa.bsa_rope_build([8]))
 
 
+def test_positions_that_want_a_gradient_are_refused():
+    from block_sparse_attention_bigbird_b200 import rotary
+    pos = torch.zeros(1, 4, requires_grad=True)
+    with pytest.raises(ValueError, match="positions"):
+        rotary(torch.zeros(1, 2, 4, 16), None, pos, bsa.bsa_rope_build([8]))
+    with torch.no_grad(), pytest.raises(ValueError, match="q must be"):  # none is wanted: q is what is wrong
+        rotary(torch.zeros(1, 2, 4, 16), None, pos, bsa.bsa_rope_build([8]))
+
+
 # ---------------------------------------------------------------- GPU
 U = {torch.bfloat16: 2.0 ** -8, torch.float16: 2.0 ** -11, torch.float32: 2.0 ** -24}
 
