@@ -71,6 +71,13 @@ def test_matmul_refuses_before_device_work():
     assert bsa.lib.bsa_fp8_matmul_workspace_bytes(4, 8, 50, None) == bsa.BSA_ERR_INVALID_ARG
 
 
+def test_linear_refuses_a_gradient_type_at_once():
+    from block_sparse_attention_bigbird_b200 import fp8_linear
+    for bad in (torch.bfloat16, torch.float8_e8m0fnu, None):
+        with pytest.raises(ValueError, match="grad_dtype"):
+            fp8_linear(torch.zeros(2, 16), torch.zeros(4, 16), grad_dtype=bad)
+
+
 # ---------------------------------------------------------------- GPU: quantiser
 def _same_codes(codes, scale, x, fmt, square):
     ref, ref_scale = O8.quantise(x.float().cpu().numpy(), fmt, square)
