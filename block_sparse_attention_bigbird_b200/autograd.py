@@ -175,7 +175,7 @@ def fp8_linear(x: torch.Tensor, weight: torch.Tensor, bias: Optional[torch.Tenso
         raise ValueError("x must be bf16 or fp32")
     if weight.dim() != 2 or weight.numel() == 0 or x.dim() < 1 or x.shape[-1] != weight.shape[1]:
         raise ValueError("x must be [.., K] and weight [N, K], N and K at least 1")
-    if grad_dtype not in (torch.float8_e4m3fn, torch.float8_e5m2):
+    if grad_dtype not in (torch.float8_e4m3fn, torch.float8_e5m2, None):  # None: e4m3, as in bsa_fp8_quantize
         raise ValueError("grad_dtype must be torch.float8_e4m3fn or torch.float8_e5m2")
     # inside a Function gradients are always off, so whether any are wanted is asked here
     return _Fp8Linear.apply(x, weight, bias, grad_dtype, torch.is_grad_enabled())
