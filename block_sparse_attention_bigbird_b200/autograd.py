@@ -169,7 +169,9 @@ def fp8_linear(x: torch.Tensor, weight: torch.Tensor, bias: Optional[torch.Tenso
     128 x 128, both to e4m3; the backward quantises the gradient to ``grad_dtype`` along its
     columns for x's gradient and along its rows for the weight's, whose other operand is x
     quantised along its rows (bsa.bsa_fp8_quantize, bsa.bsa_fp8_matmul).  Differentiable in x,
-    weight and bias.
+    weight and bias (the bias's gradient is torch's sum over rows).  The weight is quantised in
+    every call: who multiplies many times by one weight keeps its codes and calls
+    bsa.bsa_fp8_matmul (4 x 8192 x 8192: 17 us, 61 with the quantisers).
     """
     if x.dtype not in (torch.bfloat16, torch.float32):
         raise ValueError("x must be bf16 or fp32")

@@ -735,7 +735,8 @@ def bsa_block_norm(x, y=None, post: Optional[str] = None, post_weight=None, post
 
     x, y: contiguous bf16, fp16 or fp32 CUDA tensors [.., C], C <= 8192.  post, pre: "rms",
     "layer" or None for no norm (then normed is None).  gate: [C], or [B, C] with one row for
-    each index of x's first axis.  Parameters and gate are all of x's type or all fp32; None
+    each index of x's first axis (made for batch elements of many rows: the backward's time and
+    workspace grow with the gate's rows).  Parameters and gate are all of x's type or all fp32; None
     stands for 1 (weights, gate) and 0 (biases).  Without y the stream is x itself and only
     the pre norm is taken.  stats (with ``save_stats``): fp32 [rows, 4], for the backward.
     out and normed may be given; they may be x or y, not each other.

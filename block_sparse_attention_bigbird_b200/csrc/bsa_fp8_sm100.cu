@@ -25,13 +25,15 @@
 // (16x128b 277, 16x256b 521), their additions 340 (kBRows 540: two operations a pair), waits and
 // hand-overs about 350.  Reads and additions hardly overlap, as the two warps of a scheduler wait
 // for the same accumulator, so the adding warps are what bounds long products: about 1000 cycles,
-// kBRows 1300.  65536 x 2304 x 768 takes 141 us (1.65 PFLOP/s; without its loads 128, without
+// kBRows 1300.  Their reads and additions alone would fit under the MMAs (kBRows would not): it is
+// the waits in series with them that do not.  65536 x 2304 x 768 takes 141 us (1.65 PFLOP/s; without its loads 128, without
 // writing 124), 8192^3 524 us (2.10 PFLOP/s, at the power limit), 2304 x 768 x 65536 with
 // kBRows 159 us (1.46 PFLOP/s).
 // What follows from it.  An issuer whose loop is uniform over the warp and elects a lane for the
 // MMAs alone takes half the time of a single thread's loop, whose descriptors have to be moved to
 // uniform registers after every wait (513 cycles a block, 711 to 851); two of them hide the waits.
-// No register may spill: with the shared memory taken, L1 is too small to hold them.  Both halves
+// Registers may hardly spill: with the shared memory taken, L1 is too small to hold them (256
+// columns with kBRows spill 16 bytes, the other forms none).  Both halves
 // of the columns run the same code (a copy for each took 147 us instead of 141).  Halves with
 // MMAs of N = 128 and accumulators of their own took 155 us: at that width shared memory cannot
 // feed the tensor cores.
@@ -44,7 +46,9 @@
 // m16n8k16 with b as the 16-row side and the tokens as the 8 columns (a tcgen05 tile of 128 rows
 // would be 15/16 empty).  The products of a block of 128 are summed in fp32 before their scale;
 // the warps' sums meet in shared memory in a fixed order.
-// 4 x 8192 x 8192 (67 MB of b) takes 16.9 us in a graph, a loop that only reads b 11 us.  Where
+// 4 x 8192 x 8192 (67 MB of b) takes 16.9 us in a graph, a loop that only reads b 11 us: its 512
+// tiles are three rounds of 148 SMs and one of 68, so that the SMs stand still for 13 % of the
+// time, and a short kernel's start and end do the rest.  Where
 // the kernels meet, 8 and 9 rows of N = K = 8192 take 17.2 and 19.4 us, of 2304 x 768 2.6 and 4.9:
 // eight tokens are what one mma.sync has columns for.
 //
@@ -675,7 +679,9 @@ __global__ void __launch_bounds__(kMThreads, 1) bsa_fp8_mma_kernel(const __grid_
 
 // Sums the splits' partial results in order, adds the bias and rounds once; kVec elements a
 // thread (4 where rows of the result are multiples of 4).  Launched as the product's
-// programmatic dependent: its launch overlaps the product's end.
+// programmatic dependent.  The product triggers nothing early, so that its blocks come when the
+// product's have ended: what is saved is a launch's own time (2304 x 768 x 65536: 190 us a pass,
+// 192 as an ordinary launch).
 template <int kVec>
 __global__ void __launch_bounds__(256) bsa_fp8_sum_kernel(const float* part, int splits, int64_t stride, int64_t n,
                                                           int N, const void* bias, int bias_f32, void* out,

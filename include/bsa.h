@@ -469,6 +469,8 @@ int bsa_rope_apply(const void* q, void* q_out, int H, const void* k, void* k_out
  * norm is taken.
  *   rows = B * rows_per_batch rows, below 2^31; gate is [C] (gate_rows = 1) or [B, C] (gate_rows = B),
  *   row i taking row i / rows_per_batch of it.  1 <= C <= 8192.
+ *   The backward's time and workspace grow with the gate's rows: it is made for gates that many rows
+ *   share.
  *   Parameters and gate are device arrays of `param_type` (`type` or BSA_FP32); weights and
  *   biases may be NULL (1 and 0), the gate too (1).  Biases need a norm.
  */
@@ -520,8 +522,9 @@ int bsa_block_norm_backward(const bsa_block_norm_args* args, const void* dstream
  * bsa_fp8_matmul.  x: device, BSA_BF16, BSA_FP16 or BSA_FP32, [R, C] contiguous.
  * code_type T: BSA_E4M3 or BSA_E5M2 with largest value top.  A block with largest
  * magnitude m (taken as at least 2^-100) has
- *     scale = m / top,   code = T(x (top / m)), rounded to nearest even,
- * so x ~ code scale.  A block that holds a NaN or an infinity has a scale or codes that
+ *     scale = fl(m / top),   code = T(fl(x fl(top / m))),
+ * fl rounding to fp32 and T to the format, to nearest even (a quotient within 2^-23 of a tie between
+ * two codes may therefore go either way), so x ~ code scale.  A block that holds a NaN or an infinity has a scale or codes that
  * are not finite either.
  *   rows form: codes [R, C] with row pitch ld (bytes, a multiple of 16, >= C), scale fp32
  *     [R, ceil(C/128)]: a block is 128 consecutive columns of one row;
