@@ -42,6 +42,9 @@
 // no 16-byte starts, so that a thread's pieces are of two elements (8-byte copies) and a row takes
 // two barriers of a team, both a matter of this layout and no limit of the card.  Without the ring
 // (loads straight to registers) the three took 102, 285 and 136 us.
+// Statistics of the stored stream (kStored) cost a bf16 layer norm's training forward 5 to 10 % with
+// biases (65536 rows of 768: 128 and 135 us, 8192 of 4096: 173 and 192); taken by two sums of
+// their own after the first ones they cost up to 35 % (140 and 189 us without biases, now 159).
 #include <cuda_runtime.h>
 
 #include <algorithm>
@@ -246,7 +249,45 @@ __device__ __forceinline__ float2 statistics(Pairs<kVec * kNV>& v, int kind, con
   return make_float2(mean, 1.f / sqrtf(fmaf(s[0], p.inv_c, p.eps)));
 }
 
+// The same for a layer norm, and what its backward starts from: mean and 1 / sqrt(..) of the row as it
+// is stored, rounded to T (x, y of the result; z, w the ones of v itself).  The backward reads the
+// stored row, and the statistics of the unrounded one do not fit a row that rounding moves by a good
+// part of its deviation: its normalised values would have a mean, or a square, far from 0 and 1.
+// Sums of the stored row are taken from the rounded mean s, near which such a row's values are a few
+// steps of T, so that the difference of squares does not cancel (a constant row gives exact zeros);
+// they share the second sum's steps over the team.
+template <typename T, int kVec, int kNV, bool kWarpTeam>
+__device__ __forceinline__ float4 statistics_stored(Pairs<kVec * kNV>& v, const Cols<kVec, kNV, kWarpTeam>& cols,
+                                                    const NormParams& p, TeamSum<1, kWarpTeam>& sum,
+                                                    TeamSum<3, kWarpTeam>& sum3) {
+  constexpr int kP = kVec * kNV / 2;
+  uint64_t a = 0ull;
+#pragma unroll
+  for (int e = 0; e < kP; ++e) a = ptx::fadd2(a, v.v[e]);
+  float m[1] = {sum2(a)};
+  sum(m);
+  const float mean = m[0] * p.inv_c, s = to_f32(from_f32<T>(mean));
+  uint64_t squares = 0ull, off = 0ull, off2 = 0ull;
+#pragma unroll
+  for (int e = 0; e < kP; ++e) {
+    float lo, hi;
+    ptx::unpack2(v.v[e], lo, hi);
+    unpack(pack(lo, hi, T()), T(), lo, hi);
+    const uint64_t d = ptx::fadd2(ptx::pack2(lo, hi), cols.inside(e, -s));
+    off = ptx::fadd2(off, d);
+    off2 = ptx::ffma2(d, d, off2);
+    v.v[e] = ptx::fadd2(v.v[e], cols.inside(e, -mean));
+    squares = ptx::ffma2(v.v[e], v.v[e], squares);
+  }
+  float q[3] = {sum2(squares), sum2(off), sum2(off2)};
+  sum3(q);
+  const float d = q[1] * p.inv_c, var = fmaxf(fmaf(q[2], p.inv_c, -d * d), 0.f);
+  return make_float4(s + d, 1.f / sqrtf(var + p.eps), mean, 1.f / sqrtf(fmaf(q[0], p.inv_c, p.eps)));
+}
+
 constexpr int kWarpBlock = 128;  // threads of a forward block whose teams are warps
+// a forward team's areas for its sums: [2][1][32] floats, and [2][3][32] with kStored
+__host__ __device__ constexpr int sum_bytes(bool stored) { return stored ? 1024 : 256; }
 // Threads of a backward block at most: where a thread has more than eight elements of a row it
 // needs 168 registers, else 128 do.  (Rows of more than 4096 columns take 512 threads whatever
 // that costs.)
@@ -383,18 +424,20 @@ struct Ring {
   }
 };
 
-template <typename T, int kVec, int kNV, bool kWarpTeam, bool kBias>
+// kStored: a 16-bit stream is written, its pre norm is a layer norm and its statistics are kept.
+template <typename T, int kVec, int kNV, bool kWarpTeam, bool kBias, bool kStored>
 __global__ void __launch_bounds__(kWarpTeam ? 128 : 512, kWarpTeam ? 4 : 1) bsa_block_norm_kernel(const __grid_constant__ NormParams p,
                                                                                int team_threads) {
   constexpr int kE = kVec * kNV, kP = kE / 2;
   extern __shared__ __align__(16) uint8_t smem[];  // the reduction areas, then the ring
   const int teams = blockDim.x / team_threads, team = threadIdx.x / team_threads, t = threadIdx.x % team_threads;
   TeamSum<1, kWarpTeam> sum{reinterpret_cast<float*>(smem) + team * 64, team_threads, 1 + team};
+  TeamSum<3, kWarpTeam> sum3{reinterpret_cast<float*>(smem) + teams * 64 + team * 192, team_threads, 1 + team};
   const Cols<kVec, kNV, kWarpTeam> cols(p.C, team_threads, t);
   const int step = gridDim.x * teams, rows = static_cast<int>(p.rows);  // rows and steps fit 31 bits
   int row = blockIdx.x * teams + team;
   Ring<T, kVec, kNV, 2, kWarpTeam, kWarpTeam ? kWarpBlock : 0> ring;
-  ring.init(ptx::smem_addr(smem) + teams * 256, cols, row, step, p.depth, {p.x, p.y});
+  ring.init(ptx::smem_addr(smem) + teams * sum_bytes(kStored), cols, row, step, p.depth, {p.x, p.y});
   int64_t ahead = row;  // the next row to fetch
   for (int d = 0; d + 1 < p.depth; ++d, ahead += step) ring.fetch(cols, ahead < rows);
   T* out = static_cast<T*>(p.out) + static_cast<int64_t>(row) * p.C + cols.at(0);
@@ -451,8 +494,16 @@ __global__ void __launch_bounds__(kWarpTeam ? 128 : 512, kWarpTeam ? 4 : 1) bsa_
       cols.store(out, st);
     }
     if (p.pre != BSA_NORM_NONE) {
-      pre = statistics<kVec, kNV, kWarpTeam>(st, p.pre, cols, p, sum);
-      const uint64_t r2 = twice(pre.y);
+      float r;
+      if constexpr (kStored) {
+        const float4 both = statistics_stored<T, kVec, kNV, kWarpTeam>(st, cols, p, sum, sum3);
+        pre = make_float2(both.x, both.y);
+        r = both.w;
+      } else {
+        pre = statistics<kVec, kNV, kWarpTeam>(st, p.pre, cols, p, sum);
+        r = pre.y;
+      }
+      const uint64_t r2 = twice(r);
 #pragma unroll
       for (int e = 0; e < kP; ++e) st.v[e] = ptx::fmul2(ptx::fmul2(st.v[e], r2), wpre.v[e]);
       if (kBias && p.pre_b != nullptr) {
@@ -772,6 +823,7 @@ struct Team {
 constexpr size_t kSmemMost = 220 * 1024;
 constexpr int kSmemBlock = 227 * 1024;  // what a block can have, and no layout of team_of is above
 
+// means: the backward's kMeans, or the forward's kStored.
 Team team_of(int C, size_t esize, bool aligned, bool backward, bool means) {
   Team t{};
   t.vec = aligned && C % 8 == 0 ? 8 : aligned && C % 2 == 0 ? 2 : 1;
@@ -794,7 +846,7 @@ Team team_of(int C, size_t esize, bool aligned, bool backward, bool means) {
     // about 128 registers a thread
     t.teams = t.warp ? kWarpBlock / 32 : std::max(1, 256 / t.threads);
     t.per_sm = std::max(1, 512 / (t.threads * t.teams));
-    const size_t fixed = t.teams * 256;
+    const size_t fixed = t.teams * sum_bytes(means);
     t.depth = 3;
     while (t.depth > 1 && (fixed + t.depth * slot() + 1024) * t.per_sm > kSmemMost) --t.depth;
     while (t.per_sm > 1 && (fixed + t.depth * slot() + 1024) * t.per_sm > kSmemMost) --t.per_sm;
@@ -869,28 +921,30 @@ bool start(F* kernel, const NormParams& p, const Team& t, int64_t blocks, cudaSt
   return cudaPeekAtLastError() == cudaSuccess;
 }
 
-template <typename T, bool kBias>
+template <typename T, bool kBias, bool kStored>
 bool launch_norm(const NormParams& p, const Team& t, int64_t blocks, cudaStream_t s) {
   if (t.warp) {
-    if (t.nv == 1) return start(bsa_block_norm_kernel<T, 8, 1, true, kBias>, p, t, blocks, s);
-    if (t.nv == 2) return start(bsa_block_norm_kernel<T, 8, 2, true, kBias>, p, t, blocks, s);
-    return start(bsa_block_norm_kernel<T, 8, 3, true, kBias>, p, t, blocks, s);
+    if (t.nv == 1) return start(bsa_block_norm_kernel<T, 8, 1, true, kBias, kStored>, p, t, blocks, s);
+    if (t.nv == 2) return start(bsa_block_norm_kernel<T, 8, 2, true, kBias, kStored>, p, t, blocks, s);
+    return start(bsa_block_norm_kernel<T, 8, 3, true, kBias, kStored>, p, t, blocks, s);
   }
   if (t.vec == 8)
-    return t.nv == 1 ? start(bsa_block_norm_kernel<T, 8, 1, false, kBias>, p, t, blocks, s)
-                     : start(bsa_block_norm_kernel<T, 8, 2, false, kBias>, p, t, blocks, s);
+    return t.nv == 1 ? start(bsa_block_norm_kernel<T, 8, 1, false, kBias, kStored>, p, t, blocks, s)
+                     : start(bsa_block_norm_kernel<T, 8, 2, false, kBias, kStored>, p, t, blocks, s);
   if (t.vec == 2)
-    return t.nv == 6 ? start(bsa_block_norm_kernel<T, 2, 6, false, kBias>, p, t, blocks, s)
-                     : start(bsa_block_norm_kernel<T, 2, 8, false, kBias>, p, t, blocks, s);
-  return t.nv == 12 ? start(bsa_block_norm_kernel<T, 1, 12, false, kBias>, p, t, blocks, s)
-                   : start(bsa_block_norm_kernel<T, 1, 16, false, kBias>, p, t, blocks, s);
+    return t.nv == 6 ? start(bsa_block_norm_kernel<T, 2, 6, false, kBias, kStored>, p, t, blocks, s)
+                     : start(bsa_block_norm_kernel<T, 2, 8, false, kBias, kStored>, p, t, blocks, s);
+  return t.nv == 12 ? start(bsa_block_norm_kernel<T, 1, 12, false, kBias, kStored>, p, t, blocks, s)
+                   : start(bsa_block_norm_kernel<T, 1, 16, false, kBias, kStored>, p, t, blocks, s);
 }
 template <typename T>
-bool launch_norm(NormParams p, const Team& t, int sms, cudaStream_t s) {
+bool launch_norm(NormParams p, const Team& t, bool stored, int sms, cudaStream_t s) {
   p.depth = t.depth;
   const int64_t blocks = std::min<int64_t>((p.rows + t.teams - 1) / t.teams, static_cast<int64_t>(sms) * t.per_sm);
-  return p.post_b != nullptr || p.pre_b != nullptr ? launch_norm<T, true>(p, t, blocks, s)
-                                                   : launch_norm<T, false>(p, t, blocks, s);
+  const bool bias = p.post_b != nullptr || p.pre_b != nullptr;
+  if constexpr (sizeof(T) == 2)
+    if (stored) return bias ? launch_norm<T, true, true>(p, t, blocks, s) : launch_norm<T, false, true>(p, t, blocks, s);
+  return bias ? launch_norm<T, true, false>(p, t, blocks, s) : launch_norm<T, false, false>(p, t, blocks, s);
 }
 
 struct BackPlan {
@@ -963,11 +1017,13 @@ int bsa_block_norm(const bsa_block_norm_args* args, const void* x, const void* y
   const bool aligned = all_aligned({x, y, stream_out, normed, a.post_weight, a.post_bias, a.gate, a.pre_weight,
                                     a.pre_bias});
   p.x = x, p.y = y, p.out = stream_out, p.normed = normed, p.stats = stats;
-  const Team t = team_of(a.C, type_bytes(a.type), aligned, false, takes_means(a));
+  // an fp32 stream is stored as it is, and without y there is nothing to round
+  const bool stored = y != nullptr && stats != nullptr && a.pre == BSA_NORM_LAYER && a.type != BSA_FP32;
+  const Team t = team_of(a.C, type_bytes(a.type), aligned, false, stored);
   cudaStream_t s = static_cast<cudaStream_t>(stream);
-  const bool ok = a.type == BSA_BF16   ? launch_norm<__nv_bfloat16>(p, t, sms, s)
-                  : a.type == BSA_FP16 ? launch_norm<__half>(p, t, sms, s)
-                                       : launch_norm<float>(p, t, sms, s);
+  const bool ok = a.type == BSA_BF16   ? launch_norm<__nv_bfloat16>(p, t, stored, sms, s)
+                  : a.type == BSA_FP16 ? launch_norm<__half>(p, t, stored, sms, s)
+                                       : launch_norm<float>(p, t, stored, sms, s);
   return cudaGetLastError() == cudaSuccess && ok ? BSA_OK : BSA_ERR_CUDA;
 }
 

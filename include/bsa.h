@@ -490,7 +490,8 @@ typedef struct {
  * not each other.
  * stats: device fp32 [rows, 4] or NULL: mean and 1/sqrt(..) of the post norm, then of the
  * pre norm (0 where there is none), for the backward.  The second norm is taken of the
- * stream before its rounding to `type`.  Enqueues one kernel.
+ * stream before its rounding to `type`; a layer norm's statistics are those of the stream as it is
+ * stored, which is what the backward reads.  Enqueues one kernel.
  */
 int bsa_block_norm(const bsa_block_norm_args* args, const void* x, const void* y, void* stream_out, void* normed,
                    float* stats, void* stream);

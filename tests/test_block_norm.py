@@ -369,3 +369,40 @@ def test_the_norm_alone_has_no_scales():
                                                dx.data_ptr(), None, None, None, None, None, None, None, 0,
                                                stream) == bsa.BSA_OK
         assert torch.equal(dx, want["x"]) and torch.equal(got, n)
+
+
+@gpu
+@needs_cuda
+@pytest.mark.parametrize("ty", [torch.bfloat16, torch.float16, torch.float32])
+@pytest.mark.parametrize("C", [1, 4, 64, 512, 1024, 8192])
+@pytest.mark.parametrize("offset", [0, 1])  # rows with and without 16-byte starts
+def test_layer_norm_gradient_is_that_of_the_stored_stream(C, ty, offset):
+    # Rows close to constant, whose rounding to 16 bits moves them by more than, or a good part of,
+    # their deviation: x = 4 + k steps of the type, stream_scale 1 + a quarter step / 4, so that the
+    # stream is stored as x itself.  The gradient of a layer norm at x has neither a component
+    # along the ones nor one along x - mean x beyond eps's.  C is a power of two and k small, so
+    # that the sums behind mean and variance are exact in fp32 and the tolerance is that of a
+    # normalised value without the mean's term.
+    R, step = 6, {torch.bfloat16: 2.0 ** -5, torch.float16: 2.0 ** -8, torch.float32: 2.0 ** -8}[ty]
+    g = torch.Generator(device="cuda").manual_seed(C)
+    make = lambda: torch.empty(R * C + offset, dtype=ty, device="cuda")[offset:].view(R, C)  # noqa: E731
+    x, y, ds, dn = make(), make(), make(), make()
+    k = torch.randint(-4, 5, (R, C), generator=g, device="cuda")
+    k[:2] = 0  # constant rows
+    x.copy_(4 + step * k), y.zero_(), ds.copy_(torch.randn(R, C, generator=g, device="cuda"))
+    dn.copy_(torch.randn(R, C, generator=g, device="cuda") + 0.5)
+    beta = 1 + step / 16 if ty != torch.float32 else 1.0
+    w = torch.rand(C, generator=g, device="cuda") + 0.5
+    b = torch.rand(C, generator=g, device="cuda")
+    a = dict(post=None, pre="layer", pre_weight=w, pre_bias=b, stream_scale=beta)
+    stream, _, st = bsa.bsa_block_norm(x, y, eps=EPS, save_stats=True, **a)
+    assert torch.equal(stream, x)
+    got = bsa.bsa_block_norm_backward(ds, dn, stream, y, st, **a)
+    X, W = _np(x), w.double().cpu().numpy()
+    m, r = ON.stats(X, "layer", EPS)
+    ref, mags = ON.backward(_np(ds), _np(dn), X, _np(y), np.concatenate([0 * m, 0 * r, m, r], 1), None, None, None, None,
+                            1.0, beta, "layer", W, b.double().cpu().numpy())
+    n, t = np.abs(X - m) * r, np.abs(_np(dn)) * W
+    dmag = np.abs(_np(ds)) + r * (t + t.mean(1, keepdims=True) + n * (t * n).mean(1, keepdims=True))
+    _near(got["x"], ref["x"], 2.0 ** -17 * dmag * beta, U[ty], "dx")
+    _near(got["pre_weight"], ref["pre_weight"], (70 * 2.0 ** -24 + 2.0 ** -17) * mags["pre_weight"], U[torch.float32], "weight")
