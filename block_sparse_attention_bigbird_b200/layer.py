@@ -134,6 +134,9 @@ class BigBirdSelfAttention(torch.nn.Module):
             self._layouts[key] = lay
         return lay
 
+    def __getstate__(self):  # copied and stored without the layouts, which are built again on first use
+        return {**self.__dict__, "_layouts": {}}
+
     def _turn(self, q, k, positions):
         if positions is None:
             positions = torch.arange(q.shape[2], device=q.device).expand(self.rope.n_axes, -1)

@@ -9,6 +9,7 @@ noise: a wrong path is off by the gradient's own size, the bound is a fraction o
 """
 
 import copy
+import pickle
 
 import numpy as np
 import pytest
@@ -79,6 +80,15 @@ def test_a_block_with_rotary_positions_is_copied():
     again = copy.deepcopy(m)
     assert again.attention.rope is not m.attention.rope and again.attention.rope.n_pairs == 32
     assert all((s == t).all() for s, t in zip(m.state_dict().values(), again.state_dict().values()))
+
+
+def test_a_block_that_has_run_is_copied_and_stored():
+    m = LY.BigBirdBlock(128, 2, rope=(8, 12, 12))
+    m.attention._layouts[(64, "cuda:0")] = bsa.bsa_layout_build(2, 64)  # what a call leaves behind
+    for again in (copy.deepcopy(m), pickle.loads(pickle.dumps(m))):
+        assert not again.attention._layouts and len(m.attention._layouts) == 1  # built again on first use
+        assert all((s == t).all() for s, t in zip(m.state_dict().values(), again.state_dict().values()))
+        assert again.attention.rope.n_pairs == 32
 
 
 def test_rotary_in_the_layer_over_fakes(monkeypatch):
