@@ -127,6 +127,7 @@ _SIGNATURES = {
     "bsa_sync_status": (ctypes.c_int, [ctypes.c_void_p]),
     "bsa_strerror": (ctypes.c_char_p, [ctypes.c_int]),
     "bsa_debug_wait_timeout": (ctypes.c_int, [ctypes.c_uint64, ctypes.c_void_p]),
+    "bsa_debug_product_wait_timeout": (ctypes.c_int, [ctypes.c_uint64, ctypes.c_void_p]),
 }
 
 
@@ -951,6 +952,11 @@ def bsa_sync_status(stream=None) -> int:
 def bsa_debug_wait_timeout(timeout_ns: int, stream=None) -> None:
     _check(lib.bsa_debug_wait_timeout(ctypes.c_uint64(timeout_ns), ctypes.c_void_p(_stream_ptr(stream))),
            "bsa_debug_wait_timeout")
+
+
+def bsa_debug_product_wait_timeout(timeout_ns: int, stream=None) -> None:
+    _check(lib.bsa_debug_product_wait_timeout(ctypes.c_uint64(timeout_ns), ctypes.c_void_p(_stream_ptr(stream))),
+           "bsa_debug_product_wait_timeout")
 
 
 def header_symbols() -> list[str]:

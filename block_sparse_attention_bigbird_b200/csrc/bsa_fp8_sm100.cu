@@ -677,6 +677,20 @@ __global__ void __launch_bounds__(kMThreads, 1) bsa_fp8_mma_kernel(const __grid_
   if (warp == 1) ptx::tmem_dealloc(tmem, kTmem);
 }
 
+// A barrier that nothing arrives at: exercises the product's bounded wait and its status word.
+__global__ void bsa_fp8_debug_wait_kernel(unsigned long long timeout_ns) {
+  __shared__ __align__(8) uint64_t bar;
+  __shared__ int abort_flag;
+  if (threadIdx.x == 0) {
+    ptx::mbar_init(ptx::smem_addr(&bar), 1);
+    abort_flag = 0;
+    ptx::fence_barrier_init();
+  }
+  __syncthreads();
+  ready(ptx::smem_addr(&bar), 0, &abort_flag, timeout_ns);
+  __syncthreads();
+}
+
 // Sums the splits' partial results in order, adds the bias and rounds once; kVec elements a
 // thread (4 where rows of the result are multiples of 4).  Launched as the product's
 // programmatic dependent.  The product triggers nothing early, so that its blocks come when the
@@ -1191,6 +1205,14 @@ int bsa_fp8_matmul(const void* a, int a_type, int64_t lda, const float* a_scale,
                                    out_f32)) != cudaSuccess)
       return BSA_ERR_CUDA;
   }
+  return cudaGetLastError() == cudaSuccess ? BSA_OK : BSA_ERR_CUDA;
+}
+
+int bsa_debug_product_wait_timeout(uint64_t timeout_ns, void* stream) {
+  const int sms = fp8_device_sms();
+  if (sms < 0) return sms;
+  const unsigned long long t = std::min<unsigned long long>(std::max<unsigned long long>(timeout_ns, 1000ull), kDefaultTimeoutNs);
+  bsa_fp8_debug_wait_kernel<<<1, 32, 0, static_cast<cudaStream_t>(stream)>>>(t);
   return cudaGetLastError() == cudaSuccess ? BSA_OK : BSA_ERR_CUDA;
 }
 

@@ -585,6 +585,9 @@ const char* bsa_strerror(int status);
  */
 int bsa_debug_wait_timeout(uint64_t timeout_ns, void* stream);
 
+/* bsa_debug_product_wait_timeout -- the same with the 8-bit product's wait and status word. */
+int bsa_debug_product_wait_timeout(uint64_t timeout_ns, void* stream);
+
 #ifdef __cplusplus
 }
 #endif

@@ -249,6 +249,22 @@ def test_product_out_workspace_streams_and_graphs():
 
 @gpu
 @needs_cuda
+def test_a_product_that_gives_up_is_reported():
+    ops = _operands(64, 64, 256, E4, E4, 1, 128, 8)[:4]
+    want = bsa.bsa_fp8_matmul(*ops)
+    assert bsa.bsa_sync_status() == 0
+    bsa.bsa_debug_product_wait_timeout(2_000_000)  # 2 ms at a barrier that nothing completes
+    assert bsa.bsa_sync_status() == bsa.BSA_ERR_DEVICE_TIMEOUT
+    assert bsa.bsa_sync_status() == 0  # the status is cleared
+    bsa.bsa_debug_wait_timeout(2_000_000)
+    bsa.bsa_debug_product_wait_timeout(2_000_000)
+    assert bsa.bsa_sync_status() == bsa.BSA_ERR_DEVICE_TIMEOUT
+    assert bsa.bsa_sync_status() == 0  # both are
+    assert torch.equal(bsa.bsa_fp8_matmul(*ops), want)
+
+
+@gpu
+@needs_cuda
 def test_product_empty_and_refused():
     a, sa, b, sb, _ = _operands(20, 40, 100, E4, E5, 1, 1, 7)
     z = bsa.bsa_fp8_matmul(a[:0], sa[:0], b, sb)
