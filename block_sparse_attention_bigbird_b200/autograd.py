@@ -83,10 +83,11 @@ def rotary(q: torch.Tensor, k: Optional[torch.Tensor], positions: torch.Tensor, 
 class _BlockNorm(torch.autograd.Function):
     @staticmethod
     def forward(ctx, x, y, post_weight, post_bias, gate, pre_weight, pre_bias, post, pre, branch_scale, stream_scale,
-                eps):
+                eps, grads):
         stream, normed, stats = bsa.bsa_block_norm(
             x, y, post=post, post_weight=post_weight, post_bias=post_bias, gate=gate, branch_scale=branch_scale,
-            stream_scale=stream_scale, pre=pre, pre_weight=pre_weight, pre_bias=pre_bias, eps=eps, save_stats=True)
+            stream_scale=stream_scale, pre=pre, pre_weight=pre_weight, pre_bias=pre_bias, eps=eps,
+            save_stats=grads and any(ctx.needs_input_grad))
         ctx.save_for_backward(stream, y, stats, post_weight, post_bias, gate, pre_weight, pre_bias)
         ctx.kinds = (post, pre, branch_scale, stream_scale)
         ctx.set_materialize_grads(False)
@@ -101,14 +102,14 @@ class _BlockNorm(torch.autograd.Function):
         post, pre, branch_scale, stream_scale = ctx.kinds
         dstream, dnormed = (None, grads[0]) if y is None else grads if pre is not None else (grads[0], None)
         if dstream is None and dnormed is None:
-            return (None,) * 12
+            return (None,) * 13
         g = bsa.bsa_block_norm_backward(
             None if dstream is None else dstream.contiguous(), None if dnormed is None else dnormed.contiguous(),
             stream, y, stats, post=post, post_weight=post_weight, post_bias=post_bias, gate=gate,
             branch_scale=branch_scale, stream_scale=stream_scale, pre=pre, pre_weight=pre_weight, pre_bias=pre_bias,
             params=any(ctx.needs_input_grad[2:7]))
         return (g["x"], g["y"], g["post_weight"], g["post_bias"], g["gate"], g["pre_weight"], g["pre_bias"],
-                None, None, None, None, None)
+                None, None, None, None, None, None)
 
 
 def block_norm(x: torch.Tensor, y: Optional[torch.Tensor] = None, post: Optional[str] = None, post_weight=None,
@@ -118,8 +119,9 @@ def block_norm(x: torch.Tensor, y: Optional[torch.Tensor] = None, post: Optional
     bsa.bsa_block_norm), differentiable in x, y, the gate and the parameters.  Without y the
     stream is x; with pre None normed is None.
     """
+    # inside a Function gradients are always off, so whether any are wanted is asked here
     got = _BlockNorm.apply(x, y, post_weight, post_bias, gate, pre_weight, pre_bias, post, pre, branch_scale,
-                           stream_scale, eps)
+                           stream_scale, eps, torch.is_grad_enabled())
     if y is None:
         return x, got
     return got if pre is not None else (got, None)

@@ -406,3 +406,25 @@ def test_layer_norm_gradient_is_that_of_the_stored_stream(C, ty, offset):
     dmag = np.abs(_np(ds)) + r * (t + t.mean(1, keepdims=True) + n * (t * n).mean(1, keepdims=True))
     _near(got["x"], ref["x"], 2.0 ** -17 * dmag * beta, U[ty], "dx")
     _near(got["pre_weight"], ref["pre_weight"], (70 * 2.0 ** -24 + 2.0 ** -17) * mags["pre_weight"], U[torch.float32], "weight")
+
+
+@gpu
+@needs_cuda
+def test_statistics_are_kept_only_for_a_gradient(monkeypatch):
+    from block_sparse_attention_bigbird_b200 import autograd
+    asked, forward = [], bsa.bsa_block_norm
+    monkeypatch.setattr(bsa, "bsa_block_norm", lambda *p, save_stats, **k: (asked.append(save_stats), forward(*p, save_stats=save_stats, **k))[1])
+    a, x, y, _, _ = _make(2, 9, 128, "rms", "layer", 1, True, torch.bfloat16, torch.float32, 5)
+    want = forward(x, y, **a)
+    leaf = x.clone().requires_grad_()
+    weight = a["post_weight"].clone().requires_grad_()
+    with torch.no_grad():
+        got = [autograd.block_norm(leaf, y, eps=1e-6, **a)]
+    with torch.inference_mode():
+        got.append(autograd.block_norm(leaf, y, eps=1e-6, **a))
+    got.append(autograd.block_norm(x, y, eps=1e-6, **a))
+    assert asked == [False] * 3
+    got.append(autograd.block_norm(leaf, y, eps=1e-6, **a))
+    got.append(autograd.block_norm(x, y, eps=1e-6, **{**a, "post_weight": weight}))
+    assert asked[3:] == [True] * 2 and got[3][0].requires_grad and got[4][1].requires_grad
+    assert all(torch.equal(g[0], want[0]) and torch.equal(g[1], want[1]) for g in got)
