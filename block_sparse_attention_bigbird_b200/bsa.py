@@ -309,13 +309,17 @@ def bsa_forward_workspace_bytes(layout: Layout, B: int, d: int) -> int:
     return n.value
 
 
-def _workspace(layout: Layout, B: int, device, d: int = 64):
+def _workspace(layout: Layout, key, size, device, stream):
+    """A workspace of size() bytes for calls of one kind (``key``) on ``stream``: kept for later calls
+    on that stream, which run one after the other; a captured call gets its own, which its
+    graph holds, as graphs may run at once."""
     import torch
-    key = (str(device), B, d)
+    if torch.cuda.is_current_stream_capturing():
+        return torch.empty(size(), dtype=torch.uint8, device=device)
+    key = (*key, str(device), _stream_ptr(stream))
     ws = layout._workspaces.get(key)
     if ws is None:
-        ws = torch.empty(bsa_forward_workspace_bytes(layout, B, d), dtype=torch.uint8, device=device)
-        layout._workspaces[key] = ws
+        layout._workspaces[key] = ws = torch.empty(size(), dtype=torch.uint8, device=device)
     return ws
 
 
@@ -326,8 +330,8 @@ def bsa_forward(q, k, v, layout: Layout, key_mask=None, scale: Optional[float] =
     q, k, v: contiguous bf16 CUDA tensors [B, H, L, d], d = 64 or 128.  key_mask: optional
     uint8 CUDA tensor [B, L] (1 = keep).  workspace: optional uint8 CUDA tensor
     of at least bsa_workspace_bytes(layout, B) bytes, any contents; when
-    omitted a cached one of the layout is used (not safe for concurrent calls
-    on different streams with the same layout).
+    omitted one that the layout keeps for the stream is used (a captured call
+    has its own, held by its graph).
     """
     import torch
     for name, t in (("q", q), ("k", k), ("v", v)):
@@ -344,7 +348,8 @@ def bsa_forward(q, k, v, layout: Layout, key_mask=None, scale: Optional[float] =
         if key_mask.dtype != torch.uint8 or tuple(key_mask.shape) != (B, L) or not key_mask.is_contiguous():
             raise ValueError("key_mask must be a contiguous uint8 tensor [B, L]")
     if workspace is None:
-        workspace = _workspace(layout, B, q.device, d)
+        workspace = _workspace(layout, ("fwd", B, d), lambda: bsa_forward_workspace_bytes(layout, B, d), q.device,
+                               stream)
     code = lib.bsa_forward(q.data_ptr(), k.data_ptr(), v.data_ptr(), B, H, L, d, layout.handle,
                            key_mask.data_ptr() if key_mask is not None else None,
                            ctypes.c_float(scale if scale is not None else 0.0), out.data_ptr(),
@@ -392,7 +397,8 @@ def bsa_backward(q, k, v, out, dout, lse, layout: Layout, key_mask=None, scale: 
     (fp32 [B, H, L]) are the forward's results for the same inputs, layout,
     key_mask and scale.  workspace: optional uint8 CUDA tensor of at least
     bsa_backward_workspace_bytes(layout, B) bytes (no clearing needed); when
-    omitted a cached one of the layout is used.
+    omitted one that the layout keeps for the stream is used (a captured call
+    has its own, held by its graph).
     """
     import torch
     for name, t in (("q", q), ("k", k), ("v", v), ("out", out), ("dout", dout)):
@@ -410,11 +416,7 @@ def bsa_backward(q, k, v, out, dout, lse, layout: Layout, key_mask=None, scale: 
     dk = torch.empty_like(k) if dk is None else dk
     dv = torch.empty_like(v) if dv is None else dv
     if workspace is None:
-        key = ("bwd", str(q.device), B)
-        workspace = layout._workspaces.get(key)
-        if workspace is None:
-            workspace = torch.empty(bsa_backward_workspace_bytes(layout, B), dtype=torch.uint8, device=q.device)
-            layout._workspaces[key] = workspace
+        workspace = _workspace(layout, ("bwd", B), lambda: bsa_backward_workspace_bytes(layout, B), q.device, stream)
     code = lib.bsa_backward(q.data_ptr(), k.data_ptr(), v.data_ptr(), out.data_ptr(), dout.data_ptr(),
                             lse.data_ptr(), B, H, L, d, layout.handle,
                             key_mask.data_ptr() if key_mask is not None else None,
