@@ -323,6 +323,45 @@ def _workspace(layout: Layout, key, size, device, stream):
     return ws
 
 
+def _fits(name, t, shape, dtype, dev):
+    """Refuses a tensor that is not a contiguous [shape] of this type on device dev."""
+    if t.dtype is not dtype or t.shape != shape or t.get_device() != dev or not t.is_contiguous():
+        raise ValueError(f"{name} must be a contiguous {str(dtype)[6:]} tensor {list(shape)} on the inputs' device")
+
+
+def _attention_inputs(q, k, v, key_mask, out, lse, workspace):
+    """Refuses what bsa_forward does not take; (B, H, L, d, device index)."""
+    import torch
+    for name, t in (("q", q), ("k", k), ("v", v)):
+        if t.dtype != torch.bfloat16 or not t.is_cuda or not t.is_contiguous() or t.dim() != 4:
+            raise ValueError(f"{name} must be a contiguous bf16 CUDA tensor [B, H, L, d]")
+    shape, dev = q.shape, q.get_device()
+    if shape != k.shape or shape != v.shape:
+        raise ValueError("q, k, v shapes differ")
+    if k.get_device() != dev or v.get_device() != dev:
+        raise ValueError("q, k, v are on different devices")
+    _attention_more(shape, dev, key_mask, workspace)
+    if out is not None:
+        _fits("out", out, shape, torch.bfloat16, dev)
+    if lse is not None:
+        _fits("lse", lse, shape[:3], torch.float32, dev)
+    return *shape, dev
+
+
+def _attention_more(shape, dev, key_mask, workspace):
+    import torch
+    if key_mask is not None:
+        _fits("key_mask", key_mask, (shape[0], shape[2]), torch.uint8, dev)
+    if workspace is not None and (workspace.get_device() != dev or not workspace.is_contiguous()):
+        raise ValueError("workspace must be contiguous and on the inputs' device")
+
+
+def _attention_outputs(q, out, lse):
+    import torch
+    return (torch.empty_like(q) if out is None else out,
+            q.new_empty(q.shape[:3], dtype=torch.float32) if lse is None else lse)
+
+
 def bsa_forward(q, k, v, layout: Layout, key_mask=None, scale: Optional[float] = None, out=None,
                 lse=None, workspace=None, stream=None):
     """O (bf16 [B,H,L,d]) and lse (fp32 [B,H,L]) of the block-sparse attention.
@@ -333,30 +372,19 @@ def bsa_forward(q, k, v, layout: Layout, key_mask=None, scale: Optional[float] =
     omitted one that the layout keeps for the stream is used (a captured call
     has its own, held by its graph).
     """
-    import torch
-    for name, t in (("q", q), ("k", k), ("v", v)):
-        if t.dtype != torch.bfloat16 or not t.is_cuda or not t.is_contiguous() or t.dim() != 4:
-            raise ValueError(f"{name} must be a contiguous bf16 CUDA tensor [B, H, L, d]")
-    if q.shape != k.shape or q.shape != v.shape:
-        raise ValueError("q, k, v shapes differ")
-    B, H, L, d = q.shape
-    if out is None:
-        out = torch.empty_like(q)
-    if lse is None:
-        lse = torch.empty((B, H, L), dtype=torch.float32, device=q.device)
-    if key_mask is not None:
-        if key_mask.dtype != torch.uint8 or tuple(key_mask.shape) != (B, L) or not key_mask.is_contiguous():
-            raise ValueError("key_mask must be a contiguous uint8 tensor [B, L]")
-    if workspace is None:
-        workspace = _workspace(layout, ("fwd", B, d), lambda: bsa_forward_workspace_bytes(layout, B, d), q.device,
-                               stream)
-    code = lib.bsa_forward(q.data_ptr(), k.data_ptr(), v.data_ptr(), B, H, L, d, layout.handle,
-                           key_mask.data_ptr() if key_mask is not None else None,
-                           ctypes.c_float(scale if scale is not None else 0.0), out.data_ptr(),
-                           lse.data_ptr(), workspace.data_ptr(), workspace.numel(),
-                           ctypes.c_void_p(_stream_ptr(stream)))
-    _check(code, "bsa_forward")
-    return out, lse
+    B, H, L, d, dev = _attention_inputs(q, k, v, key_mask, out, lse, workspace)
+
+    def call(ptr):
+        o, ls = _attention_outputs(q, out, lse)
+        ws = workspace
+        if ws is None:
+            ws = _workspace(layout, ("fwd", B, d), lambda: bsa_forward_workspace_bytes(layout, B, d), q.device, ptr)
+        code = lib.bsa_forward(q.data_ptr(), k.data_ptr(), v.data_ptr(), B, H, L, d, layout.handle, _ptr(key_mask),
+                               scale if scale is not None else 0.0, o.data_ptr(), ls.data_ptr(), ws.data_ptr(),
+                               ws.numel(), ptr)
+        _check(code, "bsa_forward")
+        return o, ls
+    return _on(dev, stream, call)
 
 
 def bsa_forward_static_ws(q, k, v, layout: Layout, key_mask=None, scale: Optional[float] = None,
@@ -369,18 +397,16 @@ def bsa_forward_static_ws(q, k, v, layout: Layout, key_mask=None, scale: Optiona
     buffer: serialise them.  Raises BsaError(BSA_ERR_STATIC_WORKSPACE) when the
     problem needs more scratch than the buffer holds.
     """
-    import torch
-    B, H, L, d = q.shape
-    if out is None:
-        out = torch.empty_like(q)
-    if lse is None:
-        lse = torch.empty((B, H, L), dtype=torch.float32, device=q.device)
-    code = lib.bsa_forward_static_ws(q.data_ptr(), k.data_ptr(), v.data_ptr(), B, H, L, d, layout.handle,
-                                     key_mask.data_ptr() if key_mask is not None else None,
-                                     ctypes.c_float(scale if scale is not None else 0.0), out.data_ptr(),
-                                     lse.data_ptr(), ctypes.c_void_p(_stream_ptr(stream)))
-    _check(code, "bsa_forward_static_ws")
-    return out, lse
+    B, H, L, d, dev = _attention_inputs(q, k, v, key_mask, out, lse, None)
+
+    def call(ptr):
+        o, ls = _attention_outputs(q, out, lse)
+        code = lib.bsa_forward_static_ws(q.data_ptr(), k.data_ptr(), v.data_ptr(), B, H, L, d, layout.handle,
+                                         _ptr(key_mask), scale if scale is not None else 0.0, o.data_ptr(),
+                                         ls.data_ptr(), ptr)
+        _check(code, "bsa_forward_static_ws")
+        return o, ls
+    return _on(dev, stream, call)
 
 
 def bsa_backward_workspace_bytes(layout: Layout, B: int) -> int:
@@ -406,25 +432,28 @@ def bsa_backward(q, k, v, out, dout, lse, layout: Layout, key_mask=None, scale: 
             raise ValueError(f"{name} must be a contiguous bf16 CUDA tensor [B, H, L, d]")
         if t.shape != q.shape:
             raise ValueError(f"{name} shape differs from q")
-    B, H, L, d = q.shape
-    if lse.dtype != torch.float32 or tuple(lse.shape) != (B, H, L) or not lse.is_contiguous():
-        raise ValueError("lse must be a contiguous fp32 tensor [B, H, L]")
-    if key_mask is not None:
-        if key_mask.dtype != torch.uint8 or tuple(key_mask.shape) != (B, L) or not key_mask.is_contiguous():
-            raise ValueError("key_mask must be a contiguous uint8 tensor [B, L]")
-    dq = torch.empty_like(q) if dq is None else dq
-    dk = torch.empty_like(k) if dk is None else dk
-    dv = torch.empty_like(v) if dv is None else dv
-    if workspace is None:
-        workspace = _workspace(layout, ("bwd", B), lambda: bsa_backward_workspace_bytes(layout, B), q.device, stream)
-    code = lib.bsa_backward(q.data_ptr(), k.data_ptr(), v.data_ptr(), out.data_ptr(), dout.data_ptr(),
-                            lse.data_ptr(), B, H, L, d, layout.handle,
-                            key_mask.data_ptr() if key_mask is not None else None,
-                            ctypes.c_float(scale if scale is not None else 0.0), dq.data_ptr(), dk.data_ptr(),
-                            dv.data_ptr(), workspace.data_ptr(), workspace.numel(),
-                            ctypes.c_void_p(_stream_ptr(stream)))
-    _check(code, "bsa_backward")
-    return dq, dk, dv
+    shape, dev = q.shape, q.get_device()
+    B, H, L, d = shape
+    if any(t.get_device() != dev for t in (k, v, out, dout)):
+        raise ValueError("q, k, v, out, dout are on different devices")
+    _fits("lse", lse, shape[:3], torch.float32, dev)
+    _attention_more(shape, dev, key_mask, workspace)
+    for name, t in (("dq", dq), ("dk", dk), ("dv", dv)):
+        if t is not None:
+            _fits(name, t, shape, torch.bfloat16, dev)
+
+    def call(ptr):
+        grads = [torch.empty_like(q) if t is None else t for t in (dq, dk, dv)]
+        ws = workspace
+        if ws is None:
+            ws = _workspace(layout, ("bwd", B), lambda: bsa_backward_workspace_bytes(layout, B), q.device, ptr)
+        code = lib.bsa_backward(q.data_ptr(), k.data_ptr(), v.data_ptr(), out.data_ptr(), dout.data_ptr(),
+                                lse.data_ptr(), B, H, L, d, layout.handle, _ptr(key_mask),
+                                scale if scale is not None else 0.0, *(t.data_ptr() for t in grads), ws.data_ptr(),
+                                ws.numel(), ptr)
+        _check(code, "bsa_backward")
+        return tuple(grads)
+    return _on(dev, stream, call)
 
 
 def _check_bf16(name, t, dim):
@@ -449,18 +478,21 @@ def bsa_qkv_projection(x, weight, bias=None, num_heads: Optional[int] = None, q=
     H = num_heads if num_heads is not None else C // 64
     if C != 64 * H or tuple(weight.shape) != (3 * C, C):
         raise ValueError("x must be [B, L, 64 H] and weight [3 C, C]")
+    dev = x.get_device()
+    _fits("weight", weight, (3 * C, C), torch.bfloat16, dev)
     if bias is not None:
-        _check_bf16("bias", bias, 1)
-        if bias.numel() != 3 * C:
-            raise ValueError("bias must have 3 C elements")
-    outs = []
-    for t in (q, k, v):
-        outs.append(torch.empty((B, H, L, 64), dtype=torch.bfloat16, device=x.device) if t is None else t)
-    code = lib.bsa_qkv_projection(x.data_ptr(), weight.data_ptr(), bias.data_ptr() if bias is not None else None,
-                                  B, L, H, outs[0].data_ptr(), outs[1].data_ptr(), outs[2].data_ptr(),
-                                  ctypes.c_void_p(_stream_ptr(stream)))
-    _check(code, "bsa_qkv_projection")
-    return tuple(outs)
+        _fits("bias", bias, (3 * C,), torch.bfloat16, dev)
+    for name, t in (("q", q), ("k", k), ("v", v)):
+        if t is not None:
+            _fits(name, t, (B, H, L, 64), torch.bfloat16, dev)
+
+    def call(ptr):
+        outs = tuple(x.new_empty((B, H, L, 64)) if t is None else t for t in (q, k, v))
+        code = lib.bsa_qkv_projection(x.data_ptr(), weight.data_ptr(), _ptr(bias), B, L, H,
+                                      *(t.data_ptr() for t in outs), ptr)
+        _check(code, "bsa_qkv_projection")
+        return outs
+    return _on(dev, stream, call)
 
 
 def bsa_out_projection(o, weight, bias=None, y=None, stream=None):
@@ -477,16 +509,19 @@ def bsa_out_projection(o, weight, bias=None, y=None, stream=None):
     N = weight.shape[0]
     if d != 64 or weight.shape[1] != 64 * H:
         raise ValueError("o must be [B, H, L, 64] and weight [N, 64 H]")
+    dev = o.get_device()
+    _fits("weight", weight, (N, 64 * H), torch.bfloat16, dev)
     if bias is not None:
-        _check_bf16("bias", bias, 1)
-        if bias.numel() != N:
-            raise ValueError("bias must have N elements")
-    if y is None:
-        y = torch.empty((B, L, N), dtype=torch.bfloat16, device=o.device)
-    code = lib.bsa_out_projection(o.data_ptr(), weight.data_ptr(), bias.data_ptr() if bias is not None else None,
-                                  B, H, L, N, y.data_ptr(), ctypes.c_void_p(_stream_ptr(stream)))
-    _check(code, "bsa_out_projection")
-    return y
+        _fits("bias", bias, (N,), torch.bfloat16, dev)
+    if y is not None:
+        _fits("y", y, (B, L, N), torch.bfloat16, dev)
+
+    def call(ptr):
+        out = o.new_empty((B, L, N)) if y is None else y
+        code = lib.bsa_out_projection(o.data_ptr(), weight.data_ptr(), _ptr(bias), B, H, L, N, out.data_ptr(), ptr)
+        _check(code, "bsa_out_projection")
+        return out
+    return _on(dev, stream, call)
 
 
 _type_codes = {}
@@ -520,10 +555,12 @@ def _on(index: int, stream, call):
     is given, the stream that call's allocations belong to.  An integer is taken to be a stream of
     that device."""
     import torch
-    if stream is None and index == torch.cuda.current_device():
-        return call(_raw_stream(index))
     if stream is not None and not isinstance(stream, int) and stream.device_index != index:
         raise ValueError("stream belongs to another device than the tensors")
+    if index == torch.cuda.current_device():
+        ptr = _raw_stream(index)
+        if stream is None or ptr == (stream if isinstance(stream, int) else stream.cuda_stream):
+            return call(ptr)
     with torch.cuda.device(index):
         if stream is None:
             return call(_raw_stream(index))
