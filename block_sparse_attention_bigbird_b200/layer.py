@@ -29,6 +29,7 @@ same pass.
 
 from __future__ import annotations
 
+import contextlib
 from typing import Optional
 
 import torch
@@ -130,7 +131,8 @@ class BigBirdSelfAttention(torch.nn.Module):
         if lay is None:
             lay = bsa.bsa_layout_build(self.num_heads, L, self.block, self.window, self.num_global,
                                        self.num_random, self.seed)
-            bsa.bsa_layout_upload(lay)
+            with torch.cuda.device(device.index) if device.type == "cuda" else contextlib.nullcontext():
+                bsa.bsa_layout_upload(lay)
             self._layouts[key] = lay
         return lay
 

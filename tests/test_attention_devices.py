@@ -114,3 +114,13 @@ def test_the_tensors_device_is_the_current_one(calls, name):
     assert calls == [(name, 1)]
     with pytest.raises(ValueError, match="another device"):
         call(**need, **may, stream=types.SimpleNamespace(device_index=0, cuda_stream=3))
+
+
+def test_a_layers_layout_is_uploaded_to_its_inputs_device(calls, monkeypatch):
+    from block_sparse_attention_bigbird_b200 import BigBirdSelfAttention
+    monkeypatch.setattr(bsa, "bsa_layout_build", lambda *_: types.SimpleNamespace())
+    monkeypatch.setattr(bsa, "bsa_layout_upload", lambda _: calls.append(("upload", torch.cuda.current_device())))
+    layer = BigBirdSelfAttention(128, 2)
+    for device in ("cuda:1", "cuda:0", "cuda:1"):
+        layer.layout(64, torch.device(device))
+    assert calls == [("upload", 1), ("upload", 0)]
