@@ -552,14 +552,17 @@ def _raw_stream(index: int) -> int:
 
 def _on(index: int, stream, call):
     """call(stream pointer) with the tensors' device ``index`` current, and ``stream``, where one
-    is given, the stream that call's allocations belong to.  An integer is taken to be a stream of
-    that device."""
+    is given, the stream that call's allocations belong to.  An integer, or the ``cuda_stream`` of an
+    object that is no torch stream, is taken to be a stream of that device."""
     import torch
-    if stream is not None and not isinstance(stream, int) and stream.device_index != index:
-        raise ValueError("stream belongs to another device than the tensors")
+    if stream is not None:
+        if getattr(stream, "device_index", index) != index:
+            raise ValueError("stream belongs to another device than the tensors")
+        if not isinstance(stream, (int, torch.cuda.Stream)):
+            stream = stream.cuda_stream
     if index == torch.cuda.current_device():
         ptr = _raw_stream(index)
-        if stream is None or ptr == (stream if isinstance(stream, int) else stream.cuda_stream):
+        if stream is None or (stream if isinstance(stream, int) else stream.cuda_stream) == ptr:
             return call(ptr)
     with torch.cuda.device(index):
         if stream is None:
@@ -669,7 +672,7 @@ def bsa_rope_apply(q, k, positions, rope: Rope, inverse: bool = False, q_out=Non
             raise ValueError("k must be like q, [B, Hk, L, d] with contiguous columns")
         Hk = k.shape[1]
     ps, n = positions.stride(), positions.shape
-    if max(B, H, Hk, L, d) > INT_MOST:
+    if (B | H | Hk | L | d) > INT_MOST:
         raise ValueError(_TOO_LARGE)
     if pt not in (INT32, INT64, FP32) or len(n) not in (2, 3) or n[0] < rope.n_axes or n[-1] != L or \
             (len(n) == 3 and n[1] != B) or positions.get_device() != dev:
@@ -922,7 +925,7 @@ def _scale_rows(name, scale, rows, kb, dev) -> int:
 
 
 def bsa_fp8_matmul_workspace_bytes(M: int, N: int, K: int) -> int:
-    if max(M, N, K) > INT_MOST:
+    if (M | N | K) > INT_MOST:
         raise ValueError(_TOO_LARGE)
     n = ctypes.c_size_t()
     _check(lib.bsa_fp8_matmul_workspace_bytes(M, N, K, ctypes.byref(n)), "bsa_fp8_matmul_workspace_bytes")
@@ -944,7 +947,7 @@ def bsa_fp8_matmul(a, a_scale, b, b_scale, bias=None, out_dtype=None, out=None, 
     (M, K), (N, Kb) = a.shape, b.shape
     if Kb != K:
         raise ValueError("a and b must have the same number of columns")
-    if max(M, N, K) > INT_MOST:
+    if (M | N | K) > INT_MOST:
         raise ValueError(_TOO_LARGE)
     kb = (K + 127) // 128
     ar, br = _scale_rows("a_scale", a_scale, M, kb, dev), _scale_rows("b_scale", b_scale, N, kb, dev)

@@ -46,3 +46,16 @@ def test_the_default_stream_by_its_pointer():
         got = call(x)
         torch.cuda.synchronize()
         assert torch.equal(got, w)
+
+
+@gpu
+@needs_cuda
+def test_streams_of_every_kind():
+    s, taken = torch.cuda.Stream(), lambda given: bsa._on(0, given, lambda ptr: (ptr, torch.cuda.current_stream().cuda_stream))  # noqa: E731
+    foreign = types.SimpleNamespace(cuda_stream=s.cuda_stream)  # another library's stream object
+    for given in (s, s.cuda_stream, foreign, torch.cuda.ExternalStream(s.cuda_stream)):
+        assert taken(given) == (s.cuda_stream, s.cuda_stream)
+    with torch.cuda.stream(s):
+        assert taken(None) == taken(s) == taken(s.cuda_stream) == (s.cuda_stream, s.cuda_stream)
+        assert taken(0) == taken(torch.cuda.default_stream()) == (0, 0)
+    assert taken(None) == taken(0) == (0, 0) and torch.cuda.current_stream().cuda_stream == 0
